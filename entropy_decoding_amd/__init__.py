@@ -136,7 +136,43 @@ class df11_device_encode(ctypes.Structure):
     ]
 
 
+class df11_adamw_tensor(ctypes.Structure):
+    _fields_ = [
+        ("w", ctypes.c_void_p),
+        ("master", ctypes.c_void_p),
+        ("g", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("counts", ctypes.c_void_p),
+        ("numel", ctypes.c_uint64),
+        ("lr_scale", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+    ]
+
+
+class df11_adamw_config(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("step", ctypes.c_uint64),
+        ("w_type", ctypes.c_uint32),
+        ("g_type", ctypes.c_uint32),
+        ("state_bits", ctypes.c_uint32),
+        ("reserved", ctypes.c_uint32),
+        ("d_lr", ctypes.c_void_p),
+        ("d_step", ctypes.c_void_p),
+        ("d_grad_factor", ctypes.c_void_p),
+    ]
+
+
 DF11_PIPELINE_MAX_SLOTS = 4
+DF11_ADAMW_BLOCK = 256
+# df11_type, by the names of torch's types
+TYPES = {"float32": 0, "bfloat16": 1, "float16": 2}
 # df11_format; the names are what the binding's ``fmt`` arguments accept
 FORMATS = {"bf16": 0, "fp8_e4m3": 1, "fp8_e5m2": 2}
 DF11_GEMV_MAX_TENSORS = 16
@@ -212,7 +248,16 @@ def _load():
                                      ctypes.c_uint64, ctypes.c_uint32, ctypes.c_uint32,
                                      ctypes.POINTER(df11_sizes), ctypes.POINTER(df11_device_encode),
                                      vp]
+    at = ctypes.POINTER(df11_adamw_tensor)
+    L.df11_adamw_step.argtypes = [ctypes.POINTER(df11_adamw_config), at, ctypes.c_uint32, vp]
+    L.df11_adamw_values.argtypes = [at, ctypes.c_uint32, ctypes.c_uint32, ctypes.POINTER(vp),
+                                    ctypes.POINTER(vp), vp]
+    L.df11_grad_norm_scratch_bytes.argtypes = [at, ctypes.c_uint32]
+    L.df11_grad_norm_scratch_bytes.restype = ctypes.c_uint64
+    L.df11_grad_norm.argtypes = [ctypes.c_uint32, at, ctypes.c_uint32, ctypes.c_double, vp, vp,
+                                 ctypes.c_uint64, vp]
     for f in (L.df11_build_codebook, L.df11_encode_size, L.df11_encode,
+              L.df11_adamw_step, L.df11_adamw_values, L.df11_grad_norm,
               L.df11_build_codebook_fmt, L.df11_encode_size_fmt, L.df11_encode_fmt,
               L.df11_decompress_block, L.df11_decompress_tensor, L.df11_pipeline_create,
               L.df11_pipeline_destroy, L.df11_pipeline_decompress, L.df11_pipeline_acquire,
@@ -756,6 +801,206 @@ def df11_decompress_gemv_noalloc(ds: DeviceStream, layout, x, y, status=None,
                                             ctypes.c_void_p(x.data_ptr()),
                                             ctypes.c_void_p(y.data_ptr()), sp,
                                             _stream_handle(stream)))
+
+
+# ---------------------------------------------------------------- optimiser step
+
+
+def _type(dtype) -> int:
+    name = str(dtype).replace("torch.", "")
+    if name not in TYPES:
+        raise TypeError(f"no operator for {dtype}")
+    return TYPES[name]
+
+
+def _same(tensors, what, dtype=None, sizes=None, device=None):
+    """Checks a list of contiguous device tensors of one type; returns them."""
+    tensors = list(tensors)
+    if sizes is not None and [t.numel() for t in tensors] != list(sizes):
+        raise ValueError(f"{what} must have {list(sizes)[:8]} elements, one tensor each")
+    for t in tensors:
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous device tensors")
+        if t.dtype != (tensors[0].dtype if dtype is None else dtype):
+            raise TypeError(f"{what} must be of one type" if dtype is None
+                            else f"{what} must be {dtype}")
+        if device is not None and t.device != device:
+            raise ValueError(f"{what} must be on {device}")
+    return tensors
+
+
+def _on(device, stream):
+    """(a guard that makes ``stream``, or the device's current stream, and the
+    device current; the stream's handle)."""
+    import torch
+
+    if stream is None:
+        return torch.cuda.device(device), ctypes.c_void_p(
+            torch.cuda.current_stream(device).cuda_stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    if stream.device != device:
+        raise ValueError(f"the stream is not on {device}")
+    return torch.cuda.stream(stream), ctypes.c_void_p(stream.cuda_stream)
+
+
+class AdamW:
+    """df11_adamw_step over a list of device tensors (BF16 or float32 weights,
+    e.g. a unit's, at any offset of a larger buffer), with what the step keeps.
+
+    ``grads``: one tensor per weight, all BF16 or all float32.  ``masters``:
+    float32 copies of BF16 weights that carry the update.  ``state_bits``: 32
+    (float32 states) or 8 (codes of blocks of DF11_ADAMW_BLOCK elements, a
+    quarter of the memory).  ``state``: lists "m" and "v" (and "m_scale",
+    "v_scale" for 8 bits) to go on from instead of zeros; they are updated in
+    place.  ``counts``: keep each tensor's exponent histogram of the new BF16
+    weights in ``self.counts`` (one row of 256 per tensor).
+    ``weight_decay`` and ``lr_scale``: one number, or one per tensor.  ``step``:
+    steps already made.  ``device_step``: keep the step's number on the device
+    too (``self.d_step``) and advance it there, so that a captured step counts
+    on when it is replayed.
+    """
+
+    def __init__(self, weights, grads, masters=None, state_bits: int = 32, state=None,
+                 counts: bool = False, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay=0.01, lr_scale=1.0, step: int = 0, device_step: bool = False):
+        import torch
+
+        self.weights = _same(weights, "weights")
+        if not self.weights:
+            raise ValueError("no weights")
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits must be 32 or 8")
+        self.device = dev = self.weights[0].device
+        _same(self.weights, "weights", device=dev)
+        sizes = [t.numel() for t in self.weights]
+        n = len(sizes)
+        blocks = [-(-s // DF11_ADAMW_BLOCK) for s in sizes]
+        self.masters = None if masters is None else _same(masters, "masters", torch.float32, sizes, dev)
+        self.state_bits = state_bits
+        kinds = ({"m": torch.float32, "v": torch.float32} if state_bits == 32 else
+                 {"m": torch.int8, "v": torch.uint8, "m_scale": torch.float32,
+                  "v_scale": torch.float32})
+        if state is None:
+            state = {k: [torch.zeros(c, dtype=d, device=dev)
+                         for c in (blocks if k.endswith("scale") else sizes)]
+                     for k, d in kinds.items()}
+        elif set(state) != set(kinds):
+            raise ValueError(f"state must hold {sorted(kinds)}")
+        self.state = {k: _same(state[k], k, d, blocks if k.endswith("scale") else sizes, dev)
+                      for k, d in kinds.items()}
+        self.counts = (torch.zeros((n, 256), dtype=torch.int64, device=dev) if counts else None)
+        self.lr, self.steps = float(lr), int(step)
+        self.d_step = (torch.full((1,), int(step), dtype=torch.int64, device=dev)
+                       if device_step else None)
+        each = lambda x: [float(v) for v in x] if np.ndim(x) else [float(x)] * n  # noqa: E731
+        decays, scales = each(weight_decay), each(lr_scale)
+        if len(decays) != n or len(scales) != n:
+            raise ValueError("one weight_decay and one lr_scale per tensor")
+        self._t = (df11_adamw_tensor * n)()
+        for k, a in enumerate(self._t):
+            a.w = self.weights[k].data_ptr()
+            a.master = self.masters[k].data_ptr() if self.masters else None
+            for name, parts in self.state.items():
+                setattr(a, name, parts[k].data_ptr())
+            a.counts = self.counts[k].data_ptr() if counts else None
+            a.numel, a.lr_scale, a.weight_decay = sizes[k], scales[k], decays[k]
+        self._c = df11_adamw_config(self.lr, betas[0], betas[1], eps, 0,
+                                    _type(self.weights[0].dtype), 0, state_bits, 0)
+        self._norm_bytes = int(LIB.df11_grad_norm_scratch_bytes(self._t, n))
+        self.set_grads(grads)
+
+    def set_grads(self, grads) -> None:
+        """The gradients that later steps read."""
+        self.grads = _same(grads, "grads", None, [t.numel() for t in self.weights], self.device)
+        for a, g in zip(self._t, self.grads):
+            a.g = g.data_ptr()
+        self._c.g_type = _type(self.grads[0].dtype)
+
+    def grad_norm(self, max_norm: float, stream=None):
+        """A float32 device tensor [norm, clip factor] of all gradients together."""
+        import torch
+
+        guard, st = _on(self.device, stream)
+        with guard:  # memory of the stream that uses it: its reuse is ordered there
+            out = torch.empty(2, dtype=torch.float32, device=self.device)
+            scratch = torch.empty(self._norm_bytes, dtype=torch.uint8, device=self.device)
+            _check("df11_grad_norm",
+                   LIB.df11_grad_norm(self._c.g_type, self._t, len(self._t), float(max_norm),
+                                      out.data_ptr(), scratch.data_ptr(), self._norm_bytes, st))
+        return out
+
+    def step(self, lr=None, max_norm=None, grad_factor=None, stream=None):
+        """One step.  ``lr``: this step's learning rate (a number, or a float32
+        device tensor that the kernel reads).  ``max_norm``: clip the
+        gradients' norm; returns grad_norm's tensor then.  ``grad_factor``: a
+        float32 device tensor of one element to multiply the gradients with;
+        a factor that is not finite leaves everything as it was."""
+        if max_norm is not None and grad_factor is not None:
+            raise ValueError("max_norm or grad_factor")
+        norm = None if max_norm is None else self.grad_norm(max_norm, stream)
+        if norm is not None:
+            grad_factor = norm[1:]
+        c = self._c
+        by_tensor = hasattr(lr, "data_ptr")
+        for x, what in ((grad_factor, "grad_factor"), (lr if by_tensor else None, "lr")):
+            if x is not None and (_type(x.dtype) != 0 or x.numel() != 1 or x.device != self.device):
+                raise ValueError(f"{what} must be one float32 on {self.device}")
+        c.lr = self.lr if lr is None or by_tensor else float(lr)
+        c.d_lr = lr.data_ptr() if by_tensor else None
+        c.d_grad_factor = None if grad_factor is None else grad_factor.data_ptr()
+        c.step = self.steps + 1
+        guard, st = _on(self.device, stream)
+        with guard:
+            if self.d_step is not None:
+                self.d_step += 1
+                c.d_step = self.d_step.data_ptr()
+            _check("df11_adamw_step",
+                   LIB.df11_adamw_step(ctypes.byref(c), self._t, len(self._t), st))
+        self.steps += 1
+        return norm
+
+    def state_values(self, m_out=None, v_out=None, stream=None):
+        """(m, v) as lists of float32 tensors, or written into the given lists
+        of float32 or BF16 tensors: what 8-bit states stand for."""
+        import torch
+
+        if self.state_bits == 32:
+            raise ValueError("32-bit states are their own values")
+        sizes = [t.numel() for t in self.weights]
+        if m_out is None and v_out is None:
+            m_out, v_out = ([torch.empty(s, device=self.device) for s in sizes] for _ in range(2))
+        lists = []
+        for out, what in ((m_out, "m_out"), (v_out, "v_out")):
+            kind = (m_out if m_out is not None else v_out)[0].dtype
+            if out is not None:
+                out = _same(out, what, kind, sizes, self.device)
+            lists.append(None if out is None
+                         else (ctypes.c_void_p * len(out))(*[t.data_ptr() for t in out]))
+        guard, st = _on(self.device, stream)
+        with guard:
+            _check("df11_adamw_values",
+                   LIB.df11_adamw_values(self._t, len(self._t), _type(kind), lists[0], lists[1], st))
+        return m_out, v_out
+
+    def compressed_sizes(self) -> df11_sizes:
+        """What the weights of the last step would take as one compressed unit
+        (payload bits, arrays), from ``counts``: whether, and into how much
+        memory, to encode them.  Waits for the step."""
+        if self.counts is None or not self.steps:
+            raise ValueError("counts are kept by steps of AdamW(counts=True)")
+        counts = self.counts.sum(0).cpu().numpy().view(np.uint64)
+        cb, sz = df11_build_codebook_from_counts(counts), df11_sizes()
+        _check("df11_encode_size_from_counts",
+               LIB.df11_encode_size_from_counts(_format("bf16"), ctypes.byref(cb),
+                                                counts.ctypes.data_as(_u64p), int(counts.sum()),
+                                                DEFAULT_TILE_WINDOWS, DEFAULT_WINDOW_BYTES,
+                                                ctypes.byref(sz)))
+        return sz
+
+    def compress(self, stream=None):
+        """The BF16 weights as one compressed unit: encode_on_device's (DeviceStream, codebook)."""
+        return encode_on_device(self.weights, stream=stream)
 
 
 def table_bytes(cb: df11_codebook) -> int:

@@ -546,6 +546,114 @@ int df11_decompress_gemm(const df11_device_stream *s, const df11_gemv_tensor *te
                          void *scratch, uint64_t scratch_bytes, int32_t *d_status,
                          df11_hip_stream st);
 
+/* Element types of the operators below. */
+typedef enum df11_type {
+    DF11_TYPE_F32 = 0,
+    DF11_TYPE_BF16 = 1,
+    DF11_TYPE_F16 = 2
+} df11_type;
+
+/*
+ * AdamW over many tensors -- device, for weights that are trained or
+ * fine-tuned on the GPU before they are encoded there (df11_encode_device).
+ * One step of every element, in float32, each operation rounded to nearest
+ * in this order (t is the step's number, from 1; f the gradient factor):
+ *   g = f g
+ *   m = b1 m + (1 - b1) g                 v = b2 v + ((1 - b2) g) g
+ *   u = m / (sqrt(v) * (1 / sqrt(1 - b2^t)) + eps)
+ *   w = w (1 - lr weight_decay) - u (lr / (1 - b1^t))
+ * (the factors that hold no element are formed in float64 and rounded once).
+ * Without a master the weight itself is read, updated and rounded to its type;
+ * with one the float32 master is read and updated and w receives its rounding.
+ *
+ * States are float32 (state_bits 32: m and v hold numel floats) or 8-bit codes
+ * (state_bits 8) of blocks of DF11_ADAMW_BLOCK consecutive elements of one
+ * tensor, the last block possibly shorter:
+ *   m = m_scale[b] c |c|      c = m[i], int8,  -127 .. 127
+ *   v = (v_scale[b] c^2)^2    c = v[i], uint8,    0 .. 255
+ * so that steps between neighbouring codes shrink with the value.  A step
+ * decodes them, updates the weights with the new float32 m and v, and stores
+ *   m_scale = max |m| (1 / 127^2),       c = sign(m) round(sqrt(|m| (1 / m_scale)))
+ *   v_scale = max sqrt(v) (1 / 255^2),   c = round(sqrt(sqrt(v) (1 / v_scale)))
+ * (codes no larger than their 127 and 255; ties to even; the code of a v above 0 is at least 1, since a v of 0 beside
+ * an m other than 0 would make the next update unbounded; a block whose
+ * largest |m| is below 2^-100 is held as zeros).  A block that holds a NaN or
+ * an infinity gets a NaN scale: all its states are NaN from then on.  Zeroed
+ * codes and scales are valid initial states.
+ *
+ * counts, where not null, receives the exponent histogram of the tensor's new
+ * BF16 weights (256 uint64, cleared by the call), as df11_histogram_device
+ * counts it; tensors may share one array, which then holds their sum.
+ */
+#define DF11_ADAMW_BLOCK 256
+typedef struct df11_adamw_tensor {
+    void *w;               /* numel weights of w_type */
+    float *master;         /* numel float32 masters of BF16 weights, or null */
+    const void *g;         /* numel gradients of g_type */
+    void *m, *v;           /* numel floats, or numel int8 / uint8 codes */
+    float *m_scale;        /* ceil(numel / DF11_ADAMW_BLOCK) floats (8-bit states) */
+    float *v_scale;
+    uint64_t *counts;      /* 256 counts of BF16 weights' exponents, or null */
+    uint64_t numel;        /* 0 .. 2^40; an empty tensor's pointers may be null */
+    double lr_scale;       /* this tensor's learning rate is lr * lr_scale */
+    double weight_decay;
+} df11_adamw_tensor;
+
+typedef struct df11_adamw_config {
+    double lr, beta1, beta2, eps;
+    uint64_t step;               /* t, from 1 */
+    uint32_t w_type, g_type;     /* DF11_TYPE_F32 or DF11_TYPE_BF16 */
+    uint32_t state_bits;         /* 32 or 8 */
+    uint32_t reserved;           /* 0 */
+    /* device values that, where not null, take the place of lr and step and
+     * scale the gradients (read when the kernels run, so that a captured call
+     * follows them): */
+    const float *d_lr;
+    const uint64_t *d_step;
+    const float *d_grad_factor;  /* f; not finite: the step changes nothing */
+} df11_adamw_config;
+
+/*
+ * One step of the n_tensors tensors, on stream st: one launch for every 36
+ * tensors that are not empty, and as many small ones before them where
+ * tensors have counts.  Pointers need their element's alignment only, so
+ * tensors may lie anywhere in a unit.  The buffers of different tensors must
+ * not overlap (counts excepted), and either all of them have masters or none
+ * does.  Without d_step a captured call replays the
+ * step number it was captured with.  Asynchronous.  Errors: DF11_E_INVALID
+ * (null or misaligned pointers, a type, state_bits or number out of range:
+ * lr, lr_scale and weight_decay finite and at least 0, beta1 and beta2 in
+ * [0, 1), eps above 0 in float32, step at least 1; a master or counts of
+ * weights that are not BF16; masters for some tensors only), DF11_E_HIP.
+ */
+int df11_adamw_step(const df11_adamw_config *c, const df11_adamw_tensor *t, uint32_t n_tensors,
+                    df11_hip_stream st);
+
+/*
+ * The values that 8-bit states stand for: m_out[k] and v_out[k] receive tensor
+ * k's numel values of m and v in type (DF11_TYPE_F32 or DF11_TYPE_BF16,
+ * rounded to nearest); either list may be null.  Reads m, v, m_scale, v_scale
+ * and numel of the tensors.  Asynchronous.  Errors as df11_adamw_step.
+ */
+int df11_adamw_values(const df11_adamw_tensor *t, uint32_t n_tensors, uint32_t type,
+                      void *const *m_out, void *const *v_out, df11_hip_stream st);
+
+/*
+ * The norm of the gradients of all n_tensors tensors together, and the factor
+ * that clips it, into d_norm (device, 2 floats):
+ *   d_norm[0] = n = sqrt(sum of g^2)     (squares and sums in float64)
+ *   d_norm[1] = min(1, max_norm / (n + 1e-6)), NaN where n is not finite
+ * so that &d_norm[1] can be df11_adamw_config.d_grad_factor.  Reads g and numel
+ * of the tensors.  The sums have a fixed order (deterministic).  scratch:
+ * device, 8-byte aligned, df11_grad_norm_scratch_bytes(t, n_tensors) bytes, not
+ * shared by calls that may overlap; no initialisation needed.  Asynchronous.
+ * Errors: DF11_E_INVALID (null or misaligned pointers, g_type not F32 or BF16,
+ * max_norm not above 0, a scratch that is too small), DF11_E_HIP.
+ */
+uint64_t df11_grad_norm_scratch_bytes(const df11_adamw_tensor *t, uint32_t n_tensors);
+int df11_grad_norm(uint32_t g_type, const df11_adamw_tensor *t, uint32_t n_tensors, double max_norm,
+                   float *d_norm, void *scratch, uint64_t scratch_bytes, df11_hip_stream st);
+
 #ifdef __cplusplus
 }
 #endif
