@@ -169,6 +169,36 @@ class df11_adamw_config(ctypes.Structure):
     ]
 
 
+class df11_int8_rows(ctypes.Structure):
+    _fields_ = [
+        ("src", ctypes.c_void_p),
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("src_stride", ctypes.c_uint64),
+        ("code_stride", ctypes.c_uint64),
+        ("rows", ctypes.c_uint32),
+        ("cols", ctypes.c_uint32),
+    ]
+
+
+class df11_int8_tensor(ctypes.Structure):
+    _fields_ = [
+        ("w", ctypes.c_void_p),
+        ("w_scale", ctypes.c_void_p),
+        ("x", ctypes.c_void_p),
+        ("x_scale", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("w_stride", ctypes.c_uint64),
+        ("x_stride", ctypes.c_uint64),
+        ("y_stride", ctypes.c_uint64),
+        ("rows", ctypes.c_uint32),
+        ("cols", ctypes.c_uint32),
+    ]
+
+
+DF11_INT8_MAX_TENSORS = 16
+DF11_INT8_MAX_COLS = 131071
+DF11_INT8_MAX_STRIDE = 1 << 22
 DF11_PIPELINE_MAX_SLOTS = 4
 DF11_ADAMW_BLOCK = 256
 # df11_type, by the names of torch's types
@@ -256,8 +286,12 @@ def _load():
     L.df11_grad_norm_scratch_bytes.restype = ctypes.c_uint64
     L.df11_grad_norm.argtypes = [ctypes.c_uint32, at, ctypes.c_uint32, ctypes.c_double, vp, vp,
                                  ctypes.c_uint64, vp]
+    L.df11_quantize_int8.argtypes = [ctypes.c_uint32, ctypes.POINTER(df11_int8_rows),
+                                     ctypes.c_uint32, vp]
+    L.df11_gemm_int8.argtypes = [ctypes.c_uint32, ctypes.POINTER(df11_int8_tensor),
+                                 ctypes.c_uint32, ctypes.c_uint32, vp]
     for f in (L.df11_build_codebook, L.df11_encode_size, L.df11_encode,
-              L.df11_adamw_step, L.df11_adamw_values, L.df11_grad_norm,
+              L.df11_quantize_int8, L.df11_gemm_int8, L.df11_adamw_step, L.df11_adamw_values, L.df11_grad_norm,
               L.df11_build_codebook_fmt, L.df11_encode_size_fmt, L.df11_encode_fmt,
               L.df11_decompress_block, L.df11_decompress_tensor, L.df11_pipeline_create,
               L.df11_pipeline_destroy, L.df11_pipeline_decompress, L.df11_pipeline_acquire,
@@ -801,6 +835,143 @@ def df11_decompress_gemv_noalloc(ds: DeviceStream, layout, x, y, status=None,
                                             ctypes.c_void_p(x.data_ptr()),
                                             ctypes.c_void_p(y.data_ptr()), sp,
                                             _stream_handle(stream)))
+
+
+# ---------------------------------------------------------------- products in 8-bit integers
+
+
+def _matrices(tensors, what):
+    """Checks 2-D device tensors of one type whose rows are contiguous."""
+    tensors = list(tensors)
+    if not 1 <= len(tensors) <= DF11_INT8_MAX_TENSORS:
+        raise ValueError(f"1 to {DF11_INT8_MAX_TENSORS} {what}")
+    first = tensors[0]
+    for t in tensors:
+        if t.dim() != 2 or not t.is_cuda or (t.size(1) > 1 and t.stride(1) != 1) or t.stride(0) < 0:
+            raise ValueError(f"{what} must be 2-D device tensors with contiguous rows")
+        if t.dtype != first.dtype or t.device != first.device:
+            raise TypeError(f"{what} must be of one type, on one device")
+    return tensors
+
+
+def _quantize(tensors, st):
+    """(code tensor, scale tensor) of each matrix, launched on the handle st."""
+    import torch
+
+    rows = (df11_int8_rows * len(tensors))()
+    out = []
+    for a, t in zip(rows, tensors):
+        r, c = t.shape
+        stride = (c + 15) // 16 * 16
+        codes = torch.empty((r, stride), dtype=torch.int8, device=t.device)
+        scales = torch.empty(r, dtype=torch.float32, device=t.device)
+        a.src, a.codes, a.scales = t.data_ptr(), codes.data_ptr(), scales.data_ptr()
+        a.src_stride, a.code_stride, a.rows, a.cols = t.stride(0), stride, r, c
+        out.append((codes, scales))
+    _check("df11_quantize_int8", LIB.df11_quantize_int8(_type(tensors[0].dtype), rows, len(rows), st))
+    return out
+
+
+def quantize_int8(tensors, stream=None):
+    """df11_quantize_int8 of up to DF11_INT8_MAX_TENSORS matrices (BF16, F16 or
+    float32 device tensors, contiguous rows): a list of (codes, scales), the
+    codes int8 [rows, cols rounded up to 16] with zeros behind the columns."""
+    tensors = _matrices(tensors, "matrices")
+    guard, st = _on(tensors[0].device, stream)
+    with guard:
+        return _quantize(tensors, st)
+
+
+class Int8Linear:
+    """The matrices of a block as 8-bit integers with a scale for each output
+    channel, multiplied with activations that are quantised token by token
+    (df11_quantize_int8, then df11_gemm_int8: two launches a call).
+
+    ``codes``: int8 device tensors [rows, stride], 16-byte aligned with strides
+    that are multiples of 16; ``scales``: float32 [rows]; ``shapes``: (rows,
+    cols) of each matrix.
+    """
+
+    def __init__(self, codes, scales, shapes):
+        import torch
+
+        self.codes = _matrices(codes, "codes")
+        self.scales, self.shapes = list(scales), [(int(r), int(c)) for r, c in shapes]
+        self.device = self.codes[0].device
+        if not len(self.codes) == len(self.scales) == len(self.shapes):
+            raise ValueError("one codes tensor, scales tensor and shape per matrix")
+        self._t = (df11_int8_tensor * len(self.codes))()
+        for a, q, s, (r, c) in zip(self._t, self.codes, self.scales, self.shapes):
+            if q.dtype != torch.int8 or q.size(0) != r or q.size(1) < c or (r > 1 and q.stride(0) < c):
+                raise ValueError("codes must be int8 of the shape's rows and at least its columns")
+            if s.dtype != torch.float32 or s.numel() != r or not s.is_contiguous() or s.device != self.device:
+                raise ValueError("scales must be float32, one per row")
+            # the product reads whole groups of 16 columns
+            stride = q.stride(0) if r > 1 else q.size(1)
+            if stride < (c + 15) // 16 * 16 or q.size(1) < (c + 15) // 16 * 16:
+                raise ValueError("codes must reach to the next multiple of 16 columns")
+            a.w, a.w_scale, a.w_stride, a.rows, a.cols = q.data_ptr(), s.data_ptr(), stride, r, c
+
+    @classmethod
+    def from_tensors(cls, tensors, stream=None):
+        """Quantises weight matrices (BF16, F16 or float32, [rows, cols])."""
+        held = quantize_int8(tensors, stream)
+        return cls([q for q, _ in held], [s for _, s in held], [tuple(t.shape) for t in tensors])
+
+    @classmethod
+    def from_unit(cls, ds: DeviceStream, shapes, status=None, stream=None):
+        """Decompresses a BF16 unit and quantises its matrices, whose ``shapes``
+        follow one another in it."""
+        import torch
+
+        if sum(r * c for r, c in shapes) != ds.n_weights or ds.desc.format != 0:
+            raise ValueError("the shapes must tile a BF16 unit")
+        guard, st = _on(ds.stream.device, stream)
+        with guard:
+            unit = torch.empty(ds.n_weights, dtype=torch.bfloat16, device=ds.stream.device)
+            df11_decompress_block(ds, unit, status, st.value or 0)
+            parts = unit.split([r * c for r, c in shapes])
+            held = _quantize(_matrices([p.view(s) for p, s in zip(parts, shapes)], "matrices"), st)
+        return cls([q for q, _ in held], [s for _, s in held], shapes)
+
+    def __call__(self, xs, out_dtype=None, out=None, stream=None):
+        """y = x W^T of every matrix: a list of [n_tokens, rows] tensors of
+        ``out_dtype`` (BF16 by default, F16 or float32), or written into the
+        tensors ``out``.  ``xs``: one [n_tokens, cols] tensor (BF16, F16 or
+        float32) per matrix; a tensor given for several is quantised once."""
+        import torch
+
+        xs = _matrices(xs, "activations")
+        if len(xs) != len(self.shapes):
+            raise ValueError("one activation tensor per matrix")
+        if xs[0].device != self.device:
+            raise ValueError(f"activations must be on {self.device}")
+        n_tokens = xs[0].size(0)
+        for x, (_, c) in zip(xs, self.shapes):
+            if x.size(0) != n_tokens or x.size(1) != c:
+                raise ValueError("activations must be [n_tokens, cols] of their matrix")
+        guard, st = _on(self.device, stream)
+        with guard:
+            if out is None:
+                kind = torch.bfloat16 if out_dtype is None else out_dtype
+                out = [torch.empty((n_tokens, r), dtype=kind, device=self.device)
+                       for r, _ in self.shapes]
+            else:
+                out = _matrices(out, "outputs")
+                kind = out[0].dtype
+                if out[0].device != self.device or [tuple(y.shape) for y in out] != [
+                        (n_tokens, r) for r, _ in self.shapes] or out_dtype not in (None, kind):
+                    raise ValueError("outputs must be [n_tokens, rows] of their matrix")
+            y_type = _type(kind)
+            unique = {id(x): x for x in xs}
+            held = dict(zip(unique, _quantize(list(unique.values()), st)))
+            t = (df11_int8_tensor * len(xs)).from_buffer_copy(self._t)
+            for a, x, y in zip(t, xs, out):
+                q, s = held[id(x)]
+                a.x, a.x_scale, a.y = q.data_ptr(), s.data_ptr(), y.data_ptr()
+                a.x_stride, a.y_stride = q.size(1), max(y.stride(0), y.size(1)) if n_tokens < 2 else y.stride(0)
+            _check("df11_gemm_int8", LIB.df11_gemm_int8(y_type, t, len(t), n_tokens, st))
+        return out
 
 
 # ---------------------------------------------------------------- optimiser step

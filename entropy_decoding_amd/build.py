@@ -37,7 +37,8 @@ def build_library(verbose: bool = False, extra_hip_flags=()) -> str:
     _run([HIPCC, *HIP_FLAGS, *extra_hip_flags, "-I", INCLUDE, "-c",
           os.path.join(CSRC, "df11_device.hip"), "-o", dev_o], verbose)
     objs = [host_o, dev_o]
-    for name in ("df11_pipeline", "df11_encode_device", "df11_adamw"):
+    for name in ("df11_pipeline", "df11_encode_device", "df11_adamw",
+                 "df11_int8"):
         o = os.path.join(BUILD, name + ".o")
         _run([HIPCC, *HIP_FLAGS, *extra_hip_flags, "-I", INCLUDE, "-c",
               os.path.join(CSRC, name + ".hip"), "-o", o], verbose)

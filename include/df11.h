@@ -654,6 +654,75 @@ uint64_t df11_grad_norm_scratch_bytes(const df11_adamw_tensor *t, uint32_t n_ten
 int df11_grad_norm(uint32_t g_type, const df11_adamw_tensor *t, uint32_t n_tensors, double max_norm,
                    float *d_norm, void *scratch, uint64_t scratch_bytes, df11_hip_stream st);
 
+/*
+ * Products in 8-bit integers -- device, for a decoded or freshly updated block
+ * that is served in int8: a scale for each output channel (row of a weight
+ * matrix) and one for each token (row of the activations).
+ *
+ * df11_quantize_int8: the rows of n matrices (<= DF11_INT8_MAX_TENSORS; weights
+ * or activations) of src_type to codes and scales, in one launch.  With
+ * a = max |row|:
+ *   scale = a / 127 (float32)        code = round(127 x / a), ties to even
+ * The rounding is that of the real quotient 127 x / a, for every type.  A row
+ * of zeros (or of no columns) has scale 0 and codes 0; a row that holds a NaN
+ * or an infinity has scale NaN and codes 0, so that what is multiplied with it
+ * is NaN.  Row r is src[r * src_stride ..]; its codes are
+ * codes[r * code_stride ..], followed by zero codes up to the next multiple
+ * of 16 columns.  Strides are in elements.  src needs its element's alignment
+ * only; codes 16-byte aligned; code_stride a multiple of 16 and at least
+ * cols; scales 4-byte aligned.  Outputs must not overlap anything.
+ * Asynchronous.  Errors: DF11_E_INVALID (null or misaligned pointers, src_type,
+ * n, strides, cols above DF11_INT8_MAX_COLS), DF11_E_HIP.
+ */
+#define DF11_INT8_MAX_TENSORS 16
+#define DF11_INT8_MAX_COLS 131071u        /* 128 * 128 * 131071 < 2^31 */
+#define DF11_INT8_MAX_STRIDE (1u << 22)   /* of the codes */
+typedef struct df11_int8_rows {
+    const void *src;
+    int8_t *codes;
+    float *scales;
+    uint64_t src_stride;
+    uint64_t code_stride;
+    uint32_t rows;
+    uint32_t cols;
+} df11_int8_rows;
+
+int df11_quantize_int8(uint32_t src_type, const df11_int8_rows *m, uint32_t n, df11_hip_stream st);
+
+/*
+ * df11_gemm_int8: for each of n_tensors (<= DF11_INT8_MAX_TENSORS) weight
+ * matrices of rows_k x cols_k codes and n_tokens rows of activation codes,
+ *   y_k[t][r] = (float(sum over c of x_k[t][c] * w_k[r][c]) * x_scale_k[t]) * w_scale_k[r]
+ * on the matrix cores.  The sum is exact (int32; codes -128 .. 127, at most
+ * DF11_INT8_MAX_COLS columns), its conversion and the two products are
+ * rounded in float32 and the result once to y_type.  Matrices may share x.
+ * Row r of w is w[r * w_stride ..], token t of x is x[t * x_stride ..], of y
+ * y[t * y_stride ..] (elements of y_type).  w and x 16-byte aligned, w_stride
+ * and x_stride multiples of 16, at least cols and at most
+ * DF11_INT8_MAX_STRIDE; codes behind cols in a row may be anything, but are
+ * read up to the next multiple of 16.  y needs its element's alignment only,
+ * y_stride at least rows; elements of y between rows and y_stride are left as
+ * they were.  y must not overlap anything.  cols 0 gives zeros times the
+ * scales.  One launch on st, asynchronous, no workspace; the result does not
+ * depend on how the work is split.  Errors: DF11_E_INVALID (null or misaligned
+ * pointers, y_type, n_tensors, strides, sizes), DF11_E_HIP.
+ */
+typedef struct df11_int8_tensor {
+    const int8_t *w;
+    const float *w_scale;   /* rows */
+    const int8_t *x;
+    const float *x_scale;   /* n_tokens */
+    void *y;
+    uint64_t w_stride;
+    uint64_t x_stride;
+    uint64_t y_stride;
+    uint32_t rows;
+    uint32_t cols;
+} df11_int8_tensor;
+
+int df11_gemm_int8(uint32_t y_type, const df11_int8_tensor *t, uint32_t n_tensors,
+                   uint32_t n_tokens, df11_hip_stream st);
+
 #ifdef __cplusplus
 }
 #endif
