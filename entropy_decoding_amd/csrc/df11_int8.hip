@@ -239,6 +239,194 @@ __global__ __launch_bounds__(256) void gemm_rows16(GemmArgs a) {
     }
 }
 
+// Many tokens: a workgroup computes a tile of BT tokens x BR weight rows, its
+// WT x WR waves a part of 32x32 products each.  The tiles' codes go from HBM
+// straight to LDS, 128 columns at a time, into one of two buffers while the
+// other is multiplied.
+//
+// A 128-byte row of a tile is 8 chunks of 16 bytes; chunk c of row r lies in
+// slot c ^ (r % 8), so that the 8 lanes which LDS serves at once, 8 rows of
+// the same chunk, find theirs in 8 different slots.  A lane's load takes the
+// chunk that belongs in its slot (LDS receives a wave's lanes in order).
+constexpr uint32_t kDepth = 128;  // columns of a stage
+
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+// A tile's rows in global memory: where a lane's chunk lies for each of its
+// wave's loads (8 rows a load), relative to the first row.
+template <int LOADS>
+struct Source {
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t at[LOADS];
+    __device__ void init(const int8_t *first, uint32_t stride, uint32_t left, uint32_t cols,
+                         uint32_t wave, uint32_t lane) {
+        const uint32_t last = left - 1;  // rows past the end repeat the last one
+        rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(first), 0,
+                                                 int(last * stride + ((cols + 15) & ~15u)), 0x00020000);
+#pragma unroll
+        for (int j = 0; j < LOADS; j++)
+            at[j] = min((wave * LOADS + j) * 8 + (lane >> 3), last) * stride;
+    }
+    // columns c0 .. c0 + 127 to LDS; those of the last stage that lie past
+    // the row's last chunk repeat it, so that nothing outside is read
+    __device__ void load(int8_t *lds, uint32_t c0, uint32_t cols, uint32_t wave, uint32_t lane) const {
+        uint32_t c = 16 * ((lane ^ (lane >> 3)) & 7u);
+        if (c0 + kDepth > cols) c = min(c0 + c, (cols - 1) & ~15u) - c0;
+#ifdef __HIP_DEVICE_COMPILE__  // the host's pass knows no 16-byte loads to LDS
+#pragma unroll
+        for (int j = 0; j < LOADS; j++)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsrc, (lds_void *)(lds + (wave * LOADS + j) * 1024), 16, at[j] + c, c0, 0, 0);
+#endif
+    }
+};
+
+// Clears the columns from `cols` on of a stage of activations: the weights'
+// codes there, whatever they are, then add nothing.
+template <int ROWS>
+__device__ __forceinline__ void clear_behind(int8_t *lds, uint32_t left, uint32_t threads) {
+    for (uint32_t i = threadIdx.x; i < ROWS * 8; i += threads) {
+        const uint32_t row = i >> 3, c = 16 * ((i ^ row) & 7u);
+        if (c + 16 <= left) continue;
+        i32x4 *p = reinterpret_cast<i32x4 *>(lds + i * 16);
+        i32x4 v = *p;
+#pragma unroll
+        for (uint32_t d = 0; d < 4; d++) {
+            const uint32_t at = c + 4 * d, keep = at >= left ? 0u : left - at;
+            if (keep < 4) v[d] = int(uint32_t(v[d]) & ((1u << (8 * keep)) - 1u));
+        }
+        *p = v;
+    }
+}
+
+// A wave's part of a stage: four steps of 32 columns.  The operands of a step
+// are read while the one before is multiplied (the scheduling barriers hold
+// the reads there).
+template <int FT, int FR>
+__device__ __forceinline__ void multiply(const int8_t *xs, const int8_t *ws, i32x16 (&acc)[FT][FR]) {
+    const uint32_t lane = threadIdx.x & 63u;
+    i32x4 x[2][FT], w[2][FR];
+    const auto read = [&](uint32_t kk) {
+        const uint32_t at = (lane & 31u) * 128 + (((2 * kk + (lane >> 5)) ^ (lane & 7u)) << 4);
+#pragma unroll
+        for (int f = 0; f < FT; f++) x[kk & 1][f] = *reinterpret_cast<const i32x4 *>(xs + f * 4096 + at);
+#pragma unroll
+        for (int f = 0; f < FR; f++) w[kk & 1][f] = *reinterpret_cast<const i32x4 *>(ws + f * 4096 + at);
+    };
+    read(0);
+#pragma unroll
+    for (uint32_t kk = 0; kk < 4; kk++) {
+        if (kk < 3) read(kk + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < FT; f++)
+#pragma unroll
+            for (int h = 0; h < FR; h++)
+                acc[f][h] = __builtin_amdgcn_mfma_i32_32x32x32_i8(x[kk & 1][f], w[kk & 1][h], acc[f][h],
+                                                                  0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// This wave's loads have arrived, all waves' reads of the other buffer too.
+__device__ __forceinline__ void arrive() {
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): loads to LDS are no LDS operations
+    __syncthreads();
+}
+
+template <class Y, int BT, int BR, int WT, int WR>
+__global__ __launch_bounds__(64 * WT * WR) void gemm_tile(GemmArgs a, uint32_t token_tiles,
+                                                          uint32_t n_tiles) {
+    constexpr int kWaves = WT * WR, FT = BT / WT / 32, FR = BR / WR / 32;
+    __shared__ __align__(16) int8_t x0[BT * kDepth], w0[BR * kDepth], x1[BT * kDepth], w1[BR * kDepth];
+    // Workgroups go to the 8 XCDs in turn: XCD x takes the x-th run of tiles
+    const uint32_t per = n_tiles / 8, rest = n_tiles % 8, xcd = blockIdx.x % 8;
+    const uint32_t tile = xcd * per + min(xcd, rest) + blockIdx.x / 8;
+    uint32_t k = 0;
+#pragma unroll
+    for (int j = 1; j < kMax; j++) k += uint32_t(tile >= a.first[j]);
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t rows = a.rows[k], cols = a.cols[k];
+    // and walks them 4 token tiles wide, so that the tiles at work on an XCD
+    // share both operands in its L2
+    const uint32_t row_tiles = (rows + BR - 1) / BR, band = 4 * row_tiles;
+    const uint32_t in = tile - a.first[k], t_first = in / band * 4;
+    const uint32_t width = min(4u, token_tiles - t_first);
+    // (a division by a variable runs on the vector unit)
+    const uint32_t r0 = __builtin_amdgcn_readfirstlane((in % band) / width * BR);
+    const uint32_t t0 = __builtin_amdgcn_readfirstlane((t_first + (in % band) % width) * BT);
+
+    constexpr int XL = BT / 8 / kWaves, WL = BR / 8 / kWaves;
+    Source<XL> sx;
+    Source<WL> sw;
+    sx.init(a.x[k] + uint64_t(t0) * a.x_stride[k], a.x_stride[k], min(uint32_t(BT), a.n_tokens - t0),
+            cols, wave, lane);
+    sw.init(a.w[k] + uint64_t(r0) * a.w_stride[k], a.w_stride[k], min(uint32_t(BR), rows - r0), cols,
+            wave, lane);
+    const uint32_t wt = wave / WR * (BT / WT), wr = wave % WR * (BR / WR);
+    i32x16 acc[FT][FR];
+#pragma unroll
+    for (int f = 0; f < FT; f++)
+#pragma unroll
+        for (int h = 0; h < FR; h++)
+#pragma unroll
+            for (int e = 0; e < 16; e++) acc[f][h][e] = 0;
+
+    if (cols) {
+        sx.load(x0, 0, cols, wave, lane);
+        sw.load(w0, 0, cols, wave, lane);
+    }
+    uint32_t c = 0;
+    for (; c + 2 * kDepth <= cols; c += 2 * kDepth) {
+        arrive();
+        sx.load(x1, c + kDepth, cols, wave, lane);
+        sw.load(w1, c + kDepth, cols, wave, lane);
+        multiply<FT, FR>(x0 + wt * kDepth, w0 + wr * kDepth, acc);
+        arrive();
+        if (c + 2 * kDepth < cols) {
+            sx.load(x0, c + 2 * kDepth, cols, wave, lane);
+            sw.load(w0, c + 2 * kDepth, cols, wave, lane);
+        }
+        multiply<FT, FR>(x1 + wt * kDepth, w1 + wr * kDepth, acc);
+    }
+    if (c < cols) {  // one stage, whole or not, or one whole and one not
+        arrive();
+        if (c + kDepth < cols) {
+            sx.load(x1, c + kDepth, cols, wave, lane);
+            sw.load(w1, c + kDepth, cols, wave, lane);
+        } else if (cols - c < kDepth) {
+            clear_behind<BT>(x0, cols - c, 64 * kWaves);
+            __syncthreads();
+        }
+        multiply<FT, FR>(x0 + wt * kDepth, w0 + wr * kDepth, acc);
+        if (c + kDepth < cols) {
+            arrive();
+            clear_behind<BT>(x1, cols - c - kDepth, 64 * kWaves);
+            __syncthreads();
+            multiply<FT, FR>(x1 + wt * kDepth, w1 + wr * kDepth, acc);
+        }
+    }
+
+    // lane l holds row l % 32 of each product, element e token 8 (e / 4) + 4 (l / 32) + e % 4
+    Y *y = static_cast<Y *>(a.y[k]);
+#pragma unroll
+    for (int h = 0; h < FR; h++) {
+        const uint32_t r = r0 + wr + 32 * h + (lane & 31u);
+        if (r >= rows) continue;
+        const float s = a.w_scale[k][r];
+#pragma unroll
+        for (int f = 0; f < FT; f++) {
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+                const uint32_t t = t0 + wt + 32 * f + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
+                if (t < a.n_tokens) put(y, t * a.y_stride[k] + r, acc[f][h][e], a.x_scale[k][t], s);
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------- host
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -247,8 +435,22 @@ int status(hipError_t e) { return e == hipSuccess ? DF11_OK : DF11_E_HIP; }
 
 uint32_t type_bytes(uint32_t type) { return type == DF11_TYPE_F32 ? 4 : 2; }
 
+template <class Y, int BT, int BR, int WT, int WR>
+int run_tiles(GemmArgs &a, uint32_t n, hipStream_t st) {
+    const uint32_t token_tiles = (a.n_tokens + BT - 1) / BT;
+    uint64_t tiles = 0;
+    for (uint32_t k = 0; k < n; k++) {
+        a.first[k] = uint32_t(tiles);
+        tiles += uint64_t((a.rows[k] + BR - 1) / BR) * token_tiles;
+        if (tiles > 0x7FFFFFFFu) return DF11_E_INVALID;
+    }
+    return status(launch(gemm_tile<Y, BT, BR, WT, WR>, dim3(uint32_t(tiles)), dim3(64 * WT * WR), 0, st,
+                         a, token_tiles, uint32_t(tiles)));
+}
+
 template <class Y>
 int run_gemm(GemmArgs &a, uint32_t n, hipStream_t st) {
+    if (a.n_tokens > 64) return run_tiles<Y, 256, 256, 2, 4>(a, n, st);
     uint32_t tiles = 0;
     for (uint32_t k = 0; k < n; k++) {
         a.first[k] = tiles;
