@@ -149,94 +149,85 @@ __device__ __forceinline__ float scaled(int sum, float xs, float ws) {
     asm("" : "+v"(v));
     return v;
 }
-template <class Y>
-__device__ __forceinline__ void put(Y *y, uint64_t at, int sum, float xs, float ws) {
-    y[at] = Y(scaled(sum, xs, ws));
-}
-
-// 16 codes of row p at column c of `cols`, zeros past the end
+// 16 codes of a row at column c, those behind `cols` cleared; only the row is read
 __device__ __forceinline__ i32x4 codes16(const int8_t *p, uint32_t c, uint32_t cols) {
-    i32x4 v = {0, 0, 0, 0};
-    if (c < cols) v = *reinterpret_cast<const i32x4 *>(p + c);
-    return v;
-}
-// the same with the codes behind `cols` cleared
-__device__ __forceinline__ i32x4 codes16_cut(const int8_t *p, uint32_t c, uint32_t cols) {
-    i32x4 v = codes16(p, c, cols);
+    i32x4 v = *reinterpret_cast<const i32x4 *>(p + min(c, (cols - 1) & ~15u));
 #pragma unroll
     for (uint32_t d = 0; d < 4; d++) {
-        const uint32_t at = c + 4 * d;
-        const uint32_t keep = at >= cols ? 0u : cols - at;
+        const uint32_t at = c + 4 * d, keep = at >= cols ? 0u : cols - at;
         if (keep < 4) v[d] = int(uint32_t(v[d]) & ((1u << (8 * keep)) - 1u));
     }
     return v;
 }
 
-// Few tokens: a workgroup takes 16 weight rows and NT groups of 16 tokens; its
-// four waves split the columns in runs of 256 and their sums meet in LDS.
-// Lane 16 q + i of a wave holds row i (or token i) and columns 16 q .. of a
-// 16x16x64 product, which the operands' row-major order gives as is.
-template <class Y, int NT>
-__global__ __launch_bounds__(256) void gemm_rows16(GemmArgs a) {
-    __shared__ i32x4 part[3][NT][64];
+// Few rows and at most 16 tokens, where what counts is the time of one
+// workgroup: it takes 16 weight rows, its eight waves split the columns in runs
+// of 128, and each has the operands of 512 columns in flight at once.  The
+// waves' sums meet in LDS.  Lane 16 q + i of a wave holds row i (or token i) and
+// columns 16 q .. of a 16x16x64 product, which the operands' row-major order
+// gives as is.
+constexpr uint32_t kRowWaves = 8;
+
+template <class Y>
+__global__ __launch_bounds__(64 * kRowWaves) void gemm_rows16(GemmArgs a) {
+    __shared__ i32x4 part[kRowWaves - 1][64];
     uint32_t k = 0;
 #pragma unroll
     for (int j = 1; j < kMax; j++) k += uint32_t(blockIdx.x >= a.first[j]);
-    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-    const uint32_t r0 = (blockIdx.x - a.first[k]) * 16, t0 = blockIdx.y * 16 * NT;
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t r0 = (blockIdx.x - a.first[k]) * 16;
     const uint32_t rows = a.rows[k], cols = a.cols[k], i = lane & 15u, q = lane >> 4;
     const int8_t *w = a.w[k] + uint64_t(min(r0 + i, rows - 1)) * a.w_stride[k];
-    const int8_t *x[NT];
-#pragma unroll
-    for (int n = 0; n < NT; n++)
-        x[n] = a.x[k] + uint64_t(min(t0 + 16 * n + i, a.n_tokens - 1)) * a.x_stride[k];
-    i32x4 acc[NT];
-#pragma unroll
-    for (int n = 0; n < NT; n++) acc[n] = i32x4{0, 0, 0, 0};
-    for (uint32_t c0 = wave * 256; c0 < cols; c0 += 1024) {
-        if (c0 + 256 <= cols) {
-#pragma unroll
-            for (int u = 0; u < 4; u++) {
-                const uint32_t c = c0 + 64 * u + 16 * q;
-                const i32x4 wv = *reinterpret_cast<const i32x4 *>(w + c);
-#pragma unroll
-                for (int n = 0; n < NT; n++)
-                    acc[n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-                        wv, *reinterpret_cast<const i32x4 *>(x[n] + c), acc[n], 0, 0, 0);
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < 4; u++) {
-                const uint32_t c = c0 + 64 * u + 16 * q;
-                const i32x4 wv = codes16_cut(w, c, cols);
-#pragma unroll
-                for (int n = 0; n < NT; n++)
-                    acc[n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv, codes16(x[n], c, cols), acc[n],
-                                                                   0, 0, 0);
-            }
-        }
-    }
-    if (wave) {
-#pragma unroll
-        for (int n = 0; n < NT; n++) part[wave - 1][n][lane] = acc[n];
-    }
-    __syncthreads();
-    if (wave) return;
-    // lane 16 q + j holds rows 4 q .. + 3 of token j
-    Y *y = static_cast<Y *>(a.y[k]);
+    const int8_t *x = a.x[k] + uint64_t(min(i, a.n_tokens - 1)) * a.x_stride[k];
+    const float xs = a.x_scale[k][min(i, a.n_tokens - 1)];
     float ws[4];
 #pragma unroll
     for (uint32_t e = 0; e < 4; e++) ws[e] = a.w_scale[k][min(r0 + 4 * q + e, rows - 1)];
+    i32x4 acc = {0, 0, 0, 0};
+    constexpr uint32_t kRun = kRowWaves * 128;
+    // (c0 - 16 q is the same for the wave)
+    uint32_t c0 = wave * 128 + 16 * q;
+    for (; c0 - 16 * q + 3 * kRun + 128 <= cols; c0 += 4 * kRun) {
+        i32x4 wv[8], xv[8];
 #pragma unroll
-    for (int n = 0; n < NT; n++) {
-        const i32x4 s = acc[n] + part[0][n][lane] + part[1][n][lane] + part[2][n][lane];
-        const uint32_t t = t0 + 16 * n + i;
-        if (t >= a.n_tokens) continue;
-        const float xs = a.x_scale[k][t];
+        for (int u = 0; u < 8; u++) {
+            const uint32_t c = c0 + kRun * (u / 2) + 64 * (u % 2);
+            wv[u] = *reinterpret_cast<const i32x4 *>(w + c);
+            xv[u] = *reinterpret_cast<const i32x4 *>(x + c);
+        }
 #pragma unroll
-        for (uint32_t e = 0; e < 4; e++)
-            if (r0 + 4 * q + e < rows) put(y, t * a.y_stride[k] + r0 + 4 * q + e, s[e], xs, ws[e]);
+        for (int u = 0; u < 8; u++)
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u], xv[u], acc, 0, 0, 0);
     }
+    for (; c0 - 16 * q < cols; c0 += kRun) {
+        i32x4 wv[2], xv[2];
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            const uint32_t c = c0 + 64 * u;
+            if (c0 - 16 * q + 128 <= cols) {
+                wv[u] = *reinterpret_cast<const i32x4 *>(w + c);
+                xv[u] = *reinterpret_cast<const i32x4 *>(x + c);
+            } else {
+                wv[u] = codes16(w, c, cols);
+                xv[u] = *reinterpret_cast<const i32x4 *>(x + min(c, (cols - 1) & ~15u));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u], xv[u], acc, 0, 0, 0);
+    }
+    if (wave) part[wave - 1][lane] = acc;
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (uint32_t p = 0; p < kRowWaves - 1; p++) acc += part[p][lane];
+    // lane 16 q + j holds rows 4 q .. + 3 of token j
+    if (i >= a.n_tokens) return;
+    Y *y = static_cast<Y *>(a.y[k]) + i * a.y_stride[k] + r0 + 4 * q;
+#pragma unroll
+    for (uint32_t e = 0; e < 4; e++)
+        if (r0 + 4 * q + e < rows) y[e] = Y(scaled(acc[e], xs, ws[e]));
 }
 
 // Many tokens: a workgroup computes a tile of BT tokens x BR weight rows, its
@@ -245,9 +236,11 @@ __global__ __launch_bounds__(256) void gemm_rows16(GemmArgs a) {
 // other is multiplied.
 //
 // A 128-byte row of a tile is 8 chunks of 16 bytes; chunk c of row r lies in
-// slot c ^ (r % 8), so that the 8 lanes which LDS serves at once, 8 rows of
-// the same chunk, find theirs in 8 different slots.  A lane's load takes the
-// chunk that belongs in its slot (LDS receives a wave's lanes in order).
+// slot c ^ (r / 2 % 8): LDS serves 16 lanes of a 16-byte read at once, and
+// these find the same chunk of their rows without a conflict (4.1 cycles a
+// read, as for consecutive addresses; 8.1 with r % 8, 32 without a swizzle).
+// A lane's load takes the chunk that belongs in its slot (LDS receives a
+// wave's lanes in order).
 constexpr uint32_t kDepth = 128;  // columns of a stage
 
 typedef int i32x16 __attribute__((ext_vector_type(16)));
@@ -257,27 +250,44 @@ typedef __attribute__((address_space(3))) void lds_void;
 // wave's loads (8 rows a load), relative to the first row.
 template <int LOADS>
 struct Source {
-    __amdgpu_buffer_rsrc_t rsrc;
-    uint32_t at[LOADS];
-    __device__ void init(const int8_t *first, uint32_t stride, uint32_t left, uint32_t cols,
+    int8_t *first;
+    uint32_t bytes, at[LOADS];
+    // lane's first column in load j: the chunk of its slot
+    static __device__ uint32_t column(uint32_t wave, uint32_t lane, int j) {
+        return 16 * ((lane ^ (((wave * LOADS + j) * 8 + (lane >> 3)) >> 1)) & 7u);
+    }
+    __device__ void init(const int8_t *p, uint32_t stride, uint32_t left, uint32_t cols,
                          uint32_t wave, uint32_t lane) {
         const uint32_t last = left - 1;  // rows past the end repeat the last one
-        rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(first), 0,
-                                                 int(last * stride + ((cols + 15) & ~15u)), 0x00020000);
+        first = const_cast<int8_t *>(p);
+        bytes = last * stride + ((cols + 15) & ~15u);
 #pragma unroll
         for (int j = 0; j < LOADS; j++)
-            at[j] = min((wave * LOADS + j) * 8 + (lane >> 3), last) * stride;
+            at[j] = min((wave * LOADS + j) * 8 + (lane >> 3), last) * stride + column(wave, lane, j);
     }
-    // columns c0 .. c0 + 127 to LDS; those of the last stage that lie past
-    // the row's last chunk repeat it, so that nothing outside is read
-    __device__ void load(int8_t *lds, uint32_t c0, uint32_t cols, uint32_t wave, uint32_t lane) const {
-        uint32_t c = 16 * ((lane ^ (lane >> 3)) & 7u);
-        if (c0 + kDepth > cols) c = min(c0 + c, (cols - 1) & ~15u) - c0;
+    // columns tail .. `cols` to LDS; chunks past a row's last one repeat it, so
+    // that nothing outside is read
+    __device__ __forceinline__ void load_tail(int8_t *lds, uint32_t tail, uint32_t cols, uint32_t wave,
+                                              uint32_t lane) const {
+        Source s = *this;
+#pragma unroll
+        for (int j = 0; j < LOADS; j++) {
+            const uint32_t c = column(wave, lane, j);
+            s.at[j] -= c - (min(tail + c, (cols - 1) & ~15u) - tail);
+        }
+        s.load(lds, tail, true, wave);
+    }
+    // columns c0 .. c0 + 127 to LDS, loads `from` .. `to`; zeros if not `on`
+    __device__ __forceinline__ void load(int8_t *lds, uint32_t c0, bool on, uint32_t wave,
+                                         int from = 0, int to = LOADS) const {
 #ifdef __HIP_DEVICE_COMPILE__  // the host's pass knows no 16-byte loads to LDS
+        const __amdgpu_buffer_rsrc_t rsrc =
+            __builtin_amdgcn_make_buffer_rsrc(first, 0, on ? int(bytes) : 0, 0x00020000);
 #pragma unroll
         for (int j = 0; j < LOADS; j++)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rsrc, (lds_void *)(lds + (wave * LOADS + j) * 1024), 16, at[j] + c, c0, 0, 0);
+            if (j >= from && j < to)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rsrc, (lds_void *)(lds + (wave * LOADS + j) * 1024), 16, at[j], c0, 0, 0);
 #endif
     }
 };
@@ -287,7 +297,7 @@ struct Source {
 template <int ROWS>
 __device__ __forceinline__ void clear_behind(int8_t *lds, uint32_t left, uint32_t threads) {
     for (uint32_t i = threadIdx.x; i < ROWS * 8; i += threads) {
-        const uint32_t row = i >> 3, c = 16 * ((i ^ row) & 7u);
+        const uint32_t row = i >> 3, c = 16 * ((i ^ (row >> 1)) & 7u);
         if (c + 16 <= left) continue;
         i32x4 *p = reinterpret_cast<i32x4 *>(lds + i * 16);
         i32x4 v = *p;
@@ -300,59 +310,40 @@ __device__ __forceinline__ void clear_behind(int8_t *lds, uint32_t left, uint32_
     }
 }
 
-// A wave's part of a stage: four steps of 32 columns.  The operands of a step
-// are read while the one before is multiplied (the scheduling barriers hold
-// the reads there).
+// The operands of one step of 32 columns.
 template <int FT, int FR>
-__device__ __forceinline__ void multiply(const int8_t *xs, const int8_t *ws, i32x16 (&acc)[FT][FR]) {
-    const uint32_t lane = threadIdx.x & 63u;
-    i32x4 x[2][FT], w[2][FR];
-    const auto read = [&](uint32_t kk) {
-        const uint32_t at = (lane & 31u) * 128 + (((2 * kk + (lane >> 5)) ^ (lane & 7u)) << 4);
-#pragma unroll
-        for (int f = 0; f < FT; f++) x[kk & 1][f] = *reinterpret_cast<const i32x4 *>(xs + f * 4096 + at);
-#pragma unroll
-        for (int f = 0; f < FR; f++) w[kk & 1][f] = *reinterpret_cast<const i32x4 *>(ws + f * 4096 + at);
-    };
-    read(0);
-#pragma unroll
-    for (uint32_t kk = 0; kk < 4; kk++) {
-        if (kk < 3) read(kk + 1);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int f = 0; f < FT; f++)
-#pragma unroll
-            for (int h = 0; h < FR; h++)
-                acc[f][h] = __builtin_amdgcn_mfma_i32_32x32x32_i8(x[kk & 1][f], w[kk & 1][h], acc[f][h],
-                                                                  0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-    }
-}
+struct Operands {
+    i32x4 x[FT], w[FR];
+};
 
-// This wave's loads have arrived, all waves' reads of the other buffer too.
-__device__ __forceinline__ void arrive() {
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): loads to LDS are no LDS operations
-    __syncthreads();
-}
-
-template <class Y, int BT, int BR, int WT, int WR>
-__global__ __launch_bounds__(64 * WT * WR) void gemm_tile(GemmArgs a, uint32_t token_tiles,
-                                                          uint32_t n_tiles) {
+template <class Y, int BT, int BR, int WT, int WR, int NB>
+__global__ __launch_bounds__(64 * WT * WR) void gemm_tile(GemmArgs a, uint32_t token_tiles) {
     constexpr int kWaves = WT * WR, FT = BT / WT / 32, FR = BR / WR / 32;
+    // a buffer is an object of its own, so that the compiler sees that reads
+    // of one do not wait for loads to another
     __shared__ __align__(16) int8_t x0[BT * kDepth], w0[BR * kDepth], x1[BT * kDepth], w1[BR * kDepth];
-    // Workgroups go to the 8 XCDs in turn: XCD x takes the x-th run of tiles
-    const uint32_t per = n_tiles / 8, rest = n_tiles % 8, xcd = blockIdx.x % 8;
-    const uint32_t tile = xcd * per + min(xcd, rest) + blockIdx.x / 8;
+    __shared__ __align__(16) int8_t x2[NB > 2 ? BT * kDepth : 16], w2[NB > 2 ? BR * kDepth : 16];
+    __shared__ __align__(16) int8_t x3[NB > 3 ? BT * kDepth : 16], w3[NB > 3 ? BR * kDepth : 16];
+    __shared__ __align__(16) int8_t x4[NB > 4 ? BT * kDepth : 16], w4[NB > 4 ? BR * kDepth : 16];
+    __shared__ __align__(16) int8_t x5[NB > 5 ? BT * kDepth : 16], w5[NB > 5 ? BR * kDepth : 16];
+    __shared__ __align__(16) float w_scale[BR];
+    // Workgroups go to the 8 XCDs in turn: every XCD takes one run of a
+    // matrix's tiles (first counts an XCD's tiles, so that matrices of longer
+    // rows burden all of them alike)
+    const uint32_t turn = blockIdx.x / 8;
     uint32_t k = 0;
 #pragma unroll
-    for (int j = 1; j < kMax; j++) k += uint32_t(tile >= a.first[j]);
+    for (int j = 1; j < kMax; j++) k += uint32_t(turn >= a.first[j]);
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t rows = a.rows[k], cols = a.cols[k];
+    const uint32_t row_tiles = (rows + BR - 1) / BR, band = 4 * row_tiles;
+    const uint32_t tiles = row_tiles * token_tiles;
+    const uint32_t in = blockIdx.x % 8 * ((tiles + 7) / 8) + turn - a.first[k];
+    if (in >= tiles) return;
     // and walks them 4 token tiles wide, so that the tiles at work on an XCD
     // share both operands in its L2
-    const uint32_t row_tiles = (rows + BR - 1) / BR, band = 4 * row_tiles;
-    const uint32_t in = tile - a.first[k], t_first = in / band * 4;
+    const uint32_t t_first = in / band * 4;
     const uint32_t width = min(4u, token_tiles - t_first);
     // (a division by a variable runs on the vector unit)
     const uint32_t r0 = __builtin_amdgcn_readfirstlane((in % band) / width * BR);
@@ -366,6 +357,8 @@ __global__ __launch_bounds__(64 * WT * WR) void gemm_tile(GemmArgs a, uint32_t t
     sw.init(a.w[k] + uint64_t(r0) * a.w_stride[k], a.w_stride[k], min(uint32_t(BR), rows - r0), cols,
             wave, lane);
     const uint32_t wt = wave / WR * (BT / WT), wr = wave % WR * (BR / WR);
+    for (uint32_t r = threadIdx.x; r < BR; r += 64 * kWaves)
+        w_scale[r] = a.w_scale[k][min(r0 + r, rows - 1)];
     i32x16 acc[FT][FR];
 #pragma unroll
     for (int f = 0; f < FT; f++)
@@ -374,54 +367,173 @@ __global__ __launch_bounds__(64 * WT * WR) void gemm_tile(GemmArgs a, uint32_t t
 #pragma unroll
             for (int e = 0; e < 16; e++) acc[f][h][e] = 0;
 
+    // A step of 32 columns multiplies one set of operands while the next set
+    // is read from LDS; before a stage's last step its waves meet: the next
+    // stage has arrived then, and this one's buffer is free for the one after
+    // it, whose loads go out between the products of that step.  The
+    // scheduling barriers hold the reads and loads between the products.
+    Operands<FT, FR> even, odd;
+    const auto read = [&](Operands<FT, FR> &o, const int8_t *xs, const int8_t *ws, uint32_t kk, int f) {
+        const uint32_t at = (lane & 31u) * 128 + (((2 * kk + (lane >> 5)) ^ (lane >> 1 & 7u)) << 4);
+        if (f < FT) o.x[f] = *reinterpret_cast<const i32x4 *>(xs + wt * kDepth + f * 4096 + at);
+        if (f < FR) o.w[f] = *reinterpret_cast<const i32x4 *>(ws + wr * kDepth + f * 4096 + at);
+    };
+    constexpr int kF = FT > FR ? FT : FR;
+    const auto products = [&](const Operands<FT, FR> &o, int f) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (f < FT) {
+#pragma unroll
+            for (int h = 0; h < FR; h++)
+                acc[f][h] = __builtin_amdgcn_mfma_i32_32x32x32_i8(o.w[h], o.x[f], acc[f][h], 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // the next stage has arrived when at most the loads of the NB - 2 behind it are out
+    constexpr int kOut = (NB - 2) * (XL + WL);
+    static_assert(kOut < 64, "the counter of loads");
+    const auto arrived = [&] {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt((kOut & 15) | (kOut >> 4 << 14) | 0x0070);  // and lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    // Stage 0 is the last 1 .. 128 columns, cleared behind the end; stage s > 0
+    // starts at column 128 (s - 1).  Loads for stages past the last give zeros,
+    // so that the loop has no conditions and the stages that fill up a round
+    // of the buffers add nothing.
+    const uint32_t stages = (cols + kDepth - 1) / kDepth;
+    const auto stage = [&](int8_t *xs, int8_t *ws, int8_t *xn, int8_t *wn, uint32_t s) {
+#pragma unroll
+        for (uint32_t kk = 0; kk < 3; kk++) {
+#pragma unroll
+            for (int f = 0; f < kF; f++) {
+                read(kk & 1 ? even : odd, xs, ws, kk + 1, f);
+                products(kk & 1 ? odd : even, f);
+            }
+        }
+        arrived();
+        const bool on = s + NB < stages;
+#pragma unroll
+        for (int f = 0; f < kF; f++) {
+            sx.load(xs, (s + NB - 1) * kDepth, on, wave, f * XL / kF, (f + 1) * XL / kF);
+            sw.load(ws, (s + NB - 1) * kDepth, on, wave, f * WL / kF, (f + 1) * WL / kF);
+            read(even, xn, wn, 0, f);
+            products(odd, f);
+        }
+    };
     if (cols) {
-        sx.load(x0, 0, cols, wave, lane);
-        sw.load(w0, 0, cols, wave, lane);
-    }
-    uint32_t c = 0;
-    for (; c + 2 * kDepth <= cols; c += 2 * kDepth) {
-        arrive();
-        sx.load(x1, c + kDepth, cols, wave, lane);
-        sw.load(w1, c + kDepth, cols, wave, lane);
-        multiply<FT, FR>(x0 + wt * kDepth, w0 + wr * kDepth, acc);
-        arrive();
-        if (c + 2 * kDepth < cols) {
-            sx.load(x0, c + 2 * kDepth, cols, wave, lane);
-            sw.load(w0, c + 2 * kDepth, cols, wave, lane);
+        const uint32_t tail = (stages - 1) * kDepth;
+        sx.load_tail(x0, tail, cols, wave, lane);
+        sw.load_tail(w0, tail, cols, wave, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        const auto begin = [&](int8_t *xs, int8_t *ws, uint32_t s) {
+            sx.load(xs, (s - 1) * kDepth, s < stages, wave);
+            sw.load(ws, (s - 1) * kDepth, s < stages, wave);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        begin(x1, w1, 1);
+        if constexpr (NB > 2) begin(x2, w2, 2);
+        if constexpr (NB > 3) begin(x3, w3, 3);
+        if constexpr (NB > 4) begin(x4, w4, 4);
+        if constexpr (NB > 5) begin(x5, w5, 5);
+        constexpr int kFirst = (NB - 1) * (XL + WL);
+        static_assert(kFirst < 64, "the counter of loads");
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt((kFirst & 15) | (kFirst >> 4 << 14) | 0x0070);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (cols % kDepth) {
+            clear_behind<BT>(x0, cols - tail, 64 * kWaves);
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
         }
-        multiply<FT, FR>(x1 + wt * kDepth, w1 + wr * kDepth, acc);
-    }
-    if (c < cols) {  // one stage, whole or not, or one whole and one not
-        arrive();
-        if (c + kDepth < cols) {
-            sx.load(x1, c + kDepth, cols, wave, lane);
-            sw.load(w1, c + kDepth, cols, wave, lane);
-        } else if (cols - c < kDepth) {
-            clear_behind<BT>(x0, cols - c, 64 * kWaves);
-            __syncthreads();
-        }
-        multiply<FT, FR>(x0 + wt * kDepth, w0 + wr * kDepth, acc);
-        if (c + kDepth < cols) {
-            arrive();
-            clear_behind<BT>(x1, cols - c - kDepth, 64 * kWaves);
-            __syncthreads();
-            multiply<FT, FR>(x1 + wt * kDepth, w1 + wr * kDepth, acc);
+#pragma unroll
+        for (int f = 0; f < kF; f++) read(even, x0, w0, 0, f);
+        for (uint32_t s = 0; s < stages; s += NB) {
+            stage(x0, w0, x1, w1, s);
+            if constexpr (NB == 2) {
+                stage(x1, w1, x0, w0, s + 1);
+            } else {
+                stage(x1, w1, x2, w2, s + 1);
+                if constexpr (NB == 3) {
+                    stage(x2, w2, x0, w0, s + 2);
+                } else {
+                    stage(x2, w2, x3, w3, s + 2);
+                    if constexpr (NB == 4) {
+                        stage(x3, w3, x0, w0, s + 3);
+                    } else {
+                        stage(x3, w3, x4, w4, s + 3);
+                        if constexpr (NB == 5) {
+                            stage(x4, w4, x0, w0, s + 4);
+                        } else {
+                            stage(x4, w4, x5, w5, s + 4);
+                            stage(x5, w5, x0, w0, s + 5);
+                        }
+                    }
+                }
+            }
         }
     }
 
-    // lane l holds row l % 32 of each product, element e token 8 (e / 4) + 4 (l / 32) + e % 4
+    // Lane l holds token l % 32 of each product, element e row 8 (e / 4) +
+    // 4 (l / 32) + e % 4.  The results pass through LDS (the stages' buffers are
+    // free once the last loads, of zeros, have come), 128 bytes of each of 32
+    // tokens at a time, so that a token's rows leave in whole cache lines.
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
+    __syncthreads();
+    constexpr int kRows = std::min<int>(128 / sizeof(Y), 32 * FR), kParts = kRows / 32;
+    constexpr uint32_t kBytes = kRows * sizeof(Y), kPitch = kBytes + 16;  // tokens in different banks
+    constexpr uint32_t kX = BT * kDepth / (32 * kPitch), kW = BR * kDepth / (32 * kPitch);
+    static_assert(FR % kParts == 0, "whole rows of results");
+    constexpr bool kOwn = kWaves > int(2 * kX + kW);  // small buffers: memory of its own
+    __shared__ __align__(16) int8_t results[kOwn ? kWaves * 32 * kPitch : 16];
+    int8_t *out = kOwn ? results + wave * (32 * kPitch)
+                       : (wave < kX ? x0 : wave < 2 * kX ? x1 : w0) +
+                             (wave < 2 * kX ? wave % std::max(kX, 1u) : wave - 2 * kX) * (32 * kPitch);
     Y *y = static_cast<Y *>(a.y[k]);
+    typedef Y Y4 __attribute__((ext_vector_type(4)));
+    typedef Y Y16B __attribute__((ext_vector_type(16 / sizeof(Y))));
+    typedef Y16B Y16B_any __attribute__((aligned(sizeof(Y))));
+    float xs[FT];
 #pragma unroll
-    for (int h = 0; h < FR; h++) {
-        const uint32_t r = r0 + wr + 32 * h + (lane & 31u);
-        if (r >= rows) continue;
-        const float s = a.w_scale[k][r];
+    for (int f = 0; f < FT; f++)
+        xs[f] = a.x_scale[k][min(t0 + wt + 32 * f + (lane & 31u), a.n_tokens - 1)];
 #pragma unroll
-        for (int f = 0; f < FT; f++) {
+    for (int f = 0; f < FT; f++) {
 #pragma unroll
-            for (int e = 0; e < 16; e++) {
-                const uint32_t t = t0 + wt + 32 * f + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
-                if (t < a.n_tokens) put(y, t * a.y_stride[k] + r, acc[f][h][e], a.x_scale[k][t], s);
+        for (int h0 = 0; h0 < FR; h0 += kParts) {
+#pragma unroll
+            for (int h = h0; h < h0 + kParts; h++) {
+#pragma unroll
+                for (int g = 0; g < 4; g++) {
+                    const uint32_t r = 8 * g + 4 * (lane >> 5);
+                    const float4 ws = *reinterpret_cast<const float4 *>(&w_scale[wr + 32 * h + r]);
+                    Y4 v;
+#pragma unroll
+                    for (int e = 0; e < 4; e++) v[e] = Y(scaled(acc[f][h][4 * g + e], xs[f], (&ws.x)[e]));
+                    *reinterpret_cast<Y4 *>(out + (lane & 31u) * kPitch +
+                                            (32 * (h - h0) + r) * sizeof(Y)) = v;
+                }
+            }
+            // a wave's LDS operations take effect in order: no barrier
+            constexpr uint32_t kLanes = kBytes / 16;  // of a token
+            const uint32_t chunk = lane % kLanes, r = r0 + wr + 32 * h0 + chunk * (16 / sizeof(Y));
+#pragma unroll
+            for (uint32_t p = 0; p < kLanes / 2; p++) {
+                const uint32_t i = 64 / kLanes * p + lane / kLanes, tok = t0 + wt + 32 * f + i;
+                const Y16B v = *reinterpret_cast<const Y16B *>(out + i * kPitch + chunk * 16);
+                if (tok >= a.n_tokens) continue;
+                Y *to = y + tok * a.y_stride[k] + r;
+                if (r + 16 / sizeof(Y) <= rows) {
+                    *reinterpret_cast<Y16B_any *>(to) = v;
+                } else {
+#pragma unroll
+                    for (uint32_t e = 0; e < 16 / sizeof(Y) - 1; e++)
+                        if (r + e < rows) to[e] = v[e];
+                }
             }
         }
     }
@@ -435,31 +547,63 @@ int status(hipError_t e) { return e == hipSuccess ? DF11_OK : DF11_E_HIP; }
 
 uint32_t type_bytes(uint32_t type) { return type == DF11_TYPE_F32 ? 4 : 2; }
 
-template <class Y, int BT, int BR, int WT, int WR>
+template <class Y, int BT, int BR, int WT, int WR, int NB>
 int run_tiles(GemmArgs &a, uint32_t n, hipStream_t st) {
     const uint32_t token_tiles = (a.n_tokens + BT - 1) / BT;
-    uint64_t tiles = 0;
+    uint64_t turns = 0;
     for (uint32_t k = 0; k < n; k++) {
-        a.first[k] = uint32_t(tiles);
-        tiles += uint64_t((a.rows[k] + BR - 1) / BR) * token_tiles;
-        if (tiles > 0x7FFFFFFFu) return DF11_E_INVALID;
+        a.first[k] = uint32_t(turns);
+        turns += (uint64_t((a.rows[k] + BR - 1) / BR) * token_tiles + 7) / 8;
+        if (turns > 0x0FFFFFFFu) return DF11_E_INVALID;
     }
-    return status(launch(gemm_tile<Y, BT, BR, WT, WR>, dim3(uint32_t(tiles)), dim3(64 * WT * WR), 0, st,
-                         a, token_tiles, uint32_t(tiles)));
+    return status(launch(gemm_tile<Y, BT, BR, WT, WR, NB>, dim3(uint32_t(turns) * 8), dim3(64 * WT * WR), 0,
+                         st, a, token_tiles));
+}
+
+// How long the tiles of BT x BR take, in microseconds: all compute units
+// together, or the longest tile alone (stages of 128 columns; 3 more for a
+// tile's start and end).
+float tiles_time(const GemmArgs &a, uint32_t n, uint32_t bt, uint32_t br, float busy, float alone) {
+    const uint64_t token_tiles = (a.n_tokens + bt - 1) / bt;
+    uint64_t stages = 0;
+    uint32_t longest = 0;
+    for (uint32_t k = 0; k < n; k++) {
+        const uint32_t s = (a.cols[k] + kDepth - 1) / kDepth + 3;
+        stages += (a.rows[k] + br - 1) / br * token_tiles * s;
+        longest = std::max(longest, s);
+    }
+    return std::max(float(stages) / 256 * busy, float(longest) * alone);
 }
 
 template <class Y>
 int run_gemm(GemmArgs &a, uint32_t n, hipStream_t st) {
-    if (a.n_tokens > 64) return run_tiles<Y, 256, 256, 2, 4>(a, n, st);
-    uint32_t tiles = 0;
-    for (uint32_t k = 0; k < n; k++) {
-        a.first[k] = tiles;
-        tiles += (a.rows[k] + 15) / 16;
+    if (a.n_tokens <= 32) {
+        // Workgroups of 16 rows are the faster form for one token, and up to 16
+        // where they are no more than the compute units (4096 x 4096: 7.2 us
+        // against 9.6 with 1 token, 8.4 against 10.4 with 16); more of them
+        // read too much of the activations (8B block: 43.4 against 48.0 us
+        // with 1 token, but 48.4 against 48.6 with 4 and 66 against 51 with 16).
+        uint32_t tiles = 0;
+        for (uint32_t k = 0; k < n; k++) {
+            a.first[k] = tiles;
+            tiles += (a.rows[k] + 15) / 16;
+        }
+        if (a.n_tokens == 1 || (a.n_tokens <= 16 && tiles <= 256))
+            return status(launch(gemm_rows16<Y>, dim3(tiles), dim3(64 * kRowWaves), 0, st, a));
+        return run_tiles<Y, 32, 64, 1, 2, 6>(a, n, st);
     }
-    const uint32_t t = a.n_tokens;
-    if (t <= 16) return status(launch(gemm_rows16<Y, 1>, dim3(tiles), dim3(256), 0, st, a));
-    if (t <= 32) return status(launch(gemm_rows16<Y, 2>, dim3(tiles), dim3(256), 0, st, a));
-    return status(launch(gemm_rows16<Y, 4>, dim3(tiles, (t + 63) / 64), dim3(256), 0, st, a));
+    // The tile with the least time by tiles_time, whose rates are those measured
+    // with the chip full (busy, per stage and compute unit) and with one
+    // workgroup per compute unit (alone).
+    const float t64 = tiles_time(a, n, 64, 64, 0.235f, 0.25f);
+    const float t128 = tiles_time(a, n, 128, 128, 0.61f, 0.55f);
+    const float t256x128 = tiles_time(a, n, 256, 128, 1.0f, 0.85f);
+    const float t256 = tiles_time(a, n, 256, 256, 1.78f, 1.25f);
+    const float least = std::min(std::min(t64, t128), std::min(t256x128, t256));
+    if (least == t64) return run_tiles<Y, 64, 64, 2, 2, 4>(a, n, st);
+    if (least == t128) return run_tiles<Y, 128, 128, 4, 2, 4>(a, n, st);
+    if (least == t256x128) return run_tiles<Y, 256, 128, 4, 2, 3>(a, n, st);
+    return run_tiles<Y, 256, 256, 2, 4, 2>(a, n, st);
 }
 
 }  // namespace
@@ -505,10 +649,14 @@ int df11_gemm_int8(uint32_t y_type, const df11_int8_tensor *t, uint32_t n_tensor
     if ((n_tensors && !t) || n_tensors > kMax || y_type > DF11_TYPE_F16) return DF11_E_INVALID;
     if (n_tokens > (1u << 20)) return DF11_E_INVALID;
     GemmArgs a{};
-    uint32_t used = 0;
+    uint32_t used = 0, order[kMax];
     for (uint32_t &f : a.first) f = 0xFFFFFFFFu;
+    // the matrices of the longest rows first, so that the last workgroups are short ones
+    for (uint32_t k = 0; k < n_tensors; k++) order[k] = k;
+    std::stable_sort(order, order + n_tensors,
+                     [t](uint32_t i, uint32_t j) { return t[i].cols > t[j].cols; });
     for (uint32_t k = 0; k < n_tensors; k++) {
-        const df11_int8_tensor &x = t[k];
+        const df11_int8_tensor &x = t[order[k]];
         if (x.cols > DF11_INT8_MAX_COLS || x.rows > (1u << 24)) return DF11_E_INVALID;
         if (!x.rows || !n_tokens) continue;
         if (!x.w_scale || !x.x_scale || !x.y || !aligned(x.w_scale, 4) || !aligned(x.x_scale, 4) ||
