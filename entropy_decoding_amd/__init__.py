@@ -290,8 +290,14 @@ def _load():
                                      ctypes.c_uint32, vp]
     L.df11_gemm_int8.argtypes = [ctypes.c_uint32, ctypes.POINTER(df11_int8_tensor),
                                  ctypes.c_uint32, ctypes.c_uint32, vp]
+    L.df11_linear_int8_scratch_bytes.argtypes = [ctypes.POINTER(df11_int8_tensor), ctypes.c_uint32,
+                                                 ctypes.c_uint32]
+    L.df11_linear_int8_scratch_bytes.restype = ctypes.c_uint64
+    L.df11_linear_int8.argtypes = [ctypes.c_uint32, ctypes.c_uint32,
+                                   ctypes.POINTER(df11_int8_tensor), ctypes.c_uint32,
+                                   ctypes.c_uint32, vp, ctypes.c_uint64, vp]
     for f in (L.df11_build_codebook, L.df11_encode_size, L.df11_encode,
-              L.df11_quantize_int8, L.df11_gemm_int8, L.df11_adamw_step, L.df11_adamw_values, L.df11_grad_norm,
+              L.df11_quantize_int8, L.df11_gemm_int8, L.df11_linear_int8, L.df11_adamw_step, L.df11_adamw_values, L.df11_grad_norm,
               L.df11_build_codebook_fmt, L.df11_encode_size_fmt, L.df11_encode_fmt,
               L.df11_decompress_block, L.df11_decompress_tensor, L.df11_pipeline_create,
               L.df11_pipeline_destroy, L.df11_pipeline_decompress, L.df11_pipeline_acquire,
@@ -885,7 +891,7 @@ def quantize_int8(tensors, stream=None):
 class Int8Linear:
     """The matrices of a block as 8-bit integers with a scale for each output
     channel, multiplied with activations that are quantised token by token
-    (df11_quantize_int8, then df11_gemm_int8: two launches a call).
+    (df11_linear_int8: two launches a call).
 
     ``codes``: int8 device tensors [rows, stride], 16-byte aligned with strides
     that are multiples of 16; ``scales``: float32 [rows]; ``shapes``: (rows,
@@ -901,6 +907,7 @@ class Int8Linear:
         if not len(self.codes) == len(self.scales) == len(self.shapes):
             raise ValueError("one codes tensor, scales tensor and shape per matrix")
         self._t = (df11_int8_tensor * len(self.codes))()
+        self._bytes = {}  # scratch for a number of tokens
         for a, q, s, (r, c) in zip(self._t, self.codes, self.scales, self.shapes):
             if q.dtype != torch.int8 or q.size(0) != r or q.size(1) < c or (r > 1 and q.stride(0) < c):
                 raise ValueError("codes must be int8 of the shape's rows and at least its columns")
@@ -929,7 +936,7 @@ class Int8Linear:
         guard, st = _on(ds.stream.device, stream)
         with guard:
             unit = torch.empty(ds.n_weights, dtype=torch.bfloat16, device=ds.stream.device)
-            df11_decompress_block(ds, unit, status, st.value or 0)
+            df11_decompress_block(ds, unit, status, st)
             parts = unit.split([r * c for r, c in shapes])
             held = _quantize(_matrices([p.view(s) for p, s in zip(parts, shapes)], "matrices"), st)
         return cls([q for q, _ in held], [s for _, s in held], shapes)
@@ -941,47 +948,67 @@ class Int8Linear:
         float32) per matrix; a tensor given for several is quantised once."""
         import torch
 
-        xs = _matrices(xs, "activations")
         if len(xs) != len(self.shapes):
             raise ValueError("one activation tensor per matrix")
-        if xs[0].device != self.device:
-            raise ValueError(f"activations must be on {self.device}")
-        n_tokens = xs[0].size(0)
-        for x, (_, c) in zip(xs, self.shapes):
-            if x.size(0) != n_tokens or x.size(1) != c:
+        first = xs[0]
+        if first.dim() != 2 or first.device != self.device:
+            raise ValueError(f"activations must be 2-D tensors on {self.device}")
+        n_tokens, kind = first.size(0), first.dtype
+        if out is not None:
+            out = _matrices(out, "outputs")
+            if out[0].device != self.device or [tuple(y.shape) for y in out] != [
+                    (n_tokens, r) for r, _ in self.shapes] or out_dtype not in (None, out[0].dtype):
+                raise ValueError("outputs must be [n_tokens, rows] of their matrix")
+            out_dtype = out[0].dtype
+        elif out_dtype is None:
+            out_dtype = torch.bfloat16
+        x_type, y_type = _type(kind), _type(out_dtype)
+        n = len(self.shapes)
+        t = (df11_int8_tensor * n).from_buffer_copy(self._t)
+        last = None
+        for a, x, (_, c) in zip(t, xs, self.shapes):
+            if x is not last:
+                if x.shape != (n_tokens, c) or x.dtype != kind or x.device != self.device:
+                    raise ValueError("activations must be [n_tokens, cols] of their matrix, of one "
+                                     f"type, on {self.device}")
+                strides = x.stride()
+                if (strides[1] != 1 and c > 1) or strides[0] < 0:
+                    raise ValueError("activations must have contiguous rows")
+                last, p, stride = x, x.data_ptr(), strides[0]
+            elif c != last.size(1):
                 raise ValueError("activations must be [n_tokens, cols] of their matrix")
+            a.x, a.x_stride = p, stride
         guard, st = _on(self.device, stream)
         with guard:
             if out is None:
-                kind = torch.bfloat16 if out_dtype is None else out_dtype
-                out = [torch.empty((n_tokens, r), dtype=kind, device=self.device)
-                       for r, _ in self.shapes]
-            else:
-                out = _matrices(out, "outputs")
-                kind = out[0].dtype
-                if out[0].device != self.device or [tuple(y.shape) for y in out] != [
-                        (n_tokens, r) for r, _ in self.shapes] or out_dtype not in (None, kind):
-                    raise ValueError("outputs must be [n_tokens, rows] of their matrix")
-            y_type = _type(kind)
-            unique = {id(x): x for x in xs}
-            held = dict(zip(unique, _quantize(list(unique.values()), st)))
-            t = (df11_int8_tensor * len(xs)).from_buffer_copy(self._t)
-            for a, x, y in zip(t, xs, out):
-                q, s = held[id(x)]
-                a.x, a.x_scale, a.y = q.data_ptr(), s.data_ptr(), y.data_ptr()
-                a.x_stride, a.y_stride = q.size(1), max(y.stride(0), y.size(1)) if n_tokens < 2 else y.stride(0)
-            _check("df11_gemm_int8", LIB.df11_gemm_int8(y_type, t, len(t), n_tokens, st))
+                out = [first.new_empty((n_tokens, r), dtype=out_dtype) for r, _ in self.shapes]
+            for a, y in zip(t, out):
+                a.y = y.data_ptr()
+                a.y_stride = y.stride(0) if n_tokens > 1 else y.size(1)
+            need = self._bytes.get(n_tokens)
+            if need is None:
+                need = self._bytes[n_tokens] = int(
+                    LIB.df11_linear_int8_scratch_bytes(self._t, n, n_tokens))
+            scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
+            _check("df11_linear_int8",
+                   LIB.df11_linear_int8(x_type, y_type, t, n, n_tokens, scratch.data_ptr(), need, st))
         return out
 
 
 # ---------------------------------------------------------------- optimiser step
 
 
+_TYPE_OF = {}  # torch's types, filled when first seen
+
+
 def _type(dtype) -> int:
-    name = str(dtype).replace("torch.", "")
-    if name not in TYPES:
-        raise TypeError(f"no operator for {dtype}")
-    return TYPES[name]
+    kind = _TYPE_OF.get(dtype)
+    if kind is None:
+        name = str(dtype).replace("torch.", "")
+        if name not in TYPES:
+            raise TypeError(f"no operator for {dtype}")
+        kind = _TYPE_OF[dtype] = TYPES[name]
+    return kind
 
 
 def _same(tensors, what, dtype=None, sizes=None, device=None):
@@ -1000,19 +1027,32 @@ def _same(tensors, what, dtype=None, sizes=None, device=None):
     return tensors
 
 
+class _AsIs:
+    """No guard: device and stream are current already."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *_):
+        return False
+
+
+_AS_IS = _AsIs()
+
+
 def _on(device, stream):
     """(a guard that makes ``stream``, or the device's current stream, and the
     device current; the stream's handle)."""
     import torch
 
     if stream is None:
-        return torch.cuda.device(device), ctypes.c_void_p(
-            torch.cuda.current_stream(device).cuda_stream)
+        guard = _AS_IS if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        return guard, torch._C._cuda_getCurrentRawStream(device.index)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
     if stream.device != device:
         raise ValueError(f"the stream is not on {device}")
-    return torch.cuda.stream(stream), ctypes.c_void_p(stream.cuda_stream)
+    return torch.cuda.stream(stream), stream.cuda_stream
 
 
 class AdamW:
@@ -1090,15 +1130,19 @@ class AdamW:
 
     def grad_norm(self, max_norm: float, stream=None):
         """A float32 device tensor [norm, clip factor] of all gradients together."""
+        guard, st = _on(self.device, stream)
+        with guard:
+            return self._norm(max_norm, st)
+
+    def _norm(self, max_norm, st):
         import torch
 
-        guard, st = _on(self.device, stream)
-        with guard:  # memory of the stream that uses it: its reuse is ordered there
-            out = torch.empty(2, dtype=torch.float32, device=self.device)
-            scratch = torch.empty(self._norm_bytes, dtype=torch.uint8, device=self.device)
-            _check("df11_grad_norm",
-                   LIB.df11_grad_norm(self._c.g_type, self._t, len(self._t), float(max_norm),
-                                      out.data_ptr(), scratch.data_ptr(), self._norm_bytes, st))
+        # memory of the stream that uses it: its reuse is ordered there
+        out = torch.empty(2, dtype=torch.float32, device=self.device)
+        scratch = torch.empty(self._norm_bytes, dtype=torch.uint8, device=self.device)
+        _check("df11_grad_norm",
+               LIB.df11_grad_norm(self._c.g_type, self._t, len(self._t), float(max_norm),
+                                  out.data_ptr(), scratch.data_ptr(), self._norm_bytes, st))
         return out
 
     def step(self, lr=None, max_norm=None, grad_factor=None, stream=None):
@@ -1109,9 +1153,6 @@ class AdamW:
         a factor that is not finite leaves everything as it was."""
         if max_norm is not None and grad_factor is not None:
             raise ValueError("max_norm or grad_factor")
-        norm = None if max_norm is None else self.grad_norm(max_norm, stream)
-        if norm is not None:
-            grad_factor = norm[1:]
         c = self._c
         by_tensor = hasattr(lr, "data_ptr")
         for x, what in ((grad_factor, "grad_factor"), (lr if by_tensor else None, "lr")):
@@ -1119,10 +1160,14 @@ class AdamW:
                 raise ValueError(f"{what} must be one float32 on {self.device}")
         c.lr = self.lr if lr is None or by_tensor else float(lr)
         c.d_lr = lr.data_ptr() if by_tensor else None
-        c.d_grad_factor = None if grad_factor is None else grad_factor.data_ptr()
         c.step = self.steps + 1
         guard, st = _on(self.device, stream)
+        norm = None
         with guard:
+            c.d_grad_factor = None if grad_factor is None else grad_factor.data_ptr()
+            if max_norm is not None:
+                norm = self._norm(max_norm, st)
+                c.d_grad_factor = norm.data_ptr() + 4
             if self.d_step is not None:
                 self.d_step += 1
                 c.d_step = self.d_step.data_ptr()

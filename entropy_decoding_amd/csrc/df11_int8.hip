@@ -606,6 +606,46 @@ int run_gemm(GemmArgs &a, uint32_t n, hipStream_t st) {
     return run_tiles<Y, 256, 256, 2, 4, 2>(a, n, st);
 }
 
+// Checks the product's arguments and fills the kernels' (used: the matrices with work).
+int prepare_gemm(uint32_t y_type, const df11_int8_tensor *t, uint32_t n_tensors, uint32_t n_tokens,
+                 GemmArgs &a, uint32_t &used) {
+    if ((n_tensors && !t) || n_tensors > kMax || y_type > DF11_TYPE_F16) return DF11_E_INVALID;
+    if (n_tokens > (1u << 20)) return DF11_E_INVALID;
+    uint32_t order[kMax];
+    for (uint32_t &f : a.first) f = 0xFFFFFFFFu;
+    // the matrices of the longest rows first, so that the last workgroups are short ones
+    for (uint32_t k = 0; k < n_tensors; k++) order[k] = k;
+    std::stable_sort(order, order + n_tensors,
+                     [t](uint32_t i, uint32_t j) { return t[i].cols > t[j].cols; });
+    for (uint32_t k = 0; k < n_tensors; k++) {
+        const df11_int8_tensor &x = t[order[k]];
+        if (x.cols > DF11_INT8_MAX_COLS || x.rows > (1u << 24)) return DF11_E_INVALID;
+        if (!x.rows || !n_tokens) continue;
+        if (!x.w_scale || !x.x_scale || !x.y || !aligned(x.w_scale, 4) || !aligned(x.x_scale, 4) ||
+            !aligned(x.y, type_bytes(y_type)) || x.y_stride < x.rows || x.y_stride >> 40)
+            return DF11_E_INVALID;
+        if (x.cols && (!x.w || !x.x || !aligned(x.w, 16) || !aligned(x.x, 16) || x.w_stride % 16 ||
+                       x.x_stride % 16 || x.w_stride < x.cols || x.x_stride < x.cols ||
+                       x.w_stride > DF11_INT8_MAX_STRIDE || x.x_stride > DF11_INT8_MAX_STRIDE))
+            return DF11_E_INVALID;
+        a.w[used] = x.w, a.w_scale[used] = x.w_scale, a.x[used] = x.x, a.x_scale[used] = x.x_scale;
+        a.y[used] = x.y, a.y_stride[used] = x.y_stride;
+        a.w_stride[used] = uint32_t(x.w_stride), a.x_stride[used] = uint32_t(x.x_stride);
+        a.rows[used] = x.rows, a.cols[used] = x.cols;
+        used++;
+    }
+    a.n_tokens = n_tokens;
+    return DF11_OK;
+}
+
+int launch_gemm(uint32_t y_type, GemmArgs &a, uint32_t used, hipStream_t st) {
+    switch (y_type) {
+    case DF11_TYPE_F32: return run_gemm<float>(a, used, st);
+    case DF11_TYPE_BF16: return run_gemm<__bf16>(a, used, st);
+    default: return run_gemm<_Float16>(a, used, st);
+    }
+}
+
 }  // namespace
 
 extern "C" {
@@ -646,40 +686,56 @@ int df11_quantize_int8(uint32_t src_type, const df11_int8_rows *m, uint32_t n,
 
 int df11_gemm_int8(uint32_t y_type, const df11_int8_tensor *t, uint32_t n_tensors,
                    uint32_t n_tokens, df11_hip_stream stream) {
-    if ((n_tensors && !t) || n_tensors > kMax || y_type > DF11_TYPE_F16) return DF11_E_INVALID;
-    if (n_tokens > (1u << 20)) return DF11_E_INVALID;
     GemmArgs a{};
-    uint32_t used = 0, order[kMax];
-    for (uint32_t &f : a.first) f = 0xFFFFFFFFu;
-    // the matrices of the longest rows first, so that the last workgroups are short ones
-    for (uint32_t k = 0; k < n_tensors; k++) order[k] = k;
-    std::stable_sort(order, order + n_tensors,
-                     [t](uint32_t i, uint32_t j) { return t[i].cols > t[j].cols; });
+    uint32_t used = 0;
+    const int rc = prepare_gemm(y_type, t, n_tensors, n_tokens, a, used);
+    return rc == DF11_OK && used ? launch_gemm(y_type, a, used, static_cast<hipStream_t>(stream)) : rc;
+}
+
+uint64_t df11_linear_int8_scratch_bytes(const df11_int8_tensor *t, uint32_t n_tensors,
+                                        uint32_t n_tokens) {
+    uint64_t bytes = 16;
+    for (uint32_t k = 0; t && k < n_tensors; k++)
+        bytes += n_tokens * ((uint64_t(t[k].cols) + 15) / 16 * 16) + (uint64_t(n_tokens) * 4 + 15) / 16 * 16;
+    return bytes;
+}
+
+int df11_linear_int8(uint32_t x_type, uint32_t y_type, const df11_int8_tensor *t,
+                     uint32_t n_tensors, uint32_t n_tokens, void *scratch, uint64_t scratch_bytes,
+                     df11_hip_stream stream) {
+    if ((n_tensors && !t) || n_tensors > kMax || n_tokens > (1u << 20)) return DF11_E_INVALID;
+    if (!scratch || !aligned(scratch, 16) ||
+        scratch_bytes < df11_linear_int8_scratch_bytes(t, n_tensors, n_tokens))
+        return DF11_E_INVALID;
+    df11_int8_rows rows[kMax];
+    df11_int8_tensor q[kMax];
+    uint32_t n_rows = 0;
+    int8_t *at = static_cast<int8_t *>(scratch);
     for (uint32_t k = 0; k < n_tensors; k++) {
-        const df11_int8_tensor &x = t[order[k]];
-        if (x.cols > DF11_INT8_MAX_COLS || x.rows > (1u << 24)) return DF11_E_INVALID;
-        if (!x.rows || !n_tokens) continue;
-        if (!x.w_scale || !x.x_scale || !x.y || !aligned(x.w_scale, 4) || !aligned(x.x_scale, 4) ||
-            !aligned(x.y, type_bytes(y_type)) || x.y_stride < x.rows || x.y_stride >> 40)
-            return DF11_E_INVALID;
-        if (x.cols && (!x.w || !x.x || !aligned(x.w, 16) || !aligned(x.x, 16) || x.w_stride % 16 ||
-                       x.x_stride % 16 || x.w_stride < x.cols || x.x_stride < x.cols ||
-                       x.w_stride > DF11_INT8_MAX_STRIDE || x.x_stride > DF11_INT8_MAX_STRIDE))
-            return DF11_E_INVALID;
-        a.w[used] = x.w, a.w_scale[used] = x.w_scale, a.x[used] = x.x, a.x_scale[used] = x.x_scale;
-        a.y[used] = x.y, a.y_stride[used] = x.y_stride;
-        a.w_stride[used] = uint32_t(x.w_stride), a.x_stride[used] = uint32_t(x.x_stride);
-        a.rows[used] = x.rows, a.cols[used] = x.cols;
-        used++;
+        if (t[k].cols > DF11_INT8_MAX_COLS) return DF11_E_INVALID;
+        uint32_t j = 0;
+        while (j < n_rows && (rows[j].src != t[k].x || rows[j].src_stride != t[k].x_stride ||
+                              rows[j].cols != t[k].cols))
+            j++;
+        if (j == n_rows) {
+            df11_int8_rows &r = rows[n_rows++];
+            r.src = t[k].x, r.src_stride = t[k].x_stride;
+            r.rows = n_tokens, r.cols = t[k].cols;
+            r.code_stride = (uint64_t(r.cols) + 15) / 16 * 16;
+            r.codes = at;
+            at += n_tokens * r.code_stride;
+            r.scales = reinterpret_cast<float *>(at);
+            at += (uint64_t(n_tokens) * 4 + 15) / 16 * 16;
+        }
+        q[k] = t[k];
+        q[k].x = rows[j].codes, q[k].x_scale = rows[j].scales, q[k].x_stride = rows[j].code_stride;
     }
-    if (!used) return DF11_OK;
-    a.n_tokens = n_tokens;
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    switch (y_type) {
-    case DF11_TYPE_F32: return run_gemm<float>(a, used, st);
-    case DF11_TYPE_BF16: return run_gemm<__bf16>(a, used, st);
-    default: return run_gemm<_Float16>(a, used, st);
-    }
+    // the product's arguments are checked before the first launch
+    GemmArgs a{};
+    uint32_t used = 0;
+    int rc = prepare_gemm(y_type, q, n_tensors, n_tokens, a, used);
+    if (rc == DF11_OK) rc = df11_quantize_int8(x_type, rows, n_rows, stream);
+    return rc == DF11_OK && used ? launch_gemm(y_type, a, used, static_cast<hipStream_t>(stream)) : rc;
 }
 
 }  // extern "C"

@@ -723,6 +723,23 @@ typedef struct df11_int8_tensor {
 int df11_gemm_int8(uint32_t y_type, const df11_int8_tensor *t, uint32_t n_tensors,
                    uint32_t n_tokens, df11_hip_stream st);
 
+/*
+ * df11_linear_int8: both of the above for activations of x_type (x and
+ * x_stride in elements of that type, rows contiguous, element alignment;
+ * x_scale is not used): the tokens' rows are quantised into scratch, matrices
+ * that name the same x (pointer, x_stride and cols) sharing the codes, and
+ * multiplied.  scratch: device, 16-byte aligned, at least
+ * df11_linear_int8_scratch_bytes(t, n_tensors, n_tokens) bytes (enough however
+ * the matrices share), not shared by calls that may overlap; no
+ * initialisation needed.  Two launches on st.  Errors as df11_gemm_int8, and
+ * DF11_E_INVALID for x_type and the scratch.
+ */
+uint64_t df11_linear_int8_scratch_bytes(const df11_int8_tensor *t, uint32_t n_tensors,
+                                        uint32_t n_tokens);
+int df11_linear_int8(uint32_t x_type, uint32_t y_type, const df11_int8_tensor *t,
+                     uint32_t n_tensors, uint32_t n_tokens, void *scratch, uint64_t scratch_bytes,
+                     df11_hip_stream st);
+
 #ifdef __cplusplus
 }
 #endif

@@ -81,6 +81,34 @@ def test_product_of_nothing():
     assert L.df11_gemm_int8(1, tensor(rows=0, w=0, y=0), 1, 5, None) == ed.DF11_OK
 
 
+def linear(t, n=1, x_kind=1, y_kind=1, tokens=5, scratch=4096, nbytes=1 << 20):
+    return L.df11_linear_int8(x_kind, y_kind, t, n, tokens, scratch, nbytes, None)
+
+
+@pytest.mark.parametrize("change", [
+    {"w": 0}, {"w": 4104}, {"x": 0}, {"x": 16385}, {"w_scale": 0}, {"y": 0}, {"y": 65537},
+    {"w_stride": 40}, {"x_stride": 39}, {"x_stride": 1 << 41}, {"y_stride": 19}, {"cols": 131072},
+    {"rows": (1 << 24) + 1}])
+def test_linear_refuses(change):
+    assert linear(tensor(**change)) == ed.DF11_E_INVALID
+
+
+def test_linear_refuses_scratch_and_types():
+    need = L.df11_linear_int8_scratch_bytes(tensor(), 1, 5)
+    assert need >= 5 * 48 + 5 * 4
+    for change in ({"scratch": 0}, {"scratch": 4104}, {"nbytes": need - 1}, {"x_kind": 3},
+                   {"y_kind": 3}, {"tokens": (1 << 20) + 1}):
+        assert linear(tensor(), **change) == ed.DF11_E_INVALID
+    assert linear(None) == ed.DF11_E_INVALID
+    many = (ed.df11_int8_tensor * 17)(*[tensor()[0]] * 17)
+    assert linear(many, 17) == ed.DF11_E_INVALID
+
+
+def test_linear_of_nothing():
+    assert linear(None, 0) == ed.DF11_OK
+    assert linear(tensor(), tokens=0) == ed.DF11_OK
+
+
 def test_structs_match_the_header(tmp_path):
     kinds = ("df11_int8_rows", "df11_int8_tensor")
     fields = {s: [f for f, _ in getattr(ed, s)._fields_] for s in kinds}
