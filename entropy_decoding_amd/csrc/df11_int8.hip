@@ -65,49 +65,38 @@ struct Quotient<float> {
     }
 };
 
-struct QuantArgs {
-    const void *src[kMax];
-    int8_t *codes[kMax];
-    float *scales[kMax];
-    uint64_t src_stride[kMax], code_stride[kMax];
-    uint32_t cols[kMax];
-    uint32_t first[kMax];  // a matrix's first row in the grid; 0xFFFFFFFF past the last
-};
-
-// One workgroup per row: the largest magnitude (as bits, so that a NaN or an
-// infinity shows), then the codes; the row comes from the caches the second time.
+// The largest magnitude of x[c .. c + 8), as bits, so that a NaN or an infinity shows.
 template <class T>
-__global__ __launch_bounds__(kThreads) void quantize_rows(QuantArgs a) {
-    __shared__ uint32_t top_s[kThreads / 64];
-    uint32_t k = 0;
-#pragma unroll
-    for (int j = 1; j < kMax; j++) k += uint32_t(blockIdx.x >= a.first[j]);
-    const uint32_t row = blockIdx.x - a.first[k], cols = a.cols[k];
-    const T *x = static_cast<const T *>(a.src[k]) + row * a.src_stride[k];
-    int8_t *q = a.codes[k] + row * a.code_stride[k];
-
+__device__ __forceinline__ uint32_t row_top(const T *x, uint32_t c, uint32_t cols) {
     uint32_t top = 0;
-    for (uint32_t c = threadIdx.x * 8; c < cols; c += kThreads * 8) {
-        if (c + 8 <= cols) {
-            const Eight<T> v = *reinterpret_cast<const Eight<T> *>(x + c);
+    if (c + 8 <= cols) {
+        const Eight<T> v = *reinterpret_cast<const Eight<T> *>(x + c);
 #pragma unroll
-            for (int e = 0; e < 8; e++) top = max(top, __float_as_uint(to_f32(v.e[e])) & 0x7FFFFFFFu);
-        } else {
-            for (uint32_t e = c; e < cols; e++) top = max(top, __float_as_uint(to_f32(x[e])) & 0x7FFFFFFFu);
-        }
+        for (int e = 0; e < 8; e++) top = max(top, __float_as_uint(to_f32(v.e[e])) & 0x7FFFFFFFu);
+    } else {
+        for (uint32_t e = c; e < cols; e++) top = max(top, __float_as_uint(to_f32(x[e])) & 0x7FFFFFFFu);
     }
+    return top;
+}
+
+__device__ __forceinline__ uint32_t wave_top(uint32_t top) {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) top = max(top, uint32_t(__shfl_xor(int(top), d, 64)));
-    if ((threadIdx.x & 63u) == 0) top_s[threadIdx.x >> 6] = top;
-    __syncthreads();
-    top = max(max(top_s[0], top_s[1]), max(top_s[2], top_s[3]));
+    return top;
+}
 
-    const float amax = __uint_as_float(top);
-    const bool bad = top >= 0x7F800000u, zero = bad || top == 0;
-    if (threadIdx.x == 0)
-        a.scales[k][row] = bad ? __uint_as_float(0x7FC00000u) : amax / 127.0f;
-    const Quotient<T> code(zero ? 1.0f : amax);
-    for (uint32_t c = threadIdx.x * 8; c < ((cols + 15) & ~15u); c += kThreads * 8) {
+// What a row's largest magnitude says about its codes.
+template <class T>
+struct Row {
+    bool zero;
+    float scale;
+    Quotient<T> code;
+    __device__ explicit Row(uint32_t top)
+        : zero(top == 0 || top >= 0x7F800000u),
+          scale(top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(top) / 127.0f),
+          code(zero ? 1.0f : __uint_as_float(top)) {}
+    // the codes of x[c .. c + 8), zeros from cols on
+    __device__ __forceinline__ u32x2 codes(const T *x, uint32_t c, uint32_t cols) const {
         float v[8];
         if (c + 8 <= cols) {
             const Eight<T> e = *reinterpret_cast<const Eight<T> *>(x + c);
@@ -122,8 +111,39 @@ __global__ __launch_bounds__(kThreads) void quantize_rows(QuantArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; i++) out[i / 4] |= (uint32_t(int(code(v[i]))) & 0xFFu) << (8 * (i % 4));
         }
-        *reinterpret_cast<u32x2 *>(q + c) = out;
+        return out;
     }
+};
+
+struct QuantArgs {
+    const void *src[kMax];
+    int8_t *codes[kMax];
+    float *scales[kMax];
+    uint64_t src_stride[kMax], code_stride[kMax];
+    uint32_t cols[kMax];
+    uint32_t first[kMax];  // a matrix's first row in the grid; 0xFFFFFFFF past the last
+};
+
+// One workgroup per row: the largest magnitude, then the codes; the row comes
+// from the caches the second time.
+template <class T>
+__global__ __launch_bounds__(kThreads) void quantize_rows(QuantArgs a) {
+    __shared__ uint32_t top_s[kThreads / 64];
+    uint32_t k = 0;
+#pragma unroll
+    for (int j = 1; j < kMax; j++) k += uint32_t(blockIdx.x >= a.first[j]);
+    const uint32_t r = blockIdx.x - a.first[k], cols = a.cols[k];
+    const T *x = static_cast<const T *>(a.src[k]) + r * a.src_stride[k];
+    int8_t *q = a.codes[k] + r * a.code_stride[k];
+    uint32_t top = 0;
+    for (uint32_t c = threadIdx.x * 8; c < cols; c += kThreads * 8) top = max(top, row_top(x, c, cols));
+    top = wave_top(top);
+    if ((threadIdx.x & 63u) == 0) top_s[threadIdx.x >> 6] = top;
+    __syncthreads();
+    const Row<T> row(max(max(top_s[0], top_s[1]), max(top_s[2], top_s[3])));
+    if (threadIdx.x == 0) a.scales[k][r] = row.scale;
+    for (uint32_t c = threadIdx.x * 8; c < ((cols + 15) & ~15u); c += kThreads * 8)
+        *reinterpret_cast<u32x2 *>(q + c) = row.codes(x, c, cols);
 }
 
 // ---------------------------------------------------------------- product
@@ -162,11 +182,79 @@ __device__ __forceinline__ i32x4 codes16(const int8_t *p, uint32_t c, uint32_t c
 
 // Few rows and at most 16 tokens, where what counts is the time of one
 // workgroup: it takes 16 weight rows, its eight waves split the columns in runs
-// of 128, and each has the operands of 512 columns in flight at once.  The
+// of 128, and each has the weights of 512 columns in flight at once.  The
 // waves' sums meet in LDS.  Lane 16 q + i of a wave holds row i (or token i) and
 // columns 16 q .. of a 16x16x64 product, which the operands' row-major order
 // gives as is.
 constexpr uint32_t kRowWaves = 8;
+constexpr uint32_t kRun = kRowWaves * 128;
+
+// The next operands of a wave, from column c0 on (c0 - 16 q is the same in all
+// its lanes): four runs, or what is left of one; returns how many products.
+struct Runs {
+    i32x4 w[8];
+    int n;
+    __device__ __forceinline__ void load(const int8_t *p, uint32_t c0, uint32_t base, uint32_t cols) {
+        if (base + 3 * kRun + 128 <= cols) {
+            n = 8;
+#pragma unroll
+            for (int u = 0; u < 8; u++)
+                w[u] = *reinterpret_cast<const i32x4 *>(p + c0 + kRun * (u / 2) + 64 * (u % 2));
+        } else if (base < cols) {
+            n = 2;
+#pragma unroll
+            for (int u = 0; u < 2; u++) w[u] = codes16(p, c0 + 64 * u, cols);
+        } else {
+            n = 0;
+        }
+    }
+};
+
+// The product of the workgroup's rows; x(c) gives a lane 16 activation codes at
+// column c < cols rounded up to 16.  `runs` holds the first operands.
+template <class X>
+__device__ __forceinline__ i32x4 rows16_sum(Runs &runs, const int8_t *w, uint32_t c0, uint32_t base,
+                                            uint32_t cols, X x) {
+    i32x4 acc = {0, 0, 0, 0};
+    const uint32_t last = (cols - 1) & ~15u;
+    while (runs.n) {
+        Runs next;  // on their way while these are multiplied
+        const uint32_t step = runs.n == 8 ? 4 * kRun : kRun;
+        next.load(w, c0 + step, base + step, cols);
+        if (runs.n == 8) {
+            i32x4 xv[8];
+#pragma unroll
+            for (int u = 0; u < 8; u++) xv[u] = x(c0 + kRun * (u / 2) + 64 * (u % 2));
+#pragma unroll
+            for (int u = 0; u < 8; u++)
+                acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(runs.w[u], xv[u], acc, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+                acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(runs.w[u], x(min(c0 + 64 * u, last)), acc,
+                                                            0, 0, 0);
+        }
+        runs = next;
+        c0 += step, base += step;
+    }
+    return acc;
+}
+
+// Adds the waves' sums and stores: lane 16 q + j holds rows 4 q .. + 3 of token j.
+template <class Y>
+__device__ __forceinline__ void rows16_store(i32x4 acc, i32x4 (*part)[64], uint32_t wave, uint32_t lane,
+                                             Y *y, uint32_t rows_left, bool token, float xs,
+                                             const float *ws) {
+    if (wave) part[wave - 1][lane] = acc;
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (uint32_t p = 0; p < kRowWaves - 1; p++) acc += part[p][lane];
+    const uint32_t q = lane >> 4;
+#pragma unroll
+    for (uint32_t e = 0; e < 4; e++)
+        if (token && 4 * q + e < rows_left) y[4 * q + e] = Y(scaled(acc[e], xs, ws[e]));
+}
 
 template <class Y>
 __global__ __launch_bounds__(64 * kRowWaves) void gemm_rows16(GemmArgs a) {
@@ -179,55 +267,67 @@ __global__ __launch_bounds__(64 * kRowWaves) void gemm_rows16(GemmArgs a) {
     const uint32_t r0 = (blockIdx.x - a.first[k]) * 16;
     const uint32_t rows = a.rows[k], cols = a.cols[k], i = lane & 15u, q = lane >> 4;
     const int8_t *w = a.w[k] + uint64_t(min(r0 + i, rows - 1)) * a.w_stride[k];
-    const int8_t *x = a.x[k] + uint64_t(min(i, a.n_tokens - 1)) * a.x_stride[k];
-    const float xs = a.x_scale[k][min(i, a.n_tokens - 1)];
+    const uint32_t token = min(i, a.n_tokens - 1);
+    const int8_t *x = a.x[k] + uint64_t(token) * a.x_stride[k];
+    Runs runs;
+    runs.load(w, wave * 128 + 16 * q, wave * 128, cols);
+    const float xs = a.x_scale[k][token];
     float ws[4];
 #pragma unroll
     for (uint32_t e = 0; e < 4; e++) ws[e] = a.w_scale[k][min(r0 + 4 * q + e, rows - 1)];
-    i32x4 acc = {0, 0, 0, 0};
-    constexpr uint32_t kRun = kRowWaves * 128;
-    // (c0 - 16 q is the same for the wave)
-    uint32_t c0 = wave * 128 + 16 * q;
-    for (; c0 - 16 * q + 3 * kRun + 128 <= cols; c0 += 4 * kRun) {
-        i32x4 wv[8], xv[8];
+    const i32x4 acc = rows16_sum(runs, w, wave * 128 + 16 * q, wave * 128, cols, [&](uint32_t c) {
+        return *reinterpret_cast<const i32x4 *>(x + c);
+    });
+    rows16_store(acc, part, wave, lane, static_cast<Y *>(a.y[k]) + i * a.y_stride[k] + r0, rows - r0,
+                 i < a.n_tokens, xs, ws);
+}
+
+// One token that is not quantised yet: every workgroup quantises it for itself
+// while its first weights are on their way, which spares the launch before.
+// Bound by reading the weights: 47.8 us on the 8B block (4.6 TB/s) and 158 us on
+// the 70B block (5.4 TB/s), 4.8 us on 1024 x 1024, against 55.2, 165 and 7.2 us
+// with a launch for the codes before.  Holding the kernel to 80 or 64 registers
+// for more waves made it slower (8B block 59 and 79 us): its loads in flight
+// need them.
+constexpr uint32_t kOneMaxCols = 32768;  // the codes' room in LDS
+
+template <class X, class Y>
+__global__ __launch_bounds__(64 * kRowWaves) void linear_one(GemmArgs a) {
+    __shared__ i32x4 part[kRowWaves - 1][64];
+    __shared__ uint32_t top_s[kRowWaves];
+    extern __shared__ __align__(16) int8_t codes[];
+    uint32_t k = 0;
 #pragma unroll
-        for (int u = 0; u < 8; u++) {
-            const uint32_t c = c0 + kRun * (u / 2) + 64 * (u % 2);
-            wv[u] = *reinterpret_cast<const i32x4 *>(w + c);
-            xv[u] = *reinterpret_cast<const i32x4 *>(x + c);
-        }
+    for (int j = 1; j < kMax; j++) k += uint32_t(blockIdx.x >= a.first[j]);
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t r0 = (blockIdx.x - a.first[k]) * 16;
+    const uint32_t rows = a.rows[k], cols = a.cols[k], i = lane & 15u, q = lane >> 4;
+    const int8_t *w = a.w[k] + uint64_t(min(r0 + i, rows - 1)) * a.w_stride[k];
+    const X *x = reinterpret_cast<const X *>(a.x[k]);
+    Runs runs;
+    runs.load(w, wave * 128 + 16 * q, wave * 128, cols);
+    float ws[4];
 #pragma unroll
-        for (int u = 0; u < 8; u++)
-            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u], xv[u], acc, 0, 0, 0);
-    }
-    for (; c0 - 16 * q < cols; c0 += kRun) {
-        i32x4 wv[2], xv[2];
-#pragma unroll
-        for (int u = 0; u < 2; u++) {
-            const uint32_t c = c0 + 64 * u;
-            if (c0 - 16 * q + 128 <= cols) {
-                wv[u] = *reinterpret_cast<const i32x4 *>(w + c);
-                xv[u] = *reinterpret_cast<const i32x4 *>(x + c);
-            } else {
-                wv[u] = codes16(w, c, cols);
-                xv[u] = *reinterpret_cast<const i32x4 *>(x + min(c, (cols - 1) & ~15u));
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; u++)
-            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u], xv[u], acc, 0, 0, 0);
-    }
-    if (wave) part[wave - 1][lane] = acc;
+    for (uint32_t e = 0; e < 4; e++) ws[e] = a.w_scale[k][min(r0 + 4 * q + e, rows - 1)];
+
+    constexpr uint32_t kStep = 64 * kRowWaves * 8;
+    uint32_t top = 0;
+    for (uint32_t c = threadIdx.x * 8; c < cols; c += kStep) top = max(top, row_top(x, c, cols));
+    top = wave_top(top);
+    if (lane == 0) top_s[wave] = top;
     __syncthreads();
-    if (wave) return;
 #pragma unroll
-    for (uint32_t p = 0; p < kRowWaves - 1; p++) acc += part[p][lane];
-    // lane 16 q + j holds rows 4 q .. + 3 of token j
-    if (i >= a.n_tokens) return;
-    Y *y = static_cast<Y *>(a.y[k]) + i * a.y_stride[k] + r0 + 4 * q;
-#pragma unroll
-    for (uint32_t e = 0; e < 4; e++)
-        if (r0 + 4 * q + e < rows) y[e] = Y(scaled(acc[e], xs, ws[e]));
+    for (uint32_t p = 0; p < kRowWaves; p++) top = max(top, top_s[p]);
+    const Row<X> row(top);
+    for (uint32_t c = threadIdx.x * 8; c < ((cols + 15) & ~15u); c += kStep)
+        *reinterpret_cast<u32x2 *>(codes + c) = row.codes(x, c, cols);
+    __syncthreads();
+
+    const i32x4 acc = rows16_sum(runs, w, wave * 128 + 16 * q, wave * 128, cols, [&](uint32_t c) {
+        return *reinterpret_cast<const i32x4 *>(codes + c);
+    });
+    rows16_store(acc, part, wave, lane, static_cast<Y *>(a.y[k]) + r0, rows - r0, i == 0, row.scale, ws);
 }
 
 // Many tokens: a workgroup computes a tile of BT tokens x BR weight rows, its
@@ -575,6 +675,33 @@ float tiles_time(const GemmArgs &a, uint32_t n, uint32_t bt, uint32_t br, float 
     return std::max(float(stages) / 256 * busy, float(longest) * alone);
 }
 
+// first of workgroups of 16 rows; returns their number
+uint32_t sixteens(GemmArgs &a, uint32_t n) {
+    uint32_t tiles = 0;
+    for (uint32_t k = 0; k < n; k++) {
+        a.first[k] = tiles;
+        tiles += (a.rows[k] + 15) / 16;
+    }
+    return tiles;
+}
+
+template <class X, class Y>
+int run_one(GemmArgs &a, uint32_t n, hipStream_t st) {
+    uint32_t cols = 0;
+    for (uint32_t k = 0; k < n; k++) cols = std::max(cols, a.cols[k]);
+    const uint32_t tiles = sixteens(a, n);
+    return status(launch(linear_one<X, Y>, dim3(tiles), dim3(64 * kRowWaves), (cols + 15) & ~15u, st, a));
+}
+
+template <class X>
+int run_one(uint32_t y_type, GemmArgs &a, uint32_t n, hipStream_t st) {
+    switch (y_type) {
+    case DF11_TYPE_F32: return run_one<X, float>(a, n, st);
+    case DF11_TYPE_BF16: return run_one<X, __bf16>(a, n, st);
+    default: return run_one<X, _Float16>(a, n, st);
+    }
+}
+
 template <class Y>
 int run_gemm(GemmArgs &a, uint32_t n, hipStream_t st) {
     if (a.n_tokens <= 32) {
@@ -583,11 +710,7 @@ int run_gemm(GemmArgs &a, uint32_t n, hipStream_t st) {
         // against 9.6 with 1 token, 8.4 against 10.4 with 16); more of them
         // read too much of the activations (8B block: 43.4 against 48.0 us
         // with 1 token, but 48.4 against 48.6 with 4 and 66 against 51 with 16).
-        uint32_t tiles = 0;
-        for (uint32_t k = 0; k < n; k++) {
-            a.first[k] = tiles;
-            tiles += (a.rows[k] + 15) / 16;
-        }
+        const uint32_t tiles = sixteens(a, n);
         if (a.n_tokens == 1 || (a.n_tokens <= 16 && tiles <= 256))
             return status(launch(gemm_rows16<Y>, dim3(tiles), dim3(64 * kRowWaves), 0, st, a));
         return run_tiles<Y, 32, 64, 1, 2, 6>(a, n, st);
@@ -734,6 +857,27 @@ int df11_linear_int8(uint32_t x_type, uint32_t y_type, const df11_int8_tensor *t
     GemmArgs a{};
     uint32_t used = 0;
     int rc = prepare_gemm(y_type, q, n_tensors, n_tokens, a, used);
+    bool one = n_tokens == 1 && used;
+    for (uint32_t k = 0; k < n_tensors; k++)
+        one = one && t[k].cols >= 1 && t[k].cols <= kOneMaxCols;
+    if (rc == DF11_OK && one) {
+        // matrices were put in order: find each one's activations by its codes
+        for (uint32_t k = 0; k < used; k++)
+            for (uint32_t j = 0; j < n_rows; j++)
+                if (a.x[k] == rows[j].codes) {
+                    a.x[k] = static_cast<const int8_t *>(rows[j].src);
+                    break;
+                }
+        for (uint32_t j = 0; j < n_rows; j++)
+            if (!rows[j].src || !aligned(rows[j].src, type_bytes(x_type)) || x_type > DF11_TYPE_F16)
+                return DF11_E_INVALID;
+        hipStream_t st = static_cast<hipStream_t>(stream);
+        switch (x_type) {
+        case DF11_TYPE_F32: return run_one<float>(y_type, a, used, st);
+        case DF11_TYPE_BF16: return run_one<__bf16>(y_type, a, used, st);
+        default: return run_one<_Float16>(y_type, a, used, st);
+        }
+    }
     if (rc == DF11_OK) rc = df11_quantize_int8(x_type, rows, n_rows, stream);
     return rc == DF11_OK && used ? launch_gemm(y_type, a, used, static_cast<hipStream_t>(stream)) : rc;
 }

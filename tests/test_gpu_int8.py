@@ -326,6 +326,36 @@ def test_linear(tokens, kind):
         assert ((y.cpu().double() - exact).abs() <= far * (1 + 1e-4) + (exact.abs() + far) * (half + 4 * U)).all()
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("cols", [1, 15, 16, 17, 127, 128, 129, 1000, 1024, 1025, 3975, 4095, 4096, 4097,
+                                  4111, 5120, 9001, 32768, 32769])
+def test_linear_of_one_token(cols, kind):
+    """One token is quantised by the product's own workgroups (up to 32768
+    columns): the same bits as by the quantiser, beside narrower matrices."""
+    g = torch.Generator().manual_seed(cols)
+    shapes = [(33, cols), (16, min(cols, 700)), (5, cols)]
+    ws = [torch.randn(*s, generator=g).bfloat16() for s in shapes]
+    a = (torch.randn(1, cols, generator=g) * 3).to(KINDS[kind])
+    b = torch.randn(1, min(cols, 700), generator=g).to(KINDS[kind])
+    layer = ed.Int8Linear.from_tensors([w.cuda() for w in ws])
+    da, db = a.cuda(), b.cuda()
+    say(f"[gpu] Int8Linear one token {kind} {cols} columns")
+    for x, w, y in zip((a, b, a), ws, layer([da, db, da], KINDS[kind])):
+        assert torch.equal(y.cpu(), linear_reference(x, w, kind)), w.shape
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("value", [0.0, math.nan, math.inf, -math.inf, "tiny"])
+def test_linear_of_one_odd_token(value, kind):
+    x = torch.zeros(1, 300)
+    x[0, 299] = {"bf16": 9.2e-41, "f16": 6e-8, "f32": 1.4e-45}[kind] if value == "tiny" else value
+    x = x.to(KINDS[kind])
+    w = torch.randn(20, 300).bfloat16()
+    say(f"[gpu] Int8Linear one token with {value} {kind}")
+    y, = ed.Int8Linear.from_tensors([w.cuda()])([x.cuda()], torch.float32)
+    assert np.array_equal(y.cpu().numpy(), linear_reference(x, w, "f32").numpy(), equal_nan=True)
+
+
 def test_linear_of_a_compressed_unit():
     """Decode, quantise, multiply: the same as from the weights themselves."""
     rng = np.random.default_rng(6)
