@@ -14,6 +14,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "df11.h"
 #include "df11_launch.h"
@@ -63,61 +64,71 @@ typedef __bf16 bf16x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32_any __attribute__((aligned(1)));
 
-// 4 elements at p[i ..], zeros from n on; the hardware takes any alignment
-__device__ __forceinline__ f32x4 load4(const float *p, uint64_t i, uint64_t n) {
-    if (i + 4 <= n) return *reinterpret_cast<const f32x4_any *>(p + i);
+// A lane's 4 elements of the 256 at p: all of them, or those below `left`
+// (zeros behind).  The hardware takes any alignment.  Everything is touched
+// once a step, so loads and stores pass the caches by.
+template <bool WHOLE>
+__device__ __forceinline__ f32x4 load4(const float *p, uint32_t i, uint32_t left) {
+    if (WHOLE) return __builtin_nontemporal_load(reinterpret_cast<const f32x4_any *>(p + i));
     f32x4 x = {0, 0, 0, 0};
 #pragma unroll
-    for (int k = 0; k < 3; k++)
-        if (i + k < n) x[k] = p[i + k];
+    for (uint32_t k = 0; k < 4; k++)
+        if (i + k < left) x[k] = p[i + k];
     return x;
 }
-__device__ __forceinline__ f32x4 load4(const __bf16 *p, uint64_t i, uint64_t n) {
-    if (i + 4 <= n)
-        return __builtin_convertvector(*reinterpret_cast<const bf16x4_any *>(p + i), f32x4);
+template <bool WHOLE>
+__device__ __forceinline__ f32x4 load4(const __bf16 *p, uint32_t i, uint32_t left) {
+    if (WHOLE)
+        return __builtin_convertvector(
+            __builtin_nontemporal_load(reinterpret_cast<const bf16x4_any *>(p + i)), f32x4);
     f32x4 x = {0, 0, 0, 0};
 #pragma unroll
-    for (int k = 0; k < 3; k++)
-        if (i + k < n) x[k] = float(p[i + k]);
+    for (uint32_t k = 0; k < 4; k++)
+        if (i + k < left) x[k] = float(p[i + k]);
     return x;
 }
-__device__ __forceinline__ uint32_t load4(const uint8_t *p, uint64_t i, uint64_t n) {
-    if (i + 4 <= n) return *reinterpret_cast<const u32_any *>(p + i);
+template <bool WHOLE>
+__device__ __forceinline__ uint32_t load4(const uint8_t *p, uint32_t i, uint32_t left) {
+    if (WHOLE) return __builtin_nontemporal_load(reinterpret_cast<const u32_any *>(p + i));
     uint32_t x = 0;
 #pragma unroll
-    for (int k = 0; k < 3; k++)
-        if (i + k < n) x |= uint32_t(p[i + k]) << (8 * k);
+    for (uint32_t k = 0; k < 4; k++)
+        if (i + k < left) x |= uint32_t(p[i + k]) << (8 * k);
     return x;
 }
-__device__ __forceinline__ void store4(float *p, uint64_t i, uint64_t n, f32x4 x) {
-    if (i + 4 <= n) {
-        *reinterpret_cast<f32x4_any *>(p + i) = x;
+template <bool WHOLE>
+__device__ __forceinline__ void store4(float *p, uint32_t i, uint32_t left, f32x4 x) {
+    if (WHOLE) {
+        __builtin_nontemporal_store(f32x4_any(x), reinterpret_cast<f32x4_any *>(p + i));
         return;
     }
 #pragma unroll
-    for (int k = 0; k < 3; k++)
-        if (i + k < n) p[i + k] = x[k];
+    for (uint32_t k = 0; k < 4; k++)
+        if (i + k < left) p[i + k] = x[k];
 }
-__device__ __forceinline__ void store4(__bf16 *p, uint64_t i, uint64_t n, bf16x4 x) {
-    if (i + 4 <= n) {
-        *reinterpret_cast<bf16x4_any *>(p + i) = x;
+template <bool WHOLE>
+__device__ __forceinline__ void store4(__bf16 *p, uint32_t i, uint32_t left, bf16x4 x) {
+    if (WHOLE) {
+        __builtin_nontemporal_store(bf16x4_any(x), reinterpret_cast<bf16x4_any *>(p + i));
         return;
     }
 #pragma unroll
-    for (int k = 0; k < 3; k++)
-        if (i + k < n) p[i + k] = x[k];
+    for (uint32_t k = 0; k < 4; k++)
+        if (i + k < left) p[i + k] = x[k];
 }
-__device__ __forceinline__ void store4(__bf16 *p, uint64_t i, uint64_t n, f32x4 x) {
-    store4(p, i, n, __builtin_convertvector(x, bf16x4));
+template <bool WHOLE>
+__device__ __forceinline__ void store4(__bf16 *p, uint32_t i, uint32_t left, f32x4 x) {
+    store4<WHOLE>(p, i, left, __builtin_convertvector(x, bf16x4));
 }
-__device__ __forceinline__ void store4(uint8_t *p, uint64_t i, uint64_t n, uint32_t x) {
-    if (i + 4 <= n) {
-        *reinterpret_cast<u32_any *>(p + i) = x;
+template <bool WHOLE>
+__device__ __forceinline__ void store4(uint8_t *p, uint32_t i, uint32_t left, uint32_t x) {
+    if (WHOLE) {
+        __builtin_nontemporal_store(x, reinterpret_cast<u32_any *>(p + i));
         return;
     }
 #pragma unroll
-    for (int k = 0; k < 3; k++)
-        if (i + k < n) p[i + k] = uint8_t(x >> (8 * k));
+    for (uint32_t k = 0; k < 4; k++)
+        if (i + k < left) p[i + k] = uint8_t(x >> (8 * k));
 }
 
 // the largest x of the wave, in every lane (DPP inside rows of 16, then across rows)
@@ -131,16 +142,84 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
     return uint32_t(__builtin_amdgcn_readlane(int(x), 63));
 }
 
-// The scale of a block from the bits of its largest magnitude (magnitudes
-// compare as their bits do, and NaN above all), and its reciprocal.
-// unit = 1 / 127^2 or 1 / 255^2, rounded.
-__device__ __forceinline__ void block_scale(uint32_t top, float unit, float tiny, float &scale,
-                                            float &inv) {
-    const float x = __uint_as_float(top);
-    const bool bad = top >= 0x7F800000u;
-    const bool none = x < tiny;
-    scale = bad ? __uint_as_float(0x7FC00000u) : none ? 0.0f : x * unit;
-    inv = bad || none ? 0.0f : 1.0f / scale;
+// sqrt(x) of 4 values, correctly rounded as sqrtf's.  For values in the middle of
+// the range two Newton steps from the reciprocal root do that in 11
+// instructions, against 20 with sqrtf's scaling and last-place checks; other
+// values (0 apart) take the wave to sqrtf.
+__device__ __forceinline__ f32x4 roots(f32x4 x) {
+    f32x4 r;
+    bool odd = false;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        odd = odd || !(x[k] == 0.0f || (x[k] >= 0x1p-96f && x[k] <= 0x1p96f));
+        const float y = __builtin_amdgcn_rsqf(x[k]);
+        float s = x[k] * y, h = 0.5f * y;
+        const float e = __builtin_fmaf(-h, s, 0.5f);
+        s = __builtin_fmaf(s, e, s);
+        h = __builtin_fmaf(h, e, h);
+        s = __builtin_fmaf(__builtin_fmaf(-s, s, x[k]), h, s);
+        r[k] = x[k] == 0.0f ? 0.0f : s;
+    }
+    if (__builtin_amdgcn_ballot_w64(odd)) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) r[k] = sqrtf(x[k]);
+    }
+    return r;
+}
+
+// round(sqrt(x inv)) of 4 values, at most `most`.  The hardware's root is off by
+// one in the last place at most, which the rounding forgets unless the root lies
+// next to a half; then the wave takes the exact one.
+__device__ __forceinline__ f32x4 root_codes(f32x4 x, float inv, float most) {
+    f32x4 c;
+    float far = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const float s = __builtin_amdgcn_sqrtf(fabsf(x[k]) * inv);
+        c[k] = rintf(s);
+        far = fmaxf(far, fabsf(s - c[k]));
+    }
+    if (__builtin_amdgcn_ballot_w64(far > 0.4999f)) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) c[k] = rintf(sqrtf(fabsf(x[k]) * inv));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k++) c[k] = fminf(c[k], most);
+    return c;
+}
+
+// The scales of a block from the bits of its largest |m| and sqrt(v)
+// (magnitudes compare as their bits do, and NaN above all), and their
+// reciprocals: 0 for a block of zeros, and for one that is not finite, whose
+// scale is NaN.
+struct Scales {
+    float m, m_inv, v, v_inv;
+    __device__ Scales(uint32_t top_m, uint32_t top_r) {
+        const float a = __uint_as_float(top_m), b = __uint_as_float(top_r);
+        const float s = a * (1.0f / (127.0f * 127.0f)), t = b * (1.0f / (255.0f * 255.0f));
+        // one division for both: the lower lanes' and the upper lanes'
+        const float inv = 1.0f / ((threadIdx.x & 32u) ? t : s);
+        const float s_inv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), 0));
+        const float t_inv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), 32));
+        const bool bad_m = top_m >= 0x7F800000u, bad_v = top_r >= 0x7F800000u;
+        const bool no_m = a < 0x1p-100f, no_v = top_r == 0;
+        const float nan = __uint_as_float(0x7FC00000u);
+        m = bad_m ? nan : no_m ? 0.0f : s;
+        v = bad_v ? nan : no_v ? 0.0f : t;
+        m_inv = bad_m || no_m ? 0.0f : s_inv;
+        v_inv = bad_v || no_v ? 0.0f : t_inv;
+    }
+};
+
+// the values of 4 codes
+__device__ __forceinline__ void decode(uint32_t mc, uint32_t vc, float ms, float vs, f32x4 &m, f32x4 &v) {
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const int cm = int(int8_t(mc >> (8 * k))), cv = int(uint8_t(vc >> (8 * k)));
+        m[k] = ms * float(cm * (cm < 0 ? -cm : cm));
+        const float r = vs * float(cv * cv);
+        v[k] = r * r;
+    }
 }
 
 __device__ __forceinline__ const Tensor &find(const Table &a, uint32_t &chunk) {
@@ -183,89 +262,94 @@ __global__ __launch_bounds__(kThreads) void adamw(Table a, Numbers c) {
         still = !(fabsf(f) < __builtin_inff());
     }
 
-    W *w = static_cast<W *>(t.w);
-    const G *g = static_cast<const G *>(t.g);
-    for (uint64_t i = lo + threadIdx.x * 4; i < ((hi + 255) & ~uint64_t(255)); i += kStep) {
-        bf16x4 shown;  // the weights as BF16, for the histogram
-        if (still) {
-            if (!counting) break;
-            shown = __builtin_convertvector(load4(w, i, hi), bf16x4);
-        } else {
-            const uint64_t b = i / DF11_ADAMW_BLOCK;  // the same in all lanes of a wave
-            f32x4 gr = load4(g, i, hi);
-            f32x4 x = MASTER ? load4(t.master, i, hi) : load4(w, i, hi);
-            f32x4 m, v;
-            if constexpr (BITS == 32) {
-                m = load4(static_cast<const float *>(t.m), i, hi);
-                v = load4(static_cast<const float *>(t.v), i, hi);
-            } else {
-                const uint32_t mc = load4(static_cast<const uint8_t *>(t.m), i, hi);
-                const uint32_t vc = load4(static_cast<const uint8_t *>(t.v), i, hi);
-                const float ms = t.m_scale[b], vs = t.v_scale[b];
+    // the wave's next 256 elements from `at` on: all of them, or `left`
+    const uint32_t i = (threadIdx.x & 63u) * 4, copy = threadIdx.x % kCopies;
+    const auto count = [&](bf16x4 shown, uint32_t left) {
+        const uint16_t *bits = reinterpret_cast<const uint16_t *>(&shown);
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const int cm = int(int8_t(mc >> (8 * k)));
-                    const int cv = int(uint8_t(vc >> (8 * k)));
-                    m[k] = ms * float(cm * (cm < 0 ? -cm : cm));
-                    const float r = vs * float(cv * cv);
-                    v[k] = r * r;
-                }
+        for (uint32_t k = 0; k < 4; k++)
+            if (i + k < left) atomicAdd(&hist[((bits[k] >> 7) & 0xFFu) * (kCopies + 1) + copy], 1u);
+    };
+    const auto update = [&](auto whole, uint64_t at, uint32_t left) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        W *w = static_cast<W *>(t.w) + at;
+        float *master = t.master + at;
+        f32x4 g = load4<WHOLE>(static_cast<const G *>(t.g) + at, i, left), x, m, v;
+        if constexpr (MASTER) x = load4<WHOLE>(master, i, left);
+        else x = load4<WHOLE>(static_cast<const W *>(w), i, left);
+        float *m32 = static_cast<float *>(t.m) + at, *v32 = static_cast<float *>(t.v) + at;
+        uint8_t *m8 = static_cast<uint8_t *>(t.m) + at, *v8 = static_cast<uint8_t *>(t.v) + at;
+        const uint64_t block = at / DF11_ADAMW_BLOCK;
+        if constexpr (BITS == 32) {
+            m = load4<WHOLE>(static_cast<const float *>(m32), i, left);
+            v = load4<WHOLE>(static_cast<const float *>(v32), i, left);
+        } else {
+            decode(load4<WHOLE>(static_cast<const uint8_t *>(m8), i, left),
+                   load4<WHOLE>(static_cast<const uint8_t *>(v8), i, left), t.m_scale[block],
+                   t.v_scale[block], m, v);
+        }
+        if (c.d_factor) {
+#pragma unroll
+            for (int k = 0; k < 4; k++) g[k] = g[k] * f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            m[k] = m[k] * c.b1 + g[k] * c.c1;
+            v[k] = v[k] * c.b2 + (g[k] * c.c2) * g[k];
+        }
+        f32x4 r = roots(v);
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const float u = m[k] / (r[k] * inv_root + c.eps);
+            x[k] = x[k] * keep - u * size;
+        }
+        if constexpr (BITS == 32) {
+            store4<WHOLE>(m32, i, left, m);
+            store4<WHOLE>(v32, i, left, v);
+        } else {
+            uint32_t tm = 0, tr = 0;
+#pragma unroll
+            for (uint32_t k = 0; k < 4; k++) {
+                if (!WHOLE && i + k >= left) m[k] = r[k] = 0.0f;
+                tm = max(tm, __float_as_uint(m[k]) & 0x7FFFFFFFu);
+                tr = max(tr, __float_as_uint(r[k]) & 0x7FFFFFFFu);
             }
-            f32x4 r;
+            const Scales s(wave_max(tm), wave_max(tr));
+            const f32x4 cm = root_codes(m, s.m_inv, 127.0f), cv = root_codes(r, s.v_inv, 255.0f);
+            uint32_t mc = 0, vc = 0;
 #pragma unroll
             for (int k = 0; k < 4; k++) {
-                const float gk = c.d_factor ? gr[k] * f : gr[k];
-                m[k] = m[k] * c.b1 + gk * c.c1;
-                v[k] = v[k] * c.b2 + (gk * c.c2) * gk;
-                r[k] = sqrtf(v[k]);
-                const float u = m[k] / (r[k] * inv_root + c.eps);
-                x[k] = x[k] * keep - u * size;
+                const int a = int(__builtin_copysignf(cm[k], m[k])), b = int(cv[k]);
+                mc |= (uint32_t(a) & 0xFFu) << (8 * k);
+                vc |= uint32_t(r[k] > 0.0f ? max(b, 1) : b) << (8 * k);
             }
-            if constexpr (BITS == 32) {
-                store4(static_cast<float *>(t.m), i, hi, m);
-                store4(static_cast<float *>(t.v), i, hi, v);
-            } else {
-                uint32_t tm = 0, tr = 0;
-#pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    if (i + k >= hi) m[k] = r[k] = 0.0f;
-                    tm = max(tm, __float_as_uint(m[k]) & 0x7FFFFFFFu);
-                    tr = max(tr, __float_as_uint(r[k]) & 0x7FFFFFFFu);
-                }
-                float ms, mi, vs, vi;
-                block_scale(wave_max(tm), 1.0f / (127.0f * 127.0f), 0x1p-100f, ms, mi);
-                block_scale(wave_max(tr), 1.0f / (255.0f * 255.0f), 0x1p-149f, vs, vi);
-                uint32_t mc = 0, vc = 0;
-#pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const int cm = int(fminf(rintf(sqrtf(fabsf(m[k]) * mi)), 127.0f));
-                    int cv = int(fminf(rintf(sqrtf(r[k] * vi)), 255.0f));
-                    if (vi > 0.0f && r[k] > 0.0f) cv = max(cv, 1);
-                    mc |= (uint32_t(m[k] < 0.0f ? -cm : cm) & 0xFFu) << (8 * k);
-                    vc |= uint32_t(cv) << (8 * k);
-                }
-                store4(static_cast<uint8_t *>(t.m), i, hi, mi > 0.0f ? mc : 0u);
-                store4(static_cast<uint8_t *>(t.v), i, hi, vi > 0.0f ? vc : 0u);
-                if ((threadIdx.x & 63u) == 0) {
-                    t.m_scale[b] = ms;
-                    t.v_scale[b] = vs;
-                }
-            }
-            if (MASTER) store4(t.master, i, hi, x);
-            if constexpr (sizeof(W) == 2) {
-                shown = __builtin_convertvector(x, bf16x4);
-                store4(w, i, hi, shown);
-            } else {
-                store4(w, i, hi, x);
+            store4<WHOLE>(m8, i, left, s.m_inv > 0.0f ? mc : 0u);
+            store4<WHOLE>(v8, i, left, s.v_inv > 0.0f ? vc : 0u);
+            if (i == 0) {
+                t.m_scale[block] = s.m;
+                t.v_scale[block] = s.v;
             }
         }
-        if (counting) {
-            const uint32_t copy = threadIdx.x % kCopies;
-            const uint16_t *bits = reinterpret_cast<const uint16_t *>(&shown);
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-                if (i + k < hi)
-                    atomicAdd(&hist[((bits[k] >> 7) & 0xFFu) * (kCopies + 1) + copy], 1u);
+        if constexpr (MASTER) store4<WHOLE>(master, i, left, x);
+        if constexpr (sizeof(W) == 2) {
+            const bf16x4 shown = __builtin_convertvector(x, bf16x4);
+            store4<WHOLE>(w, i, left, shown);
+            if (counting) count(shown, left);
+        } else {
+            store4<WHOLE>(w, i, left, x);
+        }
+    };
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (!still) {
+        for (uint64_t at = lo + 256 * wave; at < hi; at += kStep) {
+            if (at + 256 <= hi) update(std::true_type{}, at, 256);
+            else update(std::false_type{}, at, uint32_t(hi - at));
+        }
+    } else if (counting) {
+        for (uint64_t at = lo + 256 * wave; at < hi; at += kStep) {
+            const uint32_t left = uint32_t(min(hi - at, uint64_t(256)));
+            count(__builtin_convertvector(load4<false>(static_cast<const W *>(t.w) + at, i, left), bf16x4),
+                  left);
         }
     }
     if (COUNTS) {
@@ -289,23 +373,21 @@ __global__ __launch_bounds__(kThreads) void state_values(Table a) {
     uint32_t chunk;
     const Tensor &t = find(a, chunk);
     const uint64_t lo = uint64_t(chunk) * a.chunk, hi = min(t.n, lo + a.chunk);
-    T *mo = static_cast<T *>(t.w), *vo = reinterpret_cast<T *>(t.master);
-    for (uint64_t i = lo + threadIdx.x * 4; i < hi; i += kStep) {
-        const uint64_t b = i / DF11_ADAMW_BLOCK;
+    const uint32_t i = (threadIdx.x & 63u) * 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const auto read = [&](auto whole, uint64_t at, uint32_t left) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        const uint64_t block = at / DF11_ADAMW_BLOCK;
         f32x4 m, v;
-        const uint32_t mc = load4(static_cast<const uint8_t *>(t.m), i, hi);
-        const uint32_t vc = load4(static_cast<const uint8_t *>(t.v), i, hi);
-        const float ms = t.m_scale[b], vs = t.v_scale[b];
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            const int cm = int(int8_t(mc >> (8 * k)));
-            const int cv = int(uint8_t(vc >> (8 * k)));
-            m[k] = ms * float(cm * (cm < 0 ? -cm : cm));
-            const float r = vs * float(cv * cv);
-            v[k] = r * r;
-        }
-        if (mo) store4(mo, i, hi, m);
-        if (vo) store4(vo, i, hi, v);
+        decode(load4<WHOLE>(static_cast<const uint8_t *>(t.m) + at, i, left),
+               load4<WHOLE>(static_cast<const uint8_t *>(t.v) + at, i, left), t.m_scale[block],
+               t.v_scale[block], m, v);
+        if (t.w) store4<WHOLE>(static_cast<T *>(t.w) + at, i, left, m);
+        if (t.master) store4<WHOLE>(reinterpret_cast<T *>(t.master) + at, i, left, v);
+    };
+    for (uint64_t at = lo + 256 * wave; at < hi; at += kStep) {
+        if (at + 256 <= hi) read(std::true_type{}, at, 256);
+        else read(std::false_type{}, at, uint32_t(hi - at));
     }
 }
 
@@ -329,12 +411,23 @@ __global__ __launch_bounds__(kThreads) void norm_parts(Table a, double *out) {
     const Tensor &t = find(a, chunk);
     const uint64_t lo = uint64_t(chunk) * a.chunk, hi = min(t.n, lo + a.chunk);
     const G *g = static_cast<const G *>(t.g);
+    const uint32_t i = (threadIdx.x & 63u) * 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     double s = 0.0;
-    for (uint64_t i = lo + threadIdx.x * 4; i < hi; i += kStep) {
-        const f32x4 x = load4(g, i, hi);
+    const auto add = [&](f32x4 x) {
 #pragma unroll
         for (int k = 0; k < 4; k++) s = __builtin_fma(double(x[k]), double(x[k]), s);
+    };
+    uint64_t at = lo + 256 * wave;
+    for (; at + 3 * kStep + 256 <= hi; at += 4 * kStep) {  // four loads in flight
+        f32x4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) x[k] = load4<true>(g + at + k * kStep, i, 256);
+#pragma unroll
+        for (int k = 0; k < 4; k++) add(x[k]);
     }
+    for (; at < hi; at += kStep)
+        add(load4<false>(g + at, i, uint32_t(min(hi - at, uint64_t(256)))));
     s = block_sum(s, part);
     if (threadIdx.x == 0) out[blockIdx.x] = s;
 }
