@@ -367,27 +367,49 @@ __global__ __launch_bounds__(256) void clear_counts(Table a) {
     if (p) p[threadIdx.x] = 0;
 }
 
-// m and v of 8-bit states; the outputs travel in the table's w and master
+// m and v of 8-bit states; the outputs travel in the table's w and master.  A
+// wave takes 512 elements at a time, 8 a lane, so that BF16 values leave 16
+// bytes a lane.
+typedef __bf16 bf16x8_any __attribute__((ext_vector_type(8), aligned(2)));
+typedef float f32x8_any __attribute__((ext_vector_type(8), aligned(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+
+__device__ __forceinline__ void store8(float *p, f32x8 x) {
+    __builtin_nontemporal_store(f32x8_any(x), reinterpret_cast<f32x8_any *>(p));
+}
+__device__ __forceinline__ void store8(__bf16 *p, f32x8 x) {
+    __builtin_nontemporal_store(__builtin_convertvector(x, bf16x8_any), reinterpret_cast<bf16x8_any *>(p));
+}
+
 template <class T>
 __global__ __launch_bounds__(kThreads) void state_values(Table a) {
     uint32_t chunk;
     const Tensor &t = find(a, chunk);
     const uint64_t lo = uint64_t(chunk) * a.chunk, hi = min(t.n, lo + a.chunk);
-    const uint32_t i = (threadIdx.x & 63u) * 4;
+    const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const auto read = [&](auto whole, uint64_t at, uint32_t left) {
-        constexpr bool WHOLE = decltype(whole)::value;
-        const uint64_t block = at / DF11_ADAMW_BLOCK;
-        f32x4 m, v;
-        decode(load4<WHOLE>(static_cast<const uint8_t *>(t.m) + at, i, left),
-               load4<WHOLE>(static_cast<const uint8_t *>(t.v) + at, i, left), t.m_scale[block],
-               t.v_scale[block], m, v);
-        if (t.w) store4<WHOLE>(static_cast<T *>(t.w) + at, i, left, m);
-        if (t.master) store4<WHOLE>(reinterpret_cast<T *>(t.master) + at, i, left, v);
-    };
-    for (uint64_t at = lo + 256 * wave; at < hi; at += kStep) {
-        if (at + 256 <= hi) read(std::true_type{}, at, 256);
-        else read(std::false_type{}, at, uint32_t(hi - at));
+    const uint8_t *m = static_cast<const uint8_t *>(t.m), *v = static_cast<const uint8_t *>(t.v);
+    T *mo = static_cast<T *>(t.w), *vo = reinterpret_cast<T *>(t.master);
+    for (uint64_t at = lo + 512 * wave; at < hi; at += 512 * (kThreads / 64)) {
+        const uint64_t i = at + 8 * lane;
+        if (at + 512 <= hi) {
+            const u32x2_any mc = __builtin_nontemporal_load(reinterpret_cast<const u32x2_any *>(m + i));
+            const u32x2_any vc = __builtin_nontemporal_load(reinterpret_cast<const u32x2_any *>(v + i));
+            const float ms = t.m_scale[i / DF11_ADAMW_BLOCK], vs = t.v_scale[i / DF11_ADAMW_BLOCK];
+            f32x4 m0, m1, v0, v1;
+            decode(mc[0], vc[0], ms, vs, m0, v0);
+            decode(mc[1], vc[1], ms, vs, m1, v1);
+            if (mo) store8(mo + i, __builtin_shufflevector(m0, m1, 0, 1, 2, 3, 4, 5, 6, 7));
+            if (vo) store8(vo + i, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            for (uint64_t e = i; e < min(i + 8, hi); e++) {
+                f32x4 mv, vv;
+                decode(m[e], v[e], t.m_scale[e / DF11_ADAMW_BLOCK], t.v_scale[e / DF11_ADAMW_BLOCK], mv, vv);
+                if (mo) mo[e] = T(mv[0]);
+                if (vo) vo[e] = T(vv[0]);
+            }
+        }
     }
 }
 
