@@ -131,93 +131,104 @@ __device__ __forceinline__ void store4(uint8_t *p, uint32_t i, uint32_t left, ui
         if (i + k < left) p[i + k] = uint8_t(x >> (8 * k));
 }
 
-// the largest x of the wave, in every lane (DPP inside rows of 16, then across rows)
-__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+// The largest x of each half of the wave, in all its lanes (DPP inside rows of
+// 16 lanes, then from each half's first row to its second).
+__device__ __forceinline__ uint32_t half_max(uint32_t x) {
     x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x111, 0xF, 0xF, true)));
     x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x112, 0xF, 0xF, true)));
     x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x114, 0xF, 0xF, true)));
     x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x118, 0xF, 0xF, true)));
-    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x142, 0xF, 0xF, false)));
-    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x143, 0xF, 0xF, false)));
-    return uint32_t(__builtin_amdgcn_readlane(int(x), 63));
+    x = max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x142, 0xA, 0xF, false)));
+    const int lower = __builtin_amdgcn_readlane(int(x), 31), upper = __builtin_amdgcn_readlane(int(x), 63);
+    return uint32_t((threadIdx.x & 32u) ? upper : lower);
 }
 
-// sqrt(x) of 4 values, correctly rounded as sqrtf's.  For values in the middle of
-// the range two Newton steps from the reciprocal root do that in 11
-// instructions, against 20 with sqrtf's scaling and last-place checks; other
-// values (0 apart) take the wave to sqrtf.
-__device__ __forceinline__ f32x4 roots(f32x4 x) {
-    f32x4 r;
-    bool odd = false;
+// r = sqrt(x) of N x 4 values, correctly rounded as sqrtf's.  For values in the
+// middle of the range two Newton steps from the reciprocal root do that in 11
+// instructions, against 20 with sqrtf's scaling and last-place checks; a wave
+// with another value (0, NaN) takes sqrtf.  Bits of values that are not
+// negative compare as the values do, with NaN above all.
+template <int N>
+__device__ __forceinline__ void roots(const f32x4 (&x)[N], f32x4 (&r)[N]) {
+    uint32_t least = 0xFFFFFFFFu, most = 0;
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-        odd = odd || !(x[k] == 0.0f || (x[k] >= 0x1p-96f && x[k] <= 0x1p96f));
-        const float y = __builtin_amdgcn_rsqf(x[k]);
-        float s = x[k] * y, h = 0.5f * y;
-        const float e = __builtin_fmaf(-h, s, 0.5f);
-        s = __builtin_fmaf(s, e, s);
-        h = __builtin_fmaf(h, e, h);
-        s = __builtin_fmaf(__builtin_fmaf(-s, s, x[k]), h, s);
-        r[k] = x[k] == 0.0f ? 0.0f : s;
-    }
-    if (__builtin_amdgcn_ballot_w64(odd)) {
+    for (int j = 0; j < N; j++) {
 #pragma unroll
-        for (int k = 0; k < 4; k++) r[k] = sqrtf(x[k]);
+        for (int k = 0; k < 4; k++) {
+            least = min(least, __float_as_uint(x[j][k]));
+            most = max(most, __float_as_uint(x[j][k]));
+            const float y = __builtin_amdgcn_rsqf(x[j][k]);
+            float s = x[j][k] * y, h = 0.5f * y;
+            const float e = __builtin_fmaf(-h, s, 0.5f);
+            s = __builtin_fmaf(s, e, s);
+            h = __builtin_fmaf(h, e, h);
+            r[j][k] = __builtin_fmaf(__builtin_fmaf(-s, s, x[j][k]), h, s);
+        }
     }
-    return r;
+    if (__builtin_amdgcn_ballot_w64(least < __float_as_uint(0x1p-96f) ||
+                                    most > __float_as_uint(0x1p96f))) {
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+#pragma unroll
+            for (int k = 0; k < 4; k++) r[j][k] = sqrtf(x[j][k]);
+        }
+    }
 }
 
-// round(sqrt(x inv)) of 4 values, at most `most`.  The hardware's root is off by
-// one in the last place at most, which the rounding forgets unless the root lies
-// next to a half; then the wave takes the exact one.
-__device__ __forceinline__ f32x4 root_codes(f32x4 x, float inv, float most) {
+// The codes sign(x) round(sqrt(|x| inv)) of 4 values, a byte each, ties to even;
+// AT_LEAST_1: 1 instead of 0 where x > 0.  A number below 2^22 added to
+// 1.5 2^23 is rounded to an integer, whose two's complement is then the low
+// bits.  The hardware's root is off by one in the last place at most, which
+// the rounding forgets unless the root lies next to a half; then, and where a
+// code of 0 needs the look at x, the wave takes the exact root.  No code passes
+// its largest: the largest |x| inv is 127^2 or 255^2 but for three roundings.
+template <bool AT_LEAST_1>
+__device__ __forceinline__ uint32_t root_codes(f32x4 x, float inv) {
+    constexpr float kInt = 0x1.8p23f;
     f32x4 c;
-    float far = 0.0f;
+    float far = 0.0f, least = 1.0f;
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-        const float s = __builtin_amdgcn_sqrtf(fabsf(x[k]) * inv);
-        c[k] = rintf(s);
-        far = fmaxf(far, fabsf(s - c[k]));
+        float s = __builtin_amdgcn_sqrtf(fabsf(x[k]) * inv);
+        if (AT_LEAST_1) least = fminf(least, s);
+        else s = __builtin_copysignf(s, x[k]);
+        c[k] = s + kInt;
+        far = fmaxf(far, fabsf((c[k] - kInt) - s));
     }
-    if (__builtin_amdgcn_ballot_w64(far > 0.4999f)) {
+    if (__builtin_amdgcn_ballot_w64(far > 0.4999f || (AT_LEAST_1 && least < 0.51f))) {
 #pragma unroll
-        for (int k = 0; k < 4; k++) c[k] = rintf(sqrtf(fabsf(x[k]) * inv));
+        for (int k = 0; k < 4; k++) {
+            float s = rintf(sqrtf(fabsf(x[k]) * inv));
+            if (AT_LEAST_1 && x[k] > 0.0f) s = fmaxf(s, 1.0f);
+            c[k] = (AT_LEAST_1 ? s : __builtin_copysignf(s, x[k])) + kInt;
+        }
     }
-#pragma unroll
-    for (int k = 0; k < 4; k++) c[k] = fminf(c[k], most);
-    return c;
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(c[1]), __float_as_uint(c[0]), 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(c[3]), __float_as_uint(c[2]), 0x04000C0Cu);
+    return lo | hi;
 }
 
-// The scales of a block from the bits of its largest |m| and sqrt(v)
-// (magnitudes compare as their bits do, and NaN above all), and their
-// reciprocals: 0 for a block of zeros, and for one that is not finite, whose
-// scale is NaN.
-struct Scales {
-    float m, m_inv, v, v_inv;
-    __device__ Scales(uint32_t top_m, uint32_t top_r) {
-        const float a = __uint_as_float(top_m), b = __uint_as_float(top_r);
-        const float s = a * (1.0f / (127.0f * 127.0f)), t = b * (1.0f / (255.0f * 255.0f));
-        // one division for both: the lower lanes' and the upper lanes'
-        const float inv = 1.0f / ((threadIdx.x & 32u) ? t : s);
-        const float s_inv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), 0));
-        const float t_inv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), 32));
-        const bool bad_m = top_m >= 0x7F800000u, bad_v = top_r >= 0x7F800000u;
-        const bool no_m = a < 0x1p-100f, no_v = top_r == 0;
-        const float nan = __uint_as_float(0x7FC00000u);
-        m = bad_m ? nan : no_m ? 0.0f : s;
-        v = bad_v ? nan : no_v ? 0.0f : t;
-        m_inv = bad_m || no_m ? 0.0f : s_inv;
-        v_inv = bad_v || no_v ? 0.0f : t_inv;
+// The scale of a lane's block from the bits of its largest magnitude
+// (magnitudes compare as their bits do, and NaN above all), and its reciprocal:
+// 0 for a block of zeros, and for one that is not finite, whose scale is NaN.
+// unit = 1 / 127^2 or 1 / 255^2, rounded.
+struct Scale {
+    float s, inv;
+    __device__ Scale(uint32_t top, float unit, float tiny) {
+        const float x = __uint_as_float(top);
+        const bool bad = top >= 0x7F800000u, none = x < tiny;
+        s = bad ? __uint_as_float(0x7FC00000u) : none ? 0.0f : x * unit;
+        inv = bad || none ? 0.0f : 1.0f / s;
     }
 };
 
-// the values of 4 codes
+// the values of 4 codes (squares of codes are exact)
 __device__ __forceinline__ void decode(uint32_t mc, uint32_t vc, float ms, float vs, f32x4 &m, f32x4 &v) {
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-        const int cm = int(int8_t(mc >> (8 * k))), cv = int(uint8_t(vc >> (8 * k)));
-        m[k] = ms * float(cm * (cm < 0 ? -cm : cm));
-        const float r = vs * float(cv * cv);
+        const float a = float(int8_t(mc >> (8 * k))), b = float(uint8_t(vc >> (8 * k)));
+        m[k] = ms * (a * fabsf(a));
+        const float r = vs * (b * b);
         v[k] = r * r;
     }
 }
@@ -262,9 +273,15 @@ __global__ __launch_bounds__(kThreads) void adamw(Table a, Numbers c) {
         still = !(fabsf(f) < __builtin_inff());
     }
 
-    // the wave's next 256 elements from `at` on: all of them, or `left`
-    const uint32_t i = (threadIdx.x & 63u) * 4, copy = threadIdx.x % kCopies;
-    const auto count = [&](bf16x4 shown, uint32_t left) {
+    // A wave's next elements from `at` on, all of them or `left`: NG groups of 4
+    // a lane.  With 8-bit states each half of the wave holds a block, so that
+    // what a block costs (its reductions, its scales) is shared by 8 elements.
+    constexpr int NG = BITS == 8 ? 2 : 1;
+    constexpr uint32_t kWave = 256 * NG;
+    const uint32_t lane = threadIdx.x & 63u, half = NG == 2 ? lane >> 5 : 0u;
+    const uint32_t i0 = NG == 2 ? 256 * half + 4 * (lane & 31u) : 4 * lane;  // + 128 a group
+    const uint32_t copy = threadIdx.x % kCopies;
+    const auto count = [&](bf16x4 shown, uint32_t i, uint32_t left) {
         const uint16_t *bits = reinterpret_cast<const uint16_t *>(&shown);
 #pragma unroll
         for (uint32_t k = 0; k < 4; k++)
@@ -274,82 +291,108 @@ __global__ __launch_bounds__(kThreads) void adamw(Table a, Numbers c) {
         constexpr bool WHOLE = decltype(whole)::value;
         W *w = static_cast<W *>(t.w) + at;
         float *master = t.master + at;
-        f32x4 g = load4<WHOLE>(static_cast<const G *>(t.g) + at, i, left), x, m, v;
-        if constexpr (MASTER) x = load4<WHOLE>(master, i, left);
-        else x = load4<WHOLE>(static_cast<const W *>(w), i, left);
+        f32x4 g[NG], x[NG], m[NG], v[NG], r[NG];
         float *m32 = static_cast<float *>(t.m) + at, *v32 = static_cast<float *>(t.v) + at;
         uint8_t *m8 = static_cast<uint8_t *>(t.m) + at, *v8 = static_cast<uint8_t *>(t.v) + at;
-        const uint64_t block = at / DF11_ADAMW_BLOCK;
-        if constexpr (BITS == 32) {
-            m = load4<WHOLE>(static_cast<const float *>(m32), i, left);
-            v = load4<WHOLE>(static_cast<const float *>(v32), i, left);
-        } else {
-            decode(load4<WHOLE>(static_cast<const uint8_t *>(m8), i, left),
-                   load4<WHOLE>(static_cast<const uint8_t *>(v8), i, left), t.m_scale[block],
-                   t.v_scale[block], m, v);
-        }
-        if (c.d_factor) {
+        const uint64_t block = at / DF11_ADAMW_BLOCK + half;
+        const bool mine = WHOLE || 256 * half < left;  // the lane's block exists
+        uint32_t mc[NG], vc[NG];
 #pragma unroll
-            for (int k = 0; k < 4; k++) g[k] = g[k] * f;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            m[k] = m[k] * c.b1 + g[k] * c.c1;
-            v[k] = v[k] * c.b2 + (g[k] * c.c2) * g[k];
-        }
-        f32x4 r = roots(v);
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            const float u = m[k] / (r[k] * inv_root + c.eps);
-            x[k] = x[k] * keep - u * size;
-        }
-        if constexpr (BITS == 32) {
-            store4<WHOLE>(m32, i, left, m);
-            store4<WHOLE>(v32, i, left, v);
-        } else {
-            uint32_t tm = 0, tr = 0;
-#pragma unroll
-            for (uint32_t k = 0; k < 4; k++) {
-                if (!WHOLE && i + k >= left) m[k] = r[k] = 0.0f;
-                tm = max(tm, __float_as_uint(m[k]) & 0x7FFFFFFFu);
-                tr = max(tr, __float_as_uint(r[k]) & 0x7FFFFFFFu);
+        for (int j = 0; j < NG; j++) {
+            const uint32_t i = i0 + 128 * j;
+            g[j] = load4<WHOLE>(static_cast<const G *>(t.g) + at, i, left);
+            if constexpr (MASTER) x[j] = load4<WHOLE>(static_cast<const float *>(master), i, left);
+            else x[j] = load4<WHOLE>(static_cast<const W *>(w), i, left);
+            if constexpr (BITS == 32) {
+                m[j] = load4<WHOLE>(static_cast<const float *>(m32), i, left);
+                v[j] = load4<WHOLE>(static_cast<const float *>(v32), i, left);
+            } else {
+                mc[j] = load4<WHOLE>(static_cast<const uint8_t *>(m8), i, left);
+                vc[j] = load4<WHOLE>(static_cast<const uint8_t *>(v8), i, left);
             }
-            const Scales s(wave_max(tm), wave_max(tr));
-            const f32x4 cm = root_codes(m, s.m_inv, 127.0f), cv = root_codes(r, s.v_inv, 255.0f);
-            uint32_t mc = 0, vc = 0;
+        }
+        if constexpr (BITS == 8) {
+            const float ms = mine ? t.m_scale[block] : 0.0f, vs = mine ? t.v_scale[block] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < NG; j++) decode(mc[j], vc[j], ms, vs, m[j], v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < NG; j++) {
+            if (c.d_factor) {
+#pragma unroll
+                for (int k = 0; k < 4; k++) g[j][k] = g[j][k] * f;
+            }
 #pragma unroll
             for (int k = 0; k < 4; k++) {
-                const int a = int(__builtin_copysignf(cm[k], m[k])), b = int(cv[k]);
-                mc |= (uint32_t(a) & 0xFFu) << (8 * k);
-                vc |= uint32_t(r[k] > 0.0f ? max(b, 1) : b) << (8 * k);
-            }
-            store4<WHOLE>(m8, i, left, s.m_inv > 0.0f ? mc : 0u);
-            store4<WHOLE>(v8, i, left, s.v_inv > 0.0f ? vc : 0u);
-            if (i == 0) {
-                t.m_scale[block] = s.m;
-                t.v_scale[block] = s.v;
+                m[j][k] = m[j][k] * c.b1 + g[j][k] * c.c1;
+                v[j][k] = v[j][k] * c.b2 + (g[j][k] * c.c2) * g[j][k];
             }
         }
-        if constexpr (MASTER) store4<WHOLE>(master, i, left, x);
-        if constexpr (sizeof(W) == 2) {
-            const bf16x4 shown = __builtin_convertvector(x, bf16x4);
-            store4<WHOLE>(w, i, left, shown);
-            if (counting) count(shown, left);
-        } else {
-            store4<WHOLE>(w, i, left, x);
+        roots(v, r);
+#pragma unroll
+        for (int j = 0; j < NG; j++) {
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const float u = m[j][k] / (r[j][k] * inv_root + c.eps);
+                x[j][k] = x[j][k] * keep - u * size;
+            }
+        }
+        if constexpr (BITS == 8) {
+            uint32_t tm = 0, tr = 0;
+#pragma unroll
+            for (int j = 0; j < NG; j++) {
+#pragma unroll
+                for (uint32_t k = 0; k < 4; k++) {
+                    if (!WHOLE && i0 + 128 * j + k >= left) m[j][k] = r[j][k] = 0.0f;
+                    tm = max(tm, __float_as_uint(m[j][k]) & 0x7FFFFFFFu);
+                    tr = max(tr, __float_as_uint(r[j][k]) & 0x7FFFFFFFu);
+                }
+            }
+            const Scale sm(half_max(tm), 1.0f / (127.0f * 127.0f), 0x1p-100f);
+            const Scale sv(half_max(tr), 1.0f / (255.0f * 255.0f), 0x1p-149f);
+#pragma unroll
+            for (int j = 0; j < NG; j++) {
+                mc[j] = root_codes<false>(m[j], sm.inv);
+                vc[j] = root_codes<true>(r[j], sv.inv);
+                mc[j] = sm.inv > 0.0f ? mc[j] : 0u;
+                vc[j] = sv.inv > 0.0f ? vc[j] : 0u;
+            }
+            if ((lane & 31u) == 0 && mine) {
+                t.m_scale[block] = sm.s;
+                t.v_scale[block] = sv.s;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NG; j++) {
+            const uint32_t i = i0 + 128 * j;
+            if constexpr (BITS == 32) {
+                store4<WHOLE>(m32, i, left, m[j]);
+                store4<WHOLE>(v32, i, left, v[j]);
+            } else {
+                store4<WHOLE>(m8, i, left, mc[j]);
+                store4<WHOLE>(v8, i, left, vc[j]);
+            }
+            if constexpr (MASTER) store4<WHOLE>(master, i, left, x[j]);
+            if constexpr (sizeof(W) == 2) {
+                const bf16x4 shown = __builtin_convertvector(x[j], bf16x4);
+                store4<WHOLE>(w, i, left, shown);
+                if (counting) count(shown, i, left);
+            } else {
+                store4<WHOLE>(w, i, left, x[j]);
+            }
         }
     };
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (!still) {
-        for (uint64_t at = lo + 256 * wave; at < hi; at += kStep) {
-            if (at + 256 <= hi) update(std::true_type{}, at, 256);
+        for (uint64_t at = lo + kWave * wave; at < hi; at += kWave * (kThreads / 64)) {
+            if (at + kWave <= hi) update(std::true_type{}, at, kWave);
             else update(std::false_type{}, at, uint32_t(hi - at));
         }
     } else if (counting) {
         for (uint64_t at = lo + 256 * wave; at < hi; at += kStep) {
             const uint32_t left = uint32_t(min(hi - at, uint64_t(256)));
-            count(__builtin_convertvector(load4<false>(static_cast<const W *>(t.w) + at, i, left), bf16x4),
-                  left);
+            count(__builtin_convertvector(load4<false>(static_cast<const W *>(t.w) + at, 4 * lane, left),
+                                          bf16x4), 4 * lane, left);
         }
     }
     if (COUNTS) {
