@@ -1014,16 +1014,19 @@ def _type(dtype) -> int:
 def _same(tensors, what, dtype=None, sizes=None, device=None):
     """Checks a list of contiguous device tensors of one type; returns them."""
     tensors = list(tensors)
-    if sizes is not None and [t.numel() for t in tensors] != list(sizes):
-        raise ValueError(f"{what} must have {list(sizes)[:8]} elements, one tensor each")
+    if sizes is not None and [t.numel() for t in tensors] != sizes:
+        raise ValueError(f"{what} must have {sizes[:8]} elements, one tensor each")
+    if not tensors:
+        return tensors
+    kind = tensors[0].dtype if dtype is None else dtype
+    where = tensors[0].device if device is None else device
+    if where.type != "cuda":
+        raise ValueError(f"{what} must be device tensors")
     for t in tensors:
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous device tensors")
-        if t.dtype != (tensors[0].dtype if dtype is None else dtype):
-            raise TypeError(f"{what} must be of one type" if dtype is None
-                            else f"{what} must be {dtype}")
-        if device is not None and t.device != device:
-            raise ValueError(f"{what} must be on {device}")
+        if t.dtype != kind:
+            raise TypeError(f"{what} must be of one type" if dtype is None else f"{what} must be {dtype}")
+        if t.device != where or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous tensors on {where}")
     return tensors
 
 
@@ -1083,8 +1086,7 @@ class AdamW:
         if state_bits not in (32, 8):
             raise ValueError("state_bits must be 32 or 8")
         self.device = dev = self.weights[0].device
-        _same(self.weights, "weights", device=dev)
-        sizes = [t.numel() for t in self.weights]
+        sizes = self._sizes = [t.numel() for t in self.weights]
         n = len(sizes)
         blocks = [-(-s // DF11_ADAMW_BLOCK) for s in sizes]
         self.masters = None if masters is None else _same(masters, "masters", torch.float32, sizes, dev)
@@ -1123,7 +1125,7 @@ class AdamW:
 
     def set_grads(self, grads) -> None:
         """The gradients that later steps read."""
-        self.grads = _same(grads, "grads", None, [t.numel() for t in self.weights], self.device)
+        self.grads = _same(grads, "grads", None, self._sizes, self.device)
         for a, g in zip(self._t, self.grads):
             a.g = g.data_ptr()
         self._c.g_type = _type(self.grads[0].dtype)
@@ -1183,7 +1185,7 @@ class AdamW:
 
         if self.state_bits == 32:
             raise ValueError("32-bit states are their own values")
-        sizes = [t.numel() for t in self.weights]
+        sizes = self._sizes
         if m_out is None and v_out is None:
             m_out, v_out = ([torch.empty(s, device=self.device) for s in sizes] for _ in range(2))
         lists = []

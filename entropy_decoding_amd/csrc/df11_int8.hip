@@ -15,7 +15,6 @@ namespace {
 using df11_detail::launch;
 
 constexpr int kMax = DF11_INT8_MAX_TENSORS;
-constexpr uint32_t kThreads = 256;
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -65,17 +64,22 @@ struct Quotient<float> {
     }
 };
 
-// The largest magnitude of x[c .. c + 8), as bits, so that a NaN or an infinity shows.
+// 8 elements at x[c ..], zeros from cols on
 template <class T>
-__device__ __forceinline__ uint32_t row_top(const T *x, uint32_t c, uint32_t cols) {
-    uint32_t top = 0;
-    if (c + 8 <= cols) {
-        const Eight<T> v = *reinterpret_cast<const Eight<T> *>(x + c);
+__device__ __forceinline__ Eight<T> load8(const T *x, uint32_t c, uint32_t cols) {
+    if (c + 8 <= cols) return *reinterpret_cast<const Eight<T> *>(x + c);
+    Eight<T> v;
 #pragma unroll
-        for (int e = 0; e < 8; e++) top = max(top, __float_as_uint(to_f32(v.e[e])) & 0x7FFFFFFFu);
-    } else {
-        for (uint32_t e = c; e < cols; e++) top = max(top, __float_as_uint(to_f32(x[e])) & 0x7FFFFFFFu);
-    }
+    for (uint32_t i = 0; i < 8; i++) v.e[i] = c + i < cols ? x[c + i] : T(0.0f);
+    return v;
+}
+
+// Their largest magnitude, as bits, so that a NaN or an infinity shows.
+template <class T>
+__device__ __forceinline__ uint32_t top_of(const Eight<T> &v) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; e++) top = max(top, __float_as_uint(to_f32(v.e[e])) & 0x7FFFFFFFu);
     return top;
 }
 
@@ -95,21 +99,12 @@ struct Row {
         : zero(top == 0 || top >= 0x7F800000u),
           scale(top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(top) / 127.0f),
           code(zero ? 1.0f : __uint_as_float(top)) {}
-    // the codes of x[c .. c + 8), zeros from cols on
-    __device__ __forceinline__ u32x2 codes(const T *x, uint32_t c, uint32_t cols) const {
-        float v[8];
-        if (c + 8 <= cols) {
-            const Eight<T> e = *reinterpret_cast<const Eight<T> *>(x + c);
-#pragma unroll
-            for (int i = 0; i < 8; i++) v[i] = to_f32(e.e[i]);
-        } else {
-#pragma unroll
-            for (uint32_t i = 0; i < 8; i++) v[i] = c + i < cols ? to_f32(x[c + i]) : 0.0f;
-        }
+    __device__ __forceinline__ u32x2 codes(const Eight<T> &v) const {
         u32x2 out = {0, 0};
         if (!zero) {
 #pragma unroll
-            for (int i = 0; i < 8; i++) out[i / 4] |= (uint32_t(int(code(v[i]))) & 0xFFu) << (8 * (i % 4));
+            for (int i = 0; i < 8; i++)
+                out[i / 4] |= (uint32_t(int(code(to_f32(v.e[i])))) & 0xFFu) << (8 * (i % 4));
         }
         return out;
     }
@@ -124,26 +119,46 @@ struct QuantArgs {
     uint32_t first[kMax];  // a matrix's first row in the grid; 0xFFFFFFFF past the last
 };
 
-// One workgroup per row: the largest magnitude, then the codes; the row comes
-// from the caches the second time.
-template <class T>
-__global__ __launch_bounds__(kThreads) void quantize_rows(QuantArgs a) {
-    __shared__ uint32_t top_s[kThreads / 64];
+// One workgroup per row: the largest magnitude, then the codes.  The first kHeld
+// times 8 elements of a thread stay in its registers between the two; what a
+// longer row has beyond comes from the caches the second time.
+constexpr int kHeld = 4;
+
+template <class T, int THREADS>
+__global__ __launch_bounds__(THREADS) void quantize_rows(QuantArgs a) {
+    __shared__ uint32_t top_s[THREADS / 64];
     uint32_t k = 0;
 #pragma unroll
     for (int j = 1; j < kMax; j++) k += uint32_t(blockIdx.x >= a.first[j]);
     const uint32_t r = blockIdx.x - a.first[k], cols = a.cols[k];
     const T *x = static_cast<const T *>(a.src[k]) + r * a.src_stride[k];
     int8_t *q = a.codes[k] + r * a.code_stride[k];
+    constexpr uint32_t kPass = THREADS * 8;
+    const uint32_t c0 = threadIdx.x * 8, end = (cols + 15) & ~15u;
+    Eight<T> held[kHeld];
     uint32_t top = 0;
-    for (uint32_t c = threadIdx.x * 8; c < cols; c += kThreads * 8) top = max(top, row_top(x, c, cols));
+#pragma unroll
+    for (int n = 0; n < kHeld; n++)
+        if (c0 + n * kPass < cols) held[n] = load8(x, c0 + n * kPass, cols);
+#pragma unroll
+    for (int n = 0; n < kHeld; n++)
+        if (c0 + n * kPass < cols) top = max(top, top_of(held[n]));
+    for (uint32_t c = c0 + kHeld * kPass; c < cols; c += kPass) top = max(top, top_of(load8(x, c, cols)));
     top = wave_top(top);
     if ((threadIdx.x & 63u) == 0) top_s[threadIdx.x >> 6] = top;
     __syncthreads();
-    const Row<T> row(max(max(top_s[0], top_s[1]), max(top_s[2], top_s[3])));
+#pragma unroll
+    for (int p = 0; p < THREADS / 64; p++) top = max(top, top_s[p]);
+    const Row<T> row(top);
     if (threadIdx.x == 0) a.scales[k][r] = row.scale;
-    for (uint32_t c = threadIdx.x * 8; c < ((cols + 15) & ~15u); c += kThreads * 8)
-        *reinterpret_cast<u32x2 *>(q + c) = row.codes(x, c, cols);
+#pragma unroll
+    for (int n = 0; n < kHeld; n++) {
+        const uint32_t c = c0 + n * kPass;
+        if (c < cols) *reinterpret_cast<u32x2 *>(q + c) = row.codes(held[n]);
+        else if (c < end) *reinterpret_cast<u32x2 *>(q + c) = u32x2{0, 0};
+    }
+    for (uint32_t c = c0 + kHeld * kPass; c < end; c += kPass)
+        *reinterpret_cast<u32x2 *>(q + c) = row.codes(load8(x, c, cols));
 }
 
 // ---------------------------------------------------------------- product
@@ -313,7 +328,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void linear_one(GemmArgs a) {
 
     constexpr uint32_t kStep = 64 * kRowWaves * 8;
     uint32_t top = 0;
-    for (uint32_t c = threadIdx.x * 8; c < cols; c += kStep) top = max(top, row_top(x, c, cols));
+    for (uint32_t c = threadIdx.x * 8; c < cols; c += kStep) top = max(top, top_of(load8(x, c, cols)));
     top = wave_top(top);
     if (lane == 0) top_s[wave] = top;
     __syncthreads();
@@ -321,7 +336,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void linear_one(GemmArgs a) {
     for (uint32_t p = 0; p < kRowWaves; p++) top = max(top, top_s[p]);
     const Row<X> row(top);
     for (uint32_t c = threadIdx.x * 8; c < ((cols + 15) & ~15u); c += kStep)
-        *reinterpret_cast<u32x2 *>(codes + c) = row.codes(x, c, cols);
+        *reinterpret_cast<u32x2 *>(codes + c) = row.codes(load8(x, c, cols));
     __syncthreads();
 
     const i32x4 acc = rows16_sum(runs, w, wave * 128 + 16 * q, wave * 128, cols, [&](uint32_t c) {
@@ -645,6 +660,13 @@ bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 int status(hipError_t e) { return e == hipSuccess ? DF11_OK : DF11_E_HIP; }
 
+template <class T>
+int run_rows(const QuantArgs &a, uint32_t rows, uint32_t longest, hipStream_t st) {
+    if (rows <= 512 && longest > 2048)
+        return status(launch(quantize_rows<T, 1024>, dim3(rows), dim3(1024), 0, st, a));
+    return status(launch(quantize_rows<T, 256>, dim3(rows), dim3(256), 0, st, a));
+}
+
 uint32_t type_bytes(uint32_t type) { return type == DF11_TYPE_F32 ? 4 : 2; }
 
 template <class Y, int BT, int BR, int WT, int WR, int NB>
@@ -778,7 +800,7 @@ int df11_quantize_int8(uint32_t src_type, const df11_int8_rows *m, uint32_t n,
     if ((n && !m) || n > kMax || src_type > DF11_TYPE_F16) return DF11_E_INVALID;
     QuantArgs a{};
     uint64_t rows = 0;
-    uint32_t used = 0;
+    uint32_t used = 0, longest = 0;
     for (uint32_t &f : a.first) f = 0xFFFFFFFFu;
     for (uint32_t k = 0; k < n; k++) {
         const df11_int8_rows &x = m[k];
@@ -793,17 +815,17 @@ int df11_quantize_int8(uint32_t src_type, const df11_int8_rows *m, uint32_t n,
         a.src[used] = x.src, a.codes[used] = x.codes, a.scales[used] = x.scales;
         a.src_stride[used] = x.src_stride, a.code_stride[used] = x.code_stride;
         a.cols[used] = x.cols, a.first[used] = uint32_t(rows);
+        longest = std::max(longest, x.cols);
         rows += x.rows;
         used++;
         if (rows > 0x7FFFFFFFu) return DF11_E_INVALID;
     }
     if (!rows) return DF11_OK;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const dim3 grid{uint32_t(rows)};
     switch (src_type) {
-    case DF11_TYPE_F32: return status(launch(quantize_rows<float>, grid, dim3(kThreads), 0, st, a));
-    case DF11_TYPE_BF16: return status(launch(quantize_rows<__bf16>, grid, dim3(kThreads), 0, st, a));
-    default: return status(launch(quantize_rows<_Float16>, grid, dim3(kThreads), 0, st, a));
+    case DF11_TYPE_F32: return run_rows<float>(a, uint32_t(rows), longest, st);
+    case DF11_TYPE_BF16: return run_rows<__bf16>(a, uint32_t(rows), longest, st);
+    default: return run_rows<_Float16>(a, uint32_t(rows), longest, st);
     }
 }
 
