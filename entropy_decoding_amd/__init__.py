@@ -868,8 +868,8 @@ def _quantize(tensors, st):
     out = []
     for a, t in zip(rows, tensors):
         r, c = t.shape
-        stride = (c + 15) // 16 * 16
-        codes = torch.empty((r, stride), dtype=torch.int8, device=t.device)
+        stride = (c + 127) // 128 * 128  # rows on cache lines
+        codes = torch.empty((r, stride), dtype=torch.int8, device=t.device)[:, :(c + 15) // 16 * 16]
         scales = torch.empty(r, dtype=torch.float32, device=t.device)
         a.src, a.codes, a.scales = t.data_ptr(), codes.data_ptr(), scales.data_ptr()
         a.src_stride, a.code_stride, a.rows, a.cols = t.stride(0), stride, r, c
@@ -881,7 +881,8 @@ def _quantize(tensors, st):
 def quantize_int8(tensors, stream=None):
     """df11_quantize_int8 of up to DF11_INT8_MAX_TENSORS matrices (BF16, F16 or
     float32 device tensors, contiguous rows): a list of (codes, scales), the
-    codes int8 [rows, cols rounded up to 16] with zeros behind the columns."""
+    codes int8 [rows, cols rounded up to 16] with zeros behind the columns, the
+    rows 128-byte aligned."""
     tensors = _matrices(tensors, "matrices")
     guard, st = _on(tensors[0].device, stream)
     with guard:

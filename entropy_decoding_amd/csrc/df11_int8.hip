@@ -299,8 +299,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void gemm_rows16(GemmArgs a) {
 
 // One token that is not quantised yet: every workgroup quantises it for itself
 // while its first weights are on their way, which spares the launch before.
-// Bound by reading the weights: 47.8 us on the 8B block (4.6 TB/s) and 158 us on
-// the 70B block (5.4 TB/s), 4.8 us on 1024 x 1024, against 55.2, 165 and 7.2 us
+// Bound by reading the weights: 46.3 us on the 8B block (4.7 TB/s) and 156 us on
+// the 70B block (5.5 TB/s), 4.8 us on 1024 x 1024, against 55.2, 165 and 7.2 us
 // with a launch for the codes before.  Holding the kernel to 80 or 64 registers
 // for more waves made it slower (8B block 59 and 79 us): its loads in flight
 // need them.
@@ -327,15 +327,18 @@ __global__ __launch_bounds__(64 * kRowWaves) void linear_one(GemmArgs a) {
     for (uint32_t e = 0; e < 4; e++) ws[e] = a.w_scale[k][min(r0 + 4 * q + e, rows - 1)];
 
     constexpr uint32_t kStep = 64 * kRowWaves * 8;
-    uint32_t top = 0;
-    for (uint32_t c = threadIdx.x * 8; c < cols; c += kStep) top = max(top, top_of(load8(x, c, cols)));
+    const uint32_t own = threadIdx.x * 8;  // a thread's first elements, held for their codes
+    const Eight<X> held = load8(x, own, cols);
+    uint32_t top = top_of(held);
+    for (uint32_t c = own + kStep; c < cols; c += kStep) top = max(top, top_of(load8(x, c, cols)));
     top = wave_top(top);
     if (lane == 0) top_s[wave] = top;
     __syncthreads();
 #pragma unroll
     for (uint32_t p = 0; p < kRowWaves; p++) top = max(top, top_s[p]);
     const Row<X> row(top);
-    for (uint32_t c = threadIdx.x * 8; c < ((cols + 15) & ~15u); c += kStep)
+    if (own < ((cols + 15) & ~15u)) *reinterpret_cast<u32x2 *>(codes + own) = row.codes(held);
+    for (uint32_t c = own + kStep; c < ((cols + 15) & ~15u); c += kStep)
         *reinterpret_cast<u32x2 *>(codes + c) = row.codes(load8(x, c, cols));
     __syncthreads();
 
@@ -667,6 +670,12 @@ int run_rows(const QuantArgs &a, uint32_t rows, uint32_t longest, hipStream_t st
     return status(launch(quantize_rows<T, 256>, dim3(rows), dim3(256), 0, st, a));
 }
 
+// Rows that start on a cache line: a stage's 128 columns are then one line of a
+// row and not parts of two (8B block, 128 tokens: 52 us, against 69 with rows
+// 64 bytes and 73 with rows 16 bytes off).
+uint64_t code_stride(uint64_t cols) { return (cols + 127) / 128 * 128; }
+uint64_t scale_bytes(uint64_t rows) { return (rows * 4 + 127) / 128 * 128; }
+
 uint32_t type_bytes(uint32_t type) { return type == DF11_TYPE_F32 ? 4 : 2; }
 
 template <class Y, int BT, int BR, int WT, int WR, int NB>
@@ -841,7 +850,7 @@ uint64_t df11_linear_int8_scratch_bytes(const df11_int8_tensor *t, uint32_t n_te
                                         uint32_t n_tokens) {
     uint64_t bytes = 16;
     for (uint32_t k = 0; t && k < n_tensors; k++)
-        bytes += n_tokens * ((uint64_t(t[k].cols) + 15) / 16 * 16) + (uint64_t(n_tokens) * 4 + 15) / 16 * 16;
+        bytes += n_tokens * code_stride(t[k].cols) + scale_bytes(n_tokens);
     return bytes;
 }
 
@@ -866,11 +875,11 @@ int df11_linear_int8(uint32_t x_type, uint32_t y_type, const df11_int8_tensor *t
             df11_int8_rows &r = rows[n_rows++];
             r.src = t[k].x, r.src_stride = t[k].x_stride;
             r.rows = n_tokens, r.cols = t[k].cols;
-            r.code_stride = (uint64_t(r.cols) + 15) / 16 * 16;
+            r.code_stride = code_stride(r.cols);
             r.codes = at;
             at += n_tokens * r.code_stride;
             r.scales = reinterpret_cast<float *>(at);
-            at += (uint64_t(n_tokens) * 4 + 15) / 16 * 16;
+            at += scale_bytes(n_tokens);
         }
         q[k] = t[k];
         q[k].x = rows[j].codes, q[k].x_scale = rows[j].scales, q[k].x_stride = rows[j].code_stride;
