@@ -31,15 +31,19 @@ struct alignas(sizeof(T)) Eight {
     T e[8];
 };
 
-// The code of x, as a float: the nearest integer to 127 x / a, ties to even.
+// The code of x in the low byte of the result: the nearest integer to 127 x / a,
+// ties to even.  A number below 2^22 added to 1.5 2^23 is rounded to an
+// integer, whose two's complement is then the low bits.
 //
 // 16-bit inputs: t = x inv with inv = 127 / a carries an error of at most
 // 2^-23 t.  A quotient of two numbers of 11 bits that is no tie is at least
 // 2^-19 t away from one (it is a multiple of 2^-k / 2a where the tie h is about
-// 2^-k 127), so rounding t to 21 bits first moves a tie that the error has hidden
-// back onto itself and nothing else across one.  p - (p - t) with p = 9 t is
-// that rounding.  float32 inputs: the same in float64, 2^-52 against 2^-33,
-// rounded to 40 bits.
+// 2^-k 127), so rounding t to 21 bits first (adding half of the 8 units that
+// are then cleared) moves a tie that the error has hidden back onto itself and
+// nothing else across one.  float32 inputs: the same in float64, 2^-52 against
+// 2^-33, rounded to 40 bits by p - (p - t) with p = 8193 t.
+constexpr float kInt = 0x1.8p23f;
+
 template <class T>
 struct Quotient {
     float pre, inv;
@@ -47,21 +51,24 @@ struct Quotient {
         pre = a < 0x1p-60f ? 0x1p100f : 1.0f;  // keeps 127 / a finite
         inv = 127.0f / (a * pre);
     }
-    __device__ float operator()(float x) const {
-        const float t = (x * pre) * inv;
-        const float p = t * 9.0f;
-        return rintf(p - (p - t));
+    template <bool TINY>
+    __device__ __forceinline__ uint32_t code(float x) const {
+        const float t = (TINY ? x * pre : x) * inv;
+        return __float_as_uint(__uint_as_float((__float_as_uint(t) + 4u) & ~7u) + kInt);
     }
+    __device__ bool tiny() const { return pre != 1.0f; }
 };
 template <>
 struct Quotient<float> {
     double inv;
     __device__ explicit Quotient(float a) { inv = 127.0 / double(a); }
-    __device__ float operator()(float x) const {
+    template <bool TINY>
+    __device__ __forceinline__ uint32_t code(float x) const {
         const double t = double(x) * inv;
         const double p = t * 8193.0;
-        return float(rint(p - (p - t)));
+        return __float_as_uint(float(rint(p - (p - t))) + kInt);
     }
+    __device__ bool tiny() const { return false; }
 };
 
 // 8 elements at x[c ..], zeros from cols on
@@ -74,13 +81,26 @@ __device__ __forceinline__ Eight<T> load8(const T *x, uint32_t c, uint32_t cols)
     return v;
 }
 
-// Their largest magnitude, as bits, so that a NaN or an infinity shows.
-template <class T>
-__device__ __forceinline__ uint32_t top_of(const Eight<T> &v) {
+// Their largest magnitude, as float32's bits, so that a NaN or an infinity
+// shows.  16-bit magnitudes compare as their bits, two at a time.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t top_of(const Eight<float> &v) {
     uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 8; e++) top = max(top, __float_as_uint(to_f32(v.e[e])) & 0x7FFFFFFFu);
+    for (int e = 0; e < 8; e++) top = max(top, __float_as_uint(v.e[e]) & 0x7FFFFFFFu);
     return top;
+}
+template <class T>
+__device__ __forceinline__ uint32_t top_of(const Eight<T> &v) {
+    uint32_t two[4];
+    __builtin_memcpy(two, &v, 16);
+    u16x2 top = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, two[e] & 0x7FFF7FFFu));
+    const uint16_t most = max(top[0], top[1]);
+    return __float_as_uint(to_f32(__builtin_bit_cast(T, most)));
 }
 
 __device__ __forceinline__ uint32_t wave_top(uint32_t top) {
@@ -99,14 +119,22 @@ struct Row {
         : zero(top == 0 || top >= 0x7F800000u),
           scale(top >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(top) / 127.0f),
           code(zero ? 1.0f : __uint_as_float(top)) {}
-    __device__ __forceinline__ u32x2 codes(const Eight<T> &v) const {
-        u32x2 out = {0, 0};
-        if (!zero) {
+    template <bool TINY>
+    __device__ __forceinline__ u32x2 codes_of(const Eight<T> &v) const {
+        u32x2 out;
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                out[i / 4] |= (uint32_t(int(code(to_f32(v.e[i])))) & 0xFFu) << (8 * (i % 4));
+        for (int h = 0; h < 2; h++) {
+            uint32_t c[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) c[i] = code.template code<TINY>(to_f32(v.e[4 * h + i]));
+            out[h] = __builtin_amdgcn_perm(c[1], c[0], 0x0C0C0400u) |
+                     __builtin_amdgcn_perm(c[3], c[2], 0x04000C0Cu);
         }
         return out;
+    }
+    __device__ __forceinline__ u32x2 codes(const Eight<T> &v) const {
+        if (zero) return u32x2{0, 0};
+        return code.tiny() ? codes_of<true>(v) : codes_of<false>(v);  // the same for the row
     }
 };
 
