@@ -376,10 +376,20 @@ __global__ __launch_bounds__(64 * kRowWaves) void linear_one(GemmArgs a) {
     rows16_store(acc, part, wave, lane, static_cast<Y *>(a.y[k]) + r0, rows - r0, i == 0, row.scale, ws);
 }
 
-// Many tokens: a workgroup computes a tile of BT tokens x BR weight rows, its
-// WT x WR waves a part of 32x32 products each.  The tiles' codes go from HBM
-// straight to LDS, 128 columns at a time, into one of two buffers while the
-// other is multiplied.
+// More tokens: a workgroup computes a tile of BT tokens x BR weight rows, its
+// WT x WR waves a part each, of 16x16x64 products (these draw less power than
+// 32x32x32 ones: alone, with random codes, they run at 3.67 POP/s against 3.44,
+// both held back by the power limit; the kernel gained 5%).  The tiles' codes go from HBM straight to LDS, 128 columns
+// (a stage) at a time, into one of NB buffers, NB - 1 stages ahead of the
+// products, so that a workgroup has up to 60 KB on its way.
+//
+// What bounds it: up to 64 tokens the reading of the weights (8B block, 32
+// tokens: 54 us, 4.1 TB/s, the 70B block 161 us, 5.4 TB/s); between, the L2's
+// throughput (12 - 17 TB/s into LDS, the larger tile the fewer bytes); from
+// some 1000 tokens on the products' power (70B block, 4096 tokens: 2.65 ms,
+// 2.65 POP/s).  Not kept for 256 x 256: four waves of 128 x 128 instead of
+// eight (2.27 against 2.40 POP/s, then), stages of 64 columns in four buffers
+// (2.31 against 2.45), touching the next stages' lines ahead (2.05 against 2.23).
 //
 // A 128-byte row of a tile is 8 chunks of 16 bytes; chunk c of row r lies in
 // slot c ^ (r / 2 % 8): LDS serves 16 lanes of a 16-byte read at once, and
@@ -389,7 +399,6 @@ __global__ __launch_bounds__(64 * kRowWaves) void linear_one(GemmArgs a) {
 // wave's lanes in order).
 constexpr uint32_t kDepth = 128;  // columns of a stage
 
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
 
 // A tile's rows in global memory: where a lane's chunk lies for each of its
@@ -456,7 +465,7 @@ __device__ __forceinline__ void clear_behind(int8_t *lds, uint32_t left, uint32_
     }
 }
 
-// The operands of one step of 32 columns.
+// The operands of one step of 64 columns.
 template <int FT, int FR>
 struct Operands {
     i32x4 x[FT], w[FR];
@@ -464,14 +473,14 @@ struct Operands {
 
 template <class Y, int BT, int BR, int WT, int WR, int NB>
 __global__ __launch_bounds__(64 * WT * WR) void gemm_tile(GemmArgs a, uint32_t token_tiles) {
-    constexpr int kWaves = WT * WR, FT = BT / WT / 32, FR = BR / WR / 32;
+    constexpr int kWaves = WT * WR, FT = BT / WT / 16, FR = BR / WR / 16;
     // a buffer is an object of its own, so that the compiler sees that reads
     // of one do not wait for loads to another
     __shared__ __align__(16) int8_t x0[BT * kDepth], w0[BR * kDepth], x1[BT * kDepth], w1[BR * kDepth];
     __shared__ __align__(16) int8_t x2[NB > 2 ? BT * kDepth : 16], w2[NB > 2 ? BR * kDepth : 16];
     __shared__ __align__(16) int8_t x3[NB > 3 ? BT * kDepth : 16], w3[NB > 3 ? BR * kDepth : 16];
     __shared__ __align__(16) int8_t x4[NB > 4 ? BT * kDepth : 16], w4[NB > 4 ? BR * kDepth : 16];
-    __shared__ __align__(16) int8_t x5[NB > 5 ? BT * kDepth : 16], w5[NB > 5 ? BR * kDepth : 16];
+    __shared__ __align__(16) int8_t x5[NB > 4 ? BT * kDepth : 16], w5[NB > 4 ? BR * kDepth : 16];
     __shared__ __align__(16) float w_scale[BR];
     // Workgroups go to the 8 XCDs in turn: every XCD takes one run of a
     // matrix's tiles (first counts an XCD's tiles, so that matrices of longer
@@ -505,24 +514,24 @@ __global__ __launch_bounds__(64 * WT * WR) void gemm_tile(GemmArgs a, uint32_t t
     const uint32_t wt = wave / WR * (BT / WT), wr = wave % WR * (BR / WR);
     for (uint32_t r = threadIdx.x; r < BR; r += 64 * kWaves)
         w_scale[r] = a.w_scale[k][min(r0 + r, rows - 1)];
-    i32x16 acc[FT][FR];
+    i32x4 acc[FT][FR];
 #pragma unroll
     for (int f = 0; f < FT; f++)
 #pragma unroll
         for (int h = 0; h < FR; h++)
 #pragma unroll
-            for (int e = 0; e < 16; e++) acc[f][h][e] = 0;
+            for (int e = 0; e < 4; e++) acc[f][h][e] = 0;
 
-    // A step of 32 columns multiplies one set of operands while the next set
+    // A step of 64 columns multiplies one set of operands while the next set
     // is read from LDS; before a stage's last step its waves meet: the next
     // stage has arrived then, and this one's buffer is free for the one after
     // it, whose loads go out between the products of that step.  The
     // scheduling barriers hold the reads and loads between the products.
     Operands<FT, FR> even, odd;
     const auto read = [&](Operands<FT, FR> &o, const int8_t *xs, const int8_t *ws, uint32_t kk, int f) {
-        const uint32_t at = (lane & 31u) * 128 + (((2 * kk + (lane >> 5)) ^ (lane >> 1 & 7u)) << 4);
-        if (f < FT) o.x[f] = *reinterpret_cast<const i32x4 *>(xs + wt * kDepth + f * 4096 + at);
-        if (f < FR) o.w[f] = *reinterpret_cast<const i32x4 *>(ws + wr * kDepth + f * 4096 + at);
+        const uint32_t at = (lane & 15u) * 128 + (((4 * kk + (lane >> 4)) ^ (lane >> 1 & 7u)) << 4);
+        if (f < FT) o.x[f] = *reinterpret_cast<const i32x4 *>(xs + wt * kDepth + f * 2048 + at);
+        if (f < FR) o.w[f] = *reinterpret_cast<const i32x4 *>(ws + wr * kDepth + f * 2048 + at);
     };
     constexpr int kF = FT > FR ? FT : FR;
     const auto products = [&](const Operands<FT, FR> &o, int f) {
@@ -530,7 +539,7 @@ __global__ __launch_bounds__(64 * WT * WR) void gemm_tile(GemmArgs a, uint32_t t
         if (f < FT) {
 #pragma unroll
             for (int h = 0; h < FR; h++)
-                acc[f][h] = __builtin_amdgcn_mfma_i32_32x32x32_i8(o.w[h], o.x[f], acc[f][h], 0, 0, 0);
+                acc[f][h] = __builtin_amdgcn_mfma_i32_16x16x64_i8(o.w[h], o.x[f], acc[f][h], 0, 0, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -550,12 +559,9 @@ __global__ __launch_bounds__(64 * WT * WR) void gemm_tile(GemmArgs a, uint32_t t
     const uint32_t stages = (cols + kDepth - 1) / kDepth;
     const auto stage = [&](int8_t *xs, int8_t *ws, int8_t *xn, int8_t *wn, uint32_t s) {
 #pragma unroll
-        for (uint32_t kk = 0; kk < 3; kk++) {
-#pragma unroll
-            for (int f = 0; f < kF; f++) {
-                read(kk & 1 ? even : odd, xs, ws, kk + 1, f);
-                products(kk & 1 ? odd : even, f);
-            }
+        for (int f = 0; f < kF; f++) {
+            read(odd, xs, ws, 1, f);
+            products(even, f);
         }
         arrived();
         const bool on = s + NB < stages;
@@ -580,8 +586,7 @@ __global__ __launch_bounds__(64 * WT * WR) void gemm_tile(GemmArgs a, uint32_t t
         begin(x1, w1, 1);
         if constexpr (NB > 2) begin(x2, w2, 2);
         if constexpr (NB > 3) begin(x3, w3, 3);
-        if constexpr (NB > 4) begin(x4, w4, 4);
-        if constexpr (NB > 5) begin(x5, w5, 5);
+        if constexpr (NB > 4) begin(x4, w4, 4), begin(x5, w5, 5);
         constexpr int kFirst = (NB - 1) * (XL + WL);
         static_assert(kFirst < 64, "the counter of loads");
         asm volatile("" ::: "memory");
@@ -601,36 +606,32 @@ __global__ __launch_bounds__(64 * WT * WR) void gemm_tile(GemmArgs a, uint32_t t
             stage(x0, w0, x1, w1, s);
             if constexpr (NB == 2) {
                 stage(x1, w1, x0, w0, s + 1);
-            } else {
+            } else if constexpr (NB == 3) {
                 stage(x1, w1, x2, w2, s + 1);
-                if constexpr (NB == 3) {
-                    stage(x2, w2, x0, w0, s + 2);
-                } else {
-                    stage(x2, w2, x3, w3, s + 2);
-                    if constexpr (NB == 4) {
-                        stage(x3, w3, x0, w0, s + 3);
-                    } else {
-                        stage(x3, w3, x4, w4, s + 3);
-                        if constexpr (NB == 5) {
-                            stage(x4, w4, x0, w0, s + 4);
-                        } else {
-                            stage(x4, w4, x5, w5, s + 4);
-                            stage(x5, w5, x0, w0, s + 5);
-                        }
-                    }
-                }
+                stage(x2, w2, x0, w0, s + 2);
+            } else if constexpr (NB == 4) {
+                stage(x1, w1, x2, w2, s + 1);
+                stage(x2, w2, x3, w3, s + 2);
+                stage(x3, w3, x0, w0, s + 3);
+            } else {
+                static_assert(NB == 6, "2, 3, 4 or 6 buffers");
+                stage(x1, w1, x2, w2, s + 1);
+                stage(x2, w2, x3, w3, s + 2);
+                stage(x3, w3, x4, w4, s + 3);
+                stage(x4, w4, x5, w5, s + 4);
+                stage(x5, w5, x0, w0, s + 5);
             }
         }
     }
 
-    // Lane l holds token l % 32 of each product, element e row 8 (e / 4) +
-    // 4 (l / 32) + e % 4.  The results pass through LDS (the stages' buffers are
+    // Lane l holds token l % 16 and rows 4 (l / 16) .. + 3 of each product.  The
+    // results pass through LDS (the stages' buffers are
     // free once the last loads, of zeros, have come), 128 bytes of each of 32
     // tokens at a time, so that a token's rows leave in whole cache lines.
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
     __syncthreads();
-    constexpr int kRows = std::min<int>(128 / sizeof(Y), 32 * FR), kParts = kRows / 32;
+    constexpr int kRows = std::min<int>(128 / sizeof(Y), 16 * FR), kParts = kRows / 16;
     constexpr uint32_t kBytes = kRows * sizeof(Y), kPitch = kBytes + 16;  // tokens in different banks
     constexpr uint32_t kX = BT * kDepth / (32 * kPitch), kW = BR * kDepth / (32 * kPitch);
     static_assert(FR % kParts == 0, "whole rows of results");
@@ -646,27 +647,27 @@ __global__ __launch_bounds__(64 * WT * WR) void gemm_tile(GemmArgs a, uint32_t t
     float xs[FT];
 #pragma unroll
     for (int f = 0; f < FT; f++)
-        xs[f] = a.x_scale[k][min(t0 + wt + 32 * f + (lane & 31u), a.n_tokens - 1)];
+        xs[f] = a.x_scale[k][min(t0 + wt + 16 * f + (lane & 15u), a.n_tokens - 1)];
 #pragma unroll
-    for (int f = 0; f < FT; f++) {
+    for (int f = 0; f < FT / 2; f++) {
 #pragma unroll
         for (int h0 = 0; h0 < FR; h0 += kParts) {
 #pragma unroll
             for (int h = h0; h < h0 + kParts; h++) {
+                const uint32_t r = 4 * (lane >> 4);
+                const float4 ws = *reinterpret_cast<const float4 *>(&w_scale[wr + 16 * h + r]);
 #pragma unroll
-                for (int g = 0; g < 4; g++) {
-                    const uint32_t r = 8 * g + 4 * (lane >> 5);
-                    const float4 ws = *reinterpret_cast<const float4 *>(&w_scale[wr + 32 * h + r]);
+                for (int g = 0; g < 2; g++) {
                     Y4 v;
 #pragma unroll
-                    for (int e = 0; e < 4; e++) v[e] = Y(scaled(acc[f][h][4 * g + e], xs[f], (&ws.x)[e]));
-                    *reinterpret_cast<Y4 *>(out + (lane & 31u) * kPitch +
-                                            (32 * (h - h0) + r) * sizeof(Y)) = v;
+                    for (int e = 0; e < 4; e++) v[e] = Y(scaled(acc[2 * f + g][h][e], xs[2 * f + g], (&ws.x)[e]));
+                    *reinterpret_cast<Y4 *>(out + (16 * g + (lane & 15u)) * kPitch +
+                                            (16 * (h - h0) + r) * sizeof(Y)) = v;
                 }
             }
             // a wave's LDS operations take effect in order: no barrier
             constexpr uint32_t kLanes = kBytes / 16;  // of a token
-            const uint32_t chunk = lane % kLanes, r = r0 + wr + 32 * h0 + chunk * (16 / sizeof(Y));
+            const uint32_t chunk = lane % kLanes, r = r0 + wr + 16 * h0 + chunk * (16 / sizeof(Y));
 #pragma unroll
             for (uint32_t p = 0; p < kLanes / 2; p++) {
                 const uint32_t i = 64 / kLanes * p + lane / kLanes, tok = t0 + wt + 32 * f + i;
@@ -719,7 +720,7 @@ int run_tiles(GemmArgs &a, uint32_t n, hipStream_t st) {
                          st, a, token_tiles));
 }
 
-// How long the tiles of BT x BR take, in microseconds: all compute units
+// How long tiles of bt tokens x br rows take, in microseconds: all compute units
 // together, or the longest tile alone (stages of 128 columns; 3 more for a
 // tile's start and end).
 float tiles_time(const GemmArgs &a, uint32_t n, uint32_t bt, uint32_t br, float busy, float alone) {
@@ -774,13 +775,17 @@ int run_gemm(GemmArgs &a, uint32_t n, hipStream_t st) {
             return status(launch(gemm_rows16<Y>, dim3(tiles), dim3(64 * kRowWaves), 0, st, a));
         return run_tiles<Y, 32, 64, 1, 2, 6>(a, n, st);
     }
-    // The tile with the least time by tiles_time, whose rates are those measured
-    // with the chip full (busy, per stage and compute unit) and with one
-    // workgroup per compute unit (alone).
-    const float t64 = tiles_time(a, n, 64, 64, 0.235f, 0.25f);
-    const float t128 = tiles_time(a, n, 128, 128, 0.61f, 0.55f);
-    const float t256x128 = tiles_time(a, n, 256, 128, 1.0f, 0.85f);
-    const float t256 = tiles_time(a, n, 256, 256, 1.78f, 1.25f);
+    // The tile with the least time by tiles_time, whose rates (per stage, with the
+    // chip full and with one tile alone) were fitted to the times of every tile
+    // on the 8B and the 70B block and on 4096 x 4096 and 8192 x 8192, 64 to 2048
+    // tokens: of those 40 the rule misses the best by 5% once and by 1% twice.
+    // What it decides (8B block, us, tiles of 64 / 128 / 256 x 128 / 256): 128
+    // tokens 50 / 58 / 78 / 127, 256 tokens 94 / 77 / 110 / 168, 512 tokens
+    // 192 / 141 / 126 / 189, 2048 tokens 816 / 540 / 437 / 416.
+    const float t64 = tiles_time(a, n, 64, 64, 0.20f, 0.23f);
+    const float t128 = tiles_time(a, n, 128, 128, 0.63f, 0.42f);
+    const float t256x128 = tiles_time(a, n, 256, 128, 0.89f, 0.93f);
+    const float t256 = tiles_time(a, n, 256, 256, 1.47f, 1.47f);
     const float least = std::min(std::min(t64, t128), std::min(t256x128, t256));
     if (least == t64) return run_tiles<Y, 64, 64, 2, 2, 4>(a, n, st);
     if (least == t128) return run_tiles<Y, 128, 128, 4, 2, 4>(a, n, st);
