@@ -240,6 +240,20 @@ def test_product_of_many_tokens(tokens, kind):
     p.check()
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("tokens,rows,cols", [
+    (590, 8195, 1000), (601, 8130, 130), (997, 12003, 300), (1021, 12011, 257), (1000, 12003, 385),
+    (2050, 12003, 300), (2047, 12289, 16), (2100, 11999, 641)])
+def test_product_of_large_tiles(tokens, rows, cols, kind):
+    """Enough work for tiles of 128 x 128, 256 x 128 and 256 x 256, with
+    ragged ends in every direction and odd and even numbers of stages."""
+    p = Product([(rows, cols), (70, cols + 33)], tokens, kind, seed=rows)
+    say(f"[gpu] df11_gemm_int8 {tokens} tokens {rows}x{cols} {kind}")
+    assert p.run() == ed.DF11_OK
+    torch.cuda.synchronize()
+    p.check()
+
+
 @pytest.mark.parametrize("tokens", [3, 100, 700])
 @pytest.mark.parametrize("cols", [0, 16, 100, 128, 130, 256, 257, 384, 512, 640, 1040, 2048])
 def test_product_columns(cols, tokens):
