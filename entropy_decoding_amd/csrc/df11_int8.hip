@@ -71,11 +71,21 @@ struct Quotient<float> {
     __device__ bool tiny() const { return false; }
 };
 
-// 8 elements at x[c ..], zeros from cols on
-template <class T>
+// 8 elements at x[c ..], zeros from cols on.  ONCE: they are not wanted again and
+// pass the caches by (weights of the 8B block 156 -> 124 us, and their codes
+// are still in the caches when they are multiplied; float32's two loads of a
+// lane share cache lines, and were slower that way: 199 -> 215 us).
+template <bool ONCE, class T>
 __device__ __forceinline__ Eight<T> load8(const T *x, uint32_t c, uint32_t cols) {
-    if (c + 8 <= cols) return *reinterpret_cast<const Eight<T> *>(x + c);
+    typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
     Eight<T> v;
+    if (c + 8 <= cols) {
+        if constexpr (ONCE && sizeof(T) == 2)
+            *reinterpret_cast<u32x4_any *>(&v) =
+                __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(x + c));
+        else v = *reinterpret_cast<const Eight<T> *>(x + c);
+        return v;
+    }
 #pragma unroll
     for (uint32_t i = 0; i < 8; i++) v.e[i] = c + i < cols ? x[c + i] : T(0.0f);
     return v;
@@ -167,11 +177,11 @@ __global__ __launch_bounds__(THREADS) void quantize_rows(QuantArgs a) {
     uint32_t top = 0;
 #pragma unroll
     for (int n = 0; n < kHeld; n++)
-        if (c0 + n * kPass < cols) held[n] = load8(x, c0 + n * kPass, cols);
+        if (c0 + n * kPass < cols) held[n] = load8<true>(x, c0 + n * kPass, cols);
 #pragma unroll
     for (int n = 0; n < kHeld; n++)
         if (c0 + n * kPass < cols) top = max(top, top_of(held[n]));
-    for (uint32_t c = c0 + kHeld * kPass; c < cols; c += kPass) top = max(top, top_of(load8(x, c, cols)));
+    for (uint32_t c = c0 + kHeld * kPass; c < cols; c += kPass) top = max(top, top_of(load8<false>(x, c, cols)));
     top = wave_top(top);
     if ((threadIdx.x & 63u) == 0) top_s[threadIdx.x >> 6] = top;
     __syncthreads();
@@ -186,7 +196,7 @@ __global__ __launch_bounds__(THREADS) void quantize_rows(QuantArgs a) {
         else if (c < end) *reinterpret_cast<u32x2 *>(q + c) = u32x2{0, 0};
     }
     for (uint32_t c = c0 + kHeld * kPass; c < end; c += kPass)
-        *reinterpret_cast<u32x2 *>(q + c) = row.codes(load8(x, c, cols));
+        *reinterpret_cast<u32x2 *>(q + c) = row.codes(load8<true>(x, c, cols));
 }
 
 // ---------------------------------------------------------------- product
@@ -356,9 +366,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void linear_one(GemmArgs a) {
 
     constexpr uint32_t kStep = 64 * kRowWaves * 8;
     const uint32_t own = threadIdx.x * 8;  // a thread's first elements, held for their codes
-    const Eight<X> held = load8(x, own, cols);
+    const Eight<X> held = load8<false>(x, own, cols);
     uint32_t top = top_of(held);
-    for (uint32_t c = own + kStep; c < cols; c += kStep) top = max(top, top_of(load8(x, c, cols)));
+    for (uint32_t c = own + kStep; c < cols; c += kStep) top = max(top, top_of(load8<false>(x, c, cols)));
     top = wave_top(top);
     if (lane == 0) top_s[wave] = top;
     __syncthreads();
@@ -367,7 +377,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void linear_one(GemmArgs a) {
     const Row<X> row(top);
     if (own < ((cols + 15) & ~15u)) *reinterpret_cast<u32x2 *>(codes + own) = row.codes(held);
     for (uint32_t c = own + kStep; c < ((cols + 15) & ~15u); c += kStep)
-        *reinterpret_cast<u32x2 *>(codes + c) = row.codes(load8(x, c, cols));
+        *reinterpret_cast<u32x2 *>(codes + c) = row.codes(load8<false>(x, c, cols));
     __syncthreads();
 
     const i32x4 acc = rows16_sum(runs, w, wave * 128 + 16 * q, wave * 128, cols, [&](uint32_t c) {
