@@ -279,6 +279,34 @@ def test_large_tensor_chunks():
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+def test_more_than_2_32_elements(bits):
+    """A tensor of 2^32 + 12345 elements beside a small one: the places around
+    2^31, 2^32 and the end get what the same elements get in the small tensor."""
+    n, blocks = 2 ** 32 + 12345, 16
+    small = blocks * 256
+    g = torch.Generator(device="cuda").manual_seed(5)
+    w = torch.randn(small, device="cuda", generator=g).mul_(0.02).bfloat16()
+    gr = torch.randn(small, device="cuda", generator=g).mul_(1e-3).bfloat16()
+    big_w, big_g = (torch.zeros(n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    places = [0, 2 ** 31 - 2048, 2 ** 32 - 2048, (n - small) // 256 * 256]
+    for p in places:
+        big_w[p:p + small], big_g[p:p + small] = w, gr
+    opt = ed.AdamW([big_w, w], [big_g, gr], state_bits=bits, lr=1e-2, betas=BETAS)
+    say(f"[gpu] df11_adamw_step of {n} elements, bits={bits}")
+    norm = opt.step(max_norm=1e-2)
+    torch.cuda.synchronize()
+    want = math.sqrt((len(places) + 1) * float(gr.double().square().sum()))
+    assert abs(float(norm[0]) - want) <= want * 1.01 * U
+    for p in places:
+        assert torch.equal(big_w[p:p + small], w), p
+        for name in ("m", "v"):
+            big, part = opt.state[name]
+            assert torch.equal(big[p:p + small], part), (p, name)
+    assert not big_w[small:2 ** 31 - 2048].any() and not big_w[2 ** 32 + small:places[-1]].any()
+    assert not big_w[places[-1] + small:].any()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_zero_states_and_zero_gradients(bits):
     grads = [np.zeros(600, f32), np.concatenate([np.zeros(300, f32), np.full(300, 1e-4, f32)])]
     case = Case([600, 600], "bf16", "f32", True, bits, seed=5, grads=grads, zero_state=True)

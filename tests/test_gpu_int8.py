@@ -279,6 +279,46 @@ def test_sums_are_exact_at_the_limit(tokens):
     p.check()
 
 
+def far_product(rows, cols, tokens, kind, sample):
+    """Large operands made on the device; rows and tokens of `sample` compared."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    w = torch.randint(-127, 128, (rows, cols), dtype=torch.int8, device="cuda", generator=g)
+    x = torch.randint(-127, 128, (tokens, cols), dtype=torch.int8, device="cuda", generator=g)
+    sw = torch.rand(rows, device="cuda", generator=g) + 0.5
+    sx = torch.rand(tokens, device="cuda", generator=g) + 0.5
+    y = torch.empty(tokens, rows, dtype=KINDS[kind], device="cuda")
+    t = (ed.df11_int8_tensor * 1)()
+    a = t[0]
+    a.w, a.w_scale, a.x, a.x_scale, a.y = (v.data_ptr() for v in (w, sw, x, sx, y))
+    a.w_stride = a.x_stride = cols
+    a.y_stride, a.rows, a.cols = rows, rows, cols
+    say(f"[gpu] df11_gemm_int8 {tokens} tokens {rows}x{cols} {kind}, beyond 32 bits")
+    assert ed.LIB.df11_gemm_int8(ed.TYPES[str(KINDS[kind])[6:]], t, 1, tokens, None) == ed.DF11_OK
+    torch.cuda.synchronize()
+    r, s = (torch.tensor([i % n for i in sample], device="cuda") for n in (rows, tokens))
+    _, want = product(x[s].cpu().numpy(), w[r].cpu().numpy(), sx[s].cpu().numpy(), sw[r].cpu().numpy(), kind)
+    assert torch.equal(y[s][:, r].cpu(), want)
+
+
+@pytest.mark.parametrize("rows,cols,tokens", [
+    (140_000, 32_000, 1), (140_000, 32_000, 30), (140_000, 32_000, 50),  # weights of 4.5 GB
+    (40_000, 16, 70_000),  # 2.8 G results
+    (300, 32_000, 140_000)])  # activations of 4.5 GB
+def test_offsets_beyond_32_bits(rows, cols, tokens):
+    far_product(rows, cols, tokens, "bf16", [0, 1, 17, -1, -2, -300, 2 ** 17 + 3, 67_200, 134_300])
+
+
+def test_quantiser_offsets_beyond_32_bits():
+    x = torch.randn(1, 40_000, device="cuda").bfloat16().repeat(120_000, 1)  # 4.8 G elements
+    x[-1] *= 2
+    say("[gpu] df11_quantize_int8 of 4.8 G elements")
+    (codes, scales), = ed.quantize_int8([x])
+    want, sc = reference_codes(x[:1].cpu())
+    for r in (0, 60_000, 107_380, 119_998, 119_999):
+        assert np.array_equal(codes[r].cpu().numpy(), want[0]), r
+        assert float(scales[r]) == float(sc[0]) * (2 if r == 119_999 else 1)
+
+
 @pytest.mark.parametrize("tokens", [1, 9, 66, 600])
 def test_random_sizes(tokens):
     rng = np.random.default_rng(30 + tokens)
@@ -412,9 +452,10 @@ def test_update_requantise_multiply():
         assert torch.equal(y, z)
 
 
-@pytest.mark.parametrize("tokens", [1, 40, 400])
-def test_replayed_from_a_graph(tokens):
-    shapes = [(96, 200), (300, 528)]
+@pytest.mark.parametrize("tokens,shapes", [
+    (1, [(96, 200), (300, 528)]), (40, [(96, 200), (300, 528)]), (400, [(96, 200), (300, 528)]),
+    (2050, [(12003, 300)])])
+def test_replayed_from_a_graph(tokens, shapes):
     layer = ed.Int8Linear.from_tensors([torch.randn(*s, device="cuda") for s in shapes])
     xs = [torch.randn(tokens, c, device="cuda").bfloat16() for _, c in shapes]
     out = [torch.empty(tokens, r, dtype=torch.bfloat16, device="cuda") for r, _ in shapes]
