@@ -1073,7 +1073,7 @@ class AdamW:
     ``weight_decay`` and ``lr_scale``: one number, or one per tensor.  ``step``:
     steps already made.  ``device_step``: keep the step's number on the device
     too (``self.d_step``) and advance it there, so that a captured step counts
-    on when it is replayed.
+    on when it is replayed.  Used from one host thread at a time.
     """
 
     def __init__(self, weights, grads, masters=None, state_bits: int = 32, state=None,

@@ -1,5 +1,13 @@
 // Products in 8-bit integers: rows quantised to codes with a scale each, and
 // the product of activation codes with weight codes on the matrix cores.
+//
+//   y[t][r] = (float(sum_c x[t][c] w[r][c]) * x_scale[t]) * w_scale[r]
+//
+// The sum is exact in int32, so the result is the same however the columns and
+// tiles are split; three forms share the work:
+//   linear_one   one token, quantised on the way: workgroups of 16 rows
+//   gemm_rows16  up to 16 tokens and few rows: the same on codes
+//   gemm_tile    everything else: tiles through LDS, 32 x 64 to 256 x 256
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -159,7 +167,11 @@ struct QuantArgs {
 
 // One workgroup per row: the largest magnitude, then the codes.  The first kHeld
 // times 8 elements of a thread stay in its registers between the two; what a
-// longer row has beyond comes from the caches the second time.
+// longer row has beyond comes from the caches the second time.  Bound by HBM:
+// the 8B block's weights take 121 - 126 us from BF16 (5.2 - 5.4 TB/s) and 199 us
+// from float32 (5.5 TB/s).  A wave per row (193 us, BF16 then at 158), workgroups
+// that stay and load the next row ahead (200 us and more), 512 or 1024 threads
+// for rows of 14336 (168 and 256 us against 121) were slower.
 constexpr int kHeld = 4;
 
 template <class T, int THREADS>
@@ -338,7 +350,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void gemm_rows16(GemmArgs a) {
 // One token that is not quantised yet: every workgroup quantises it for itself
 // while its first weights are on their way, which spares the launch before.
 // Bound by reading the weights: 46.3 us on the 8B block (4.7 TB/s) and 156 us on
-// the 70B block (5.5 TB/s), 4.8 us on 1024 x 1024, against 55.2, 165 and 7.2 us
+// the 70B block (5.5 TB/s), 4.5 us on 1024 x 1024, against 55.2, 165 and 7.2 us
 // with a launch for the codes before.  Holding the kernel to 80 or 64 registers
 // for more waves made it slower (8B block 59 and 79 us): its loads in flight
 // need them.
@@ -706,6 +718,8 @@ bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 int status(hipError_t e) { return e == hipSuccess ? DF11_OK : DF11_E_HIP; }
 
+// Few long rows: 1024 threads each, so that a row's time counts less (3 rows of
+// 28058: 28 -> 26 us for the whole of quantiser and product).
 template <class T>
 int run_rows(const QuantArgs &a, uint32_t rows, uint32_t longest, hipStream_t st) {
     if (rows <= 512 && longest > 2048)
@@ -792,7 +806,7 @@ int run_gemm(GemmArgs &a, uint32_t n, hipStream_t st) {
     // The tile with the least time by tiles_time, whose rates (per stage, with the
     // chip full and with one tile alone) were fitted to the times of every tile
     // on the 8B and the 70B block and on 4096 x 4096 and 8192 x 8192, 64 to 2048
-    // tokens: of those 40 the rule misses the best by 5% once and by 1% twice.
+    // tokens: of those 40 the rule misses the best by 4% once and by 1% twice.
     // What it decides (8B block, us, tiles of 64 / 128 / 256 x 128 / 256): 128
     // tokens 50 / 58 / 78 / 127, 256 tokens 94 / 77 / 110 / 168, 512 tokens
     // 192 / 141 / 126 / 189, 2048 tokens 816 / 540 / 437 / 416.
