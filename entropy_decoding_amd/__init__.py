@@ -894,31 +894,38 @@ class Int8Linear:
     channel, multiplied with activations that are quantised token by token
     (df11_linear_int8: two launches a call).
 
-    ``codes``: int8 device tensors [rows, stride], 16-byte aligned with strides
-    that are multiples of 16; ``scales``: float32 [rows]; ``shapes``: (rows,
-    cols) of each matrix.
+    ``codes``: int8 device tensors [rows, at least cols rounded up to 16];
+    ``scales``: float32 [rows]; ``shapes``: (rows, cols) of each matrix.  Codes
+    whose rows start on cache lines (quantize_int8's do) are kept as they are;
+    others are copied here, on the current stream, to rows that do.
     """
 
     def __init__(self, codes, scales, shapes):
         import torch
 
-        self.codes = _matrices(codes, "codes")
+        codes = _matrices(codes, "codes")
         self.scales, self.shapes = list(scales), [(int(r), int(c)) for r, c in shapes]
-        self.device = self.codes[0].device
-        if not len(self.codes) == len(self.scales) == len(self.shapes):
+        self.device = codes[0].device
+        if not len(codes) == len(self.scales) == len(self.shapes):
             raise ValueError("one codes tensor, scales tensor and shape per matrix")
-        self._t = (df11_int8_tensor * len(self.codes))()
+        self._t = (df11_int8_tensor * len(codes))()
         self._bytes = {}  # scratch for a number of tokens
-        for a, q, s, (r, c) in zip(self._t, self.codes, self.scales, self.shapes):
-            if q.dtype != torch.int8 or q.size(0) != r or q.size(1) < c or (r > 1 and q.stride(0) < c):
+        self._held = []   # the codes that the calls read
+        for a, q, s, (r, c) in zip(self._t, codes, self.scales, self.shapes):
+            if q.dtype != torch.int8 or q.size(0) != r or q.size(1) < c:
                 raise ValueError("codes must be int8 of the shape's rows and at least its columns")
             if s.dtype != torch.float32 or s.numel() != r or not s.is_contiguous() or s.device != self.device:
                 raise ValueError("scales must be float32, one per row")
             # the product reads whole groups of 16 columns
-            stride = q.stride(0) if r > 1 else q.size(1)
-            if stride < (c + 15) // 16 * 16 or q.size(1) < (c + 15) // 16 * 16:
+            whole = (c + 15) // 16 * 16
+            if q.size(1) < whole:
                 raise ValueError("codes must reach to the next multiple of 16 columns")
-            a.w, a.w_scale, a.w_stride, a.rows, a.cols = q.data_ptr(), s.data_ptr(), stride, r, c
+            if q.data_ptr() % 128 or (r > 1 and q.stride(0) % 128):
+                lines = torch.empty((r, (c + 127) // 128 * 128), dtype=torch.int8, device=self.device)
+                q = lines[:, :whole].copy_(q[:, :whole])
+            self._held.append(q)
+            a.w, a.w_scale, a.rows, a.cols = q.data_ptr(), s.data_ptr(), r, c
+            a.w_stride = q.stride(0) if r > 1 else whole
 
     @classmethod
     def from_tensors(cls, tensors, stream=None):

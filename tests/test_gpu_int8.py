@@ -492,6 +492,22 @@ def test_two_streams():
             assert all(torch.equal(p.cpu(), q) for p, q in zip(a, b))
 
 
+@pytest.mark.parametrize("offset,stride", [(0, 128), (8, 32), (16, 48), (3, 37), (128, 37), (0, 144)])
+def test_linear_takes_codes_anywhere(offset, stride):
+    """Rows that do not start on cache lines are laid out anew."""
+    w = torch.randn(6, 20).bfloat16()
+    (codes, scales), = ed.quantize_int8([w.cuda()])
+    room = torch.full((offset + 6 * stride,), 77, dtype=torch.int8, device="cuda")
+    held = room[offset:].view(6, stride)[:, :32]
+    held.copy_(codes)
+    x = torch.randn(3, 20).bfloat16()
+    say(f"[gpu] Int8Linear of codes at {offset}, stride {stride}")
+    y, = ed.Int8Linear([held], [scales], [(6, 20)])([x.cuda()], torch.float32)
+    assert torch.equal(y.cpu(), linear_reference(x, w, "f32"))
+    one, = ed.Int8Linear([held[:1]], [scales[:1]], [(1, 20)])([x.cuda()], torch.float32)
+    assert torch.equal(one, y[:, :1])
+
+
 def test_no_tokens():
     layer = ed.Int8Linear.from_tensors([torch.randn(5, 20, device="cuda")])
     say("[gpu] Int8Linear of no tokens")
@@ -527,7 +543,4 @@ def test_binding_refuses():
         ed.Int8Linear([codes.float()], [scales], [(6, 20)])
     with pytest.raises(ValueError):
         ed.quantize_int8([w] * 17)
-    off = torch.zeros(6 * 32 + 16, dtype=torch.int8, device="cuda")[8:8 + 6 * 32].view(6, 32)
-    with pytest.raises(ed.Df11Error):
-        ed.Int8Linear([off], [scales], [(6, 20)])([x])
     assert ctypes.sizeof(ed.df11_int8_tensor) == 72
