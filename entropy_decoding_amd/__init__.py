@@ -1212,9 +1212,12 @@ class AdamW:
     def compressed_sizes(self) -> df11_sizes:
         """What the weights of the last step would take as one compressed unit
         (payload bits, arrays), from ``counts``: whether, and into how much
-        memory, to encode them.  Waits for the step."""
+        memory, to encode them.  Waits for the step, whatever its stream."""
+        import torch
+
         if self.counts is None or not self.steps:
             raise ValueError("counts are kept by steps of AdamW(counts=True)")
+        torch.cuda.synchronize(self.device)
         counts = self.counts.sum(0).cpu().numpy().view(np.uint64)
         cb, sz = df11_build_codebook_from_counts(counts), df11_sizes()
         _check("df11_encode_size_from_counts",
@@ -1225,7 +1228,12 @@ class AdamW:
         return sz
 
     def compress(self, stream=None):
-        """The BF16 weights as one compressed unit: encode_on_device's (DeviceStream, codebook)."""
+        """The BF16 weights as one compressed unit: encode_on_device's
+        (DeviceStream, codebook).  Waits for the steps before it, whatever their
+        stream: the codebook must be that of the weights that are encoded."""
+        import torch
+
+        torch.cuda.synchronize(self.device)
         return encode_on_device(self.weights, stream=stream)
 
 

@@ -607,3 +607,32 @@ def test_update_then_compress():
     assert int(status.item()) == 0
     assert torch.equal(out.view(torch.int16), unit.view(torch.int16))
     assert not torch.equal(unit, before)
+
+
+@pytest.mark.parametrize("sizes_first", [True, False])
+def test_compressing_waits_for_a_step_on_another_stream(sizes_first):
+    w = (torch.randn(200_000, device="cuda") * 0.02).bfloat16()
+    g = torch.randn(200_000, device="cuda").bfloat16()
+    opt = ed.AdamW([w], [g], counts=True, lr=0.5)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    a = torch.randn(4096, 4096, device="cuda")
+    say("[gpu] AdamW step behind products on another stream, then its sizes and unit")
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(20):  # some ten milliseconds before the step
+            b = a @ a
+    opt.step(stream=side)
+    if sizes_first:
+        sz = opt.compressed_sizes()
+        counts = np.bincount((w.view(torch.int16).cpu().numpy().view(np.uint16).astype(np.int64) >> 7)
+                             & 0xFF, minlength=256)
+        assert np.array_equal(opt.counts[0].cpu().numpy(), counts)
+        assert int(sz.n_weights) == w.numel()
+    new, _ = opt.compress()
+    out, status = torch.empty_like(w), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ed.df11_decompress_block(new, out, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert torch.equal(out.view(torch.int16), w.view(torch.int16))
+    del b
