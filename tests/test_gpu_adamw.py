@@ -636,3 +636,13 @@ def test_compressing_waits_for_a_step_on_another_stream(sizes_first):
     assert int(status.item()) == 0
     assert torch.equal(out.view(torch.int16), w.view(torch.int16))
     del b
+
+
+def test_weights_that_overlap_are_refused():
+    flat = torch.zeros(300, device="cuda")
+    g = [torch.zeros(n, device="cuda") for n in (100, 100, 0)]
+    say("[gpu] AdamW of weights that overlap")
+    for pair in ([flat[:100], flat[:100]], [flat[50:150], flat[:100]], [flat[:100], flat[99:199]]):
+        with pytest.raises(ValueError, match="overlap"):
+            ed.AdamW(pair, g[:2])
+    ed.AdamW([flat[100:200], flat[:100], flat[50:50]], g).step()  # side by side, and an empty one
