@@ -531,10 +531,15 @@ uint64_t total(const df11_adamw_tensor *t, uint32_t n) {
 }
 
 // Elements per workgroup: as many as leave about `groups` workgroups, between
-// one iteration and `most`.
-uint32_t chunk_for(uint64_t elements, uint64_t groups, uint32_t most) {
+// one iteration and `most`; more where a tensor would have 2^23 chunks (a grid
+// holds less than 2^32 threads).
+constexpr uint32_t kMaxChunks = (1u << 24) - 1;
+uint32_t chunk_for(const df11_adamw_tensor *t, uint32_t n, uint64_t groups, uint32_t most) {
+    const uint64_t elements = total(t, n);
+    uint64_t longest = 0;
+    for (uint32_t k = 0; k < n; k++) longest = t[k].numel > longest ? t[k].numel : longest;
     uint32_t c = kStep;
-    while (c < most && elements / c > groups) c *= 2;
+    while ((c < most && elements / c > groups) || (c < 1u << 30 && longest / c >= 1u << 23)) c *= 2;
     return c;
 }
 
@@ -551,7 +556,7 @@ int each_table(const df11_adamw_tensor *t, uint32_t n, uint32_t chunk, Fill fill
         for (; k < n && used < kMaxTensors; k++) {
             if (!t[k].numel) continue;
             const uint64_t more = (t[k].numel + chunk - 1) / chunk;
-            if (chunks + more > 0x7FFFFFFFu) break;
+            if (chunks + more > kMaxChunks) break;
             a.first[used] = uint32_t(chunks);
             a.t[used].n = t[k].numel;
             fill(a.t[used], k);
@@ -654,7 +659,7 @@ int df11_adamw_step(const df11_adamw_config *c, const df11_adamw_tensor *t, uint
                 return DF11_E_HIP;
         }
     }
-    return each_table(t, n_tensors, chunk_for(total(t, n_tensors), 2048, 8 * kStep), fill,
+    return each_table(t, n_tensors, chunk_for(t, n_tensors, 2048, 8 * kStep), fill,
                       [&](const Table &a, uint32_t grid, uint32_t) {
                           if (!w16) return pick_step<float, false, false>(a, grid, num, st, g16, s8);
                           if (masters)
@@ -685,7 +690,7 @@ int df11_adamw_values(const df11_adamw_tensor *t, uint32_t n_tensors, uint32_t t
         a.w = m_out ? m_out[k] : nullptr;
         a.master = v_out ? static_cast<float *>(v_out[k]) : nullptr;
     };
-    return each_table(t, n_tensors, chunk_for(total(t, n_tensors), 2048, 8 * kStep), fill,
+    return each_table(t, n_tensors, chunk_for(t, n_tensors, 2048, 8 * kStep), fill,
                       [&](const Table &a, uint32_t grid, uint32_t) {
                           return status(type == DF11_TYPE_BF16
                                             ? launch(state_values<__bf16>, dim3(grid), dim3(kThreads), 0, st, a)
@@ -695,7 +700,7 @@ int df11_adamw_values(const df11_adamw_tensor *t, uint32_t n_tensors, uint32_t t
 
 uint64_t df11_grad_norm_scratch_bytes(const df11_adamw_tensor *t, uint32_t n_tensors) {
     if (!t) return 8;
-    const uint32_t chunk = chunk_for(total(t, n_tensors), 4096, 64 * kStep);
+    const uint32_t chunk = chunk_for(t, n_tensors, 4096, 64 * kStep);
     uint64_t parts = 0;
     for (uint32_t k = 0; k < n_tensors; k++) parts += (t[k].numel + chunk - 1) / chunk;
     return 8 * (parts ? parts : 1);
@@ -716,7 +721,7 @@ int df11_grad_norm(uint32_t g_type, const df11_adamw_tensor *t, uint32_t n_tenso
     double *parts = static_cast<double *>(scratch);
     uint64_t done = 0;
     const int rc = each_table(
-        t, n_tensors, chunk_for(total(t, n_tensors), 4096, 64 * kStep),
+        t, n_tensors, chunk_for(t, n_tensors, 4096, 64 * kStep),
         [&](Tensor &a, uint32_t k) { a.g = t[k].g; },
         [&](const Table &a, uint32_t grid, uint32_t) {
             double *p = parts + done;

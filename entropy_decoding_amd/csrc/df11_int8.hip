@@ -718,6 +718,9 @@ bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 int status(hipError_t e) { return e == hipSuccess ? DF11_OK : DF11_E_HIP; }
 
+// a grid holds less than 2^32 threads
+bool too_many(uint64_t groups, uint32_t threads) { return groups * threads >> 32; }
+
 // Few long rows: 1024 threads each, so that a row's time counts less (3 rows of
 // 28058: 28 -> 26 us for the whole of quantiser and product).
 template <class T>
@@ -742,7 +745,7 @@ int run_tiles(GemmArgs &a, uint32_t n, hipStream_t st) {
     for (uint32_t k = 0; k < n; k++) {
         a.first[k] = uint32_t(turns);
         turns += (uint64_t((a.rows[k] + BR - 1) / BR) * token_tiles + 7) / 8;
-        if (turns > 0x0FFFFFFFu) return DF11_E_INVALID;
+        if (too_many(turns * 8, 64 * WT * WR)) return DF11_E_INVALID;
     }
     return status(launch(gemm_tile<Y, BT, BR, WT, WR, NB>, dim3(uint32_t(turns) * 8), dim3(64 * WT * WR), 0,
                          st, a, token_tiles));
@@ -778,6 +781,7 @@ int run_one(GemmArgs &a, uint32_t n, hipStream_t st) {
     uint32_t cols = 0;
     for (uint32_t k = 0; k < n; k++) cols = std::max(cols, a.cols[k]);
     const uint32_t tiles = sixteens(a, n);
+    if (too_many(tiles, 64 * kRowWaves)) return DF11_E_INVALID;
     return status(launch(linear_one<X, Y>, dim3(tiles), dim3(64 * kRowWaves), (cols + 15) & ~15u, st, a));
 }
 
@@ -799,7 +803,7 @@ int run_gemm(GemmArgs &a, uint32_t n, hipStream_t st) {
         // read too much of the activations (8B block: 43.4 against 48.0 us
         // with 1 token, but 48.4 against 48.6 with 4 and 66 against 51 with 16).
         const uint32_t tiles = sixteens(a, n);
-        if (a.n_tokens == 1 || (a.n_tokens <= 16 && tiles <= 256))
+        if ((a.n_tokens == 1 && !too_many(tiles, 64 * kRowWaves)) || (a.n_tokens <= 16 && tiles <= 256))
             return status(launch(gemm_rows16<Y>, dim3(tiles), dim3(64 * kRowWaves), 0, st, a));
         return run_tiles<Y, 32, 64, 1, 2, 6>(a, n, st);
     }
@@ -888,7 +892,7 @@ int df11_quantize_int8(uint32_t src_type, const df11_int8_rows *m, uint32_t n,
         longest = std::max(longest, x.cols);
         rows += x.rows;
         used++;
-        if (rows > 0x7FFFFFFFu) return DF11_E_INVALID;
+        if (too_many(rows, 256)) return DF11_E_INVALID;
     }
     if (!rows) return DF11_OK;
     hipStream_t st = static_cast<hipStream_t>(stream);

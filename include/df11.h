@@ -670,9 +670,10 @@ int df11_grad_norm(uint32_t g_type, const df11_adamw_tensor *t, uint32_t n_tenso
  * codes[r * code_stride ..], followed by zero codes up to the next multiple
  * of 16 columns.  Strides are in elements.  src needs its element's alignment
  * only; codes 16-byte aligned; code_stride a multiple of 16 and at least
- * cols; scales 4-byte aligned.  Outputs must not overlap anything.
- * Asynchronous.  Errors: DF11_E_INVALID (null or misaligned pointers, src_type,
- * n, strides, cols above DF11_INT8_MAX_COLS), DF11_E_HIP.
+ * cols; scales 4-byte aligned.  All matrices together have less than 2^24
+ * rows.  Outputs must not overlap anything.  Asynchronous.  Errors:
+ * DF11_E_INVALID (null or misaligned pointers, src_type, n, strides, rows, cols
+ * above DF11_INT8_MAX_COLS), DF11_E_HIP.
  */
 #define DF11_INT8_MAX_TENSORS 16
 #define DF11_INT8_MAX_COLS 131071u        /* 128 * 128 * 131071 < 2^31 */
@@ -702,8 +703,9 @@ int df11_quantize_int8(uint32_t src_type, const df11_int8_rows *m, uint32_t n, d
  * DF11_INT8_MAX_STRIDE; codes behind cols in a row may be anything, but are
  * read up to the next multiple of 16.  y needs its element's alignment only,
  * y_stride at least rows; elements of y between rows and y_stride are left as
- * they were.  y must not overlap anything.  cols 0 gives zeros times the
- * scales.  One launch on st, asynchronous, no workspace; the result does not
+ * they were.  y must not overlap anything.  rows up to 2^24, n_tokens up to
+ * 2^20, and no more results than the tiles of one grid of 2^32 threads cover
+ * (2^35 always fit).  cols 0 gives zeros times the scales.  One launch on st, asynchronous, no workspace; the result does not
  * depend on how the work is split.  Errors: DF11_E_INVALID (null or misaligned
  * pointers, y_type, n_tensors, strides, sizes), DF11_E_HIP.
  */

@@ -111,6 +111,13 @@ def test_norm_scratch_covers_every_chunk():
         assert L.df11_grad_norm_scratch_bytes(tensor(numel=numel), 1) >= 8 * max(1, numel // 65536)
 
 
+def test_long_tensors_have_few_enough_chunks():
+    """A workgroup of 256 threads a chunk, less than 2^32 threads a grid."""
+    for numel in (2 ** 36, 2 ** 39 + 1, 2 ** 40):
+        parts = L.df11_grad_norm_scratch_bytes(tensor(numel=numel), 1) // 8
+        assert numel / 2 ** 30 <= parts <= 2 ** 23
+
+
 def test_structs_match_the_header(tmp_path):
     names = [f for f, _ in ed.df11_adamw_tensor._fields_], [f for f, _ in ed.df11_adamw_config._fields_]
     body = "".join(f'printf("%zu ", offsetof({s}, {f}));' for s, fs in

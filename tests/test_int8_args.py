@@ -51,6 +51,24 @@ def test_quantiser_refuses_lists():
     assert L.df11_quantize_int8(1, many, 2, None) == ed.DF11_E_INVALID
 
 
+@pytest.mark.parametrize("kind", [0, 1, 2])
+def test_more_rows_than_a_grid_holds_are_refused(kind):
+    """One workgroup of 256 threads a row: 2^24 rows would be 2^32 threads."""
+    assert L.df11_quantize_int8(kind, rows(rows=1 << 24), 1, None) == ed.DF11_E_INVALID
+    half = (ed.df11_int8_rows * 2)(*[rows(rows=1 << 23)[0]] * 2)
+    assert L.df11_quantize_int8(kind, half, 2, None) == ed.DF11_E_INVALID
+
+
+@pytest.mark.parametrize("kind", [0, 1, 2])
+def test_more_tiles_than_a_grid_holds_are_refused(kind):
+    """2^24 rows and 2^20 tokens are 2^28 tiles of 256 x 256, 512 threads each."""
+    t = tensor(rows=1 << 24, y_stride=1 << 24)
+    assert L.df11_gemm_int8(kind, t, 1, 1 << 20, None) == ed.DF11_E_INVALID
+    many = (ed.df11_int8_tensor * 16)(*[t[0]] * 16)  # 2^24 workgroups of 16 rows
+    nbytes = L.df11_linear_int8_scratch_bytes(many, 16, 1)
+    assert linear(many, 16, kind, kind, 1, 4096, nbytes) == ed.DF11_E_INVALID
+
+
 def test_quantiser_of_nothing():
     assert L.df11_quantize_int8(1, None, 0, None) == ed.DF11_OK
     assert L.df11_quantize_int8(1, rows(rows=0, src=0, codes=0, scales=0), 1, None) == ed.DF11_OK
