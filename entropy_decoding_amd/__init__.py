@@ -920,7 +920,7 @@ class Int8Linear:
             whole = (c + 15) // 16 * 16
             if q.size(1) < whole:
                 raise ValueError("codes must reach to the next multiple of 16 columns")
-            if q.data_ptr() % 128 or (r > 1 and q.stride(0) % 128):
+            if q.data_ptr() % 128 or (r > 1 and (q.stride(0) % 128 or q.stride(0) < whole)):
                 lines = torch.empty((r, (c + 127) // 128 * 128), dtype=torch.int8, device=self.device)
                 q = lines[:, :whole].copy_(q[:, :whole])
             self._held.append(q)
@@ -930,6 +930,7 @@ class Int8Linear:
     @classmethod
     def from_tensors(cls, tensors, stream=None):
         """Quantises weight matrices (BF16, F16 or float32, [rows, cols])."""
+        tensors = list(tensors)
         held = quantize_int8(tensors, stream)
         return cls([q for q, _ in held], [s for _, s in held], [tuple(t.shape) for t in tensors])
 
@@ -939,6 +940,9 @@ class Int8Linear:
         follow one another in it."""
         import torch
 
+        shapes = [(int(r), int(c)) for r, c in shapes]
+        if not 1 <= len(shapes) <= DF11_INT8_MAX_TENSORS:
+            raise ValueError(f"1 to {DF11_INT8_MAX_TENSORS} matrices")
         if sum(r * c for r, c in shapes) != ds.n_weights or ds.desc.format != 0:
             raise ValueError("the shapes must tile a BF16 unit")
         guard, st = _on(ds.stream.device, stream)

@@ -508,6 +508,19 @@ def test_linear_takes_codes_anywhere(offset, stride):
     assert torch.equal(one, y[:, :1])
 
 
+def test_linear_takes_one_row_of_codes_for_all():
+    """Codes and scales of one row, broadcast over the matrix."""
+    w = torch.randn(1, 200).bfloat16()
+    (codes, scales), = ed.quantize_int8([w.cuda()])
+    x = torch.randn(4, 200).bfloat16()
+    say("[gpu] Int8Linear of broadcast codes")
+    layer = ed.Int8Linear([codes.expand(9, -1)], [scales.expand(9).contiguous()], [(9, 200)])
+    y, = layer([x.cuda()], torch.float32)
+    assert torch.equal(y.cpu(), linear_reference(x, w.expand(9, -1), "f32"))
+    again, = ed.Int8Linear.from_tensors(iter([w.cuda().expand(9, -1).contiguous()]))([x.cuda()], torch.float32)
+    assert torch.equal(again, y)
+
+
 def test_no_tokens():
     layer = ed.Int8Linear.from_tensors([torch.randn(5, 20, device="cuda")])
     say("[gpu] Int8Linear of no tokens")

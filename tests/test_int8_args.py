@@ -122,6 +122,16 @@ def test_linear_refuses_scratch_and_types():
     assert linear(many, 17) == ed.DF11_E_INVALID
 
 
+@pytest.mark.parametrize("change", [
+    {"w": 0}, {"x": 0}, {"x": 16385}, {"w_scale": 0}, {"y": 0}, {"y": 65537}, {"w_stride": 40},
+    {"y_stride": 19}, {"cols": 131072}])
+def test_linear_of_one_token_refuses(change):
+    assert linear(tensor(**change), tokens=1) == ed.DF11_E_INVALID
+    for bad in ({"x_kind": 3}, {"y_kind": 3}, {"scratch": 0}, {"nbytes": 15}):
+        assert linear(tensor(), tokens=1, **bad) == ed.DF11_E_INVALID
+    assert linear(tensor(x=16386), x_kind=0, tokens=1) == ed.DF11_E_INVALID
+
+
 def test_linear_of_nothing():
     assert linear(None, 0) == ed.DF11_OK
     assert linear(tensor(), tokens=0) == ed.DF11_OK
