@@ -886,7 +886,9 @@ def quantize_int8(tensors, stream=None):
     tensors = _matrices(tensors, "matrices")
     guard, st = _on(tensors[0].device, stream)
     with guard:
-        return _quantize(tensors, st)
+        out = _quantize(tensors, st)
+    _lend(tensors[0].device, stream, tensors)
+    return out
 
 
 class Int8Linear:
@@ -1004,6 +1006,8 @@ class Int8Linear:
             scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
             _check("df11_linear_int8",
                    LIB.df11_linear_int8(x_type, y_type, t, n, n_tokens, scratch.data_ptr(), need, st))
+        if stream is not None:
+            _lend(self.device, stream, [*xs, *out, *self._held, *self.scales])
         return out
 
 
@@ -1055,6 +1059,24 @@ class _AsIs:
 _AS_IS = _AsIs()
 
 
+def _stream_of(device, stream):
+    """A stream object, or a stream's handle, as torch's stream."""
+    import torch
+
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+
+
+def _lend(device, stream, tensors):
+    """Keeps the memory of tensors that a call on ``stream`` uses from another
+    use before that call is done, when they are freed earlier on their own stream."""
+    if stream is not None:
+        stream = _stream_of(device, stream)
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _on(device, stream):
     """(a guard that makes ``stream``, or the device's current stream, and the
     device current; the stream's handle)."""
@@ -1063,8 +1085,7 @@ def _on(device, stream):
     if stream is None:
         guard = _AS_IS if torch.cuda.current_device() == device.index else torch.cuda.device(device)
         return guard, torch._C._cuda_getCurrentRawStream(device.index)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    stream = _stream_of(device, stream)
     if stream.device != device:
         raise ValueError(f"the stream is not on {device}")
     return torch.cuda.stream(stream), stream.cuda_stream
@@ -1154,7 +1175,9 @@ class AdamW:
         """A float32 device tensor [norm, clip factor] of all gradients together."""
         guard, st = _on(self.device, stream)
         with guard:
-            return self._norm(max_norm, st)
+            out = self._norm(max_norm, st)
+        _lend(self.device, stream, self.grads)
+        return out
 
     def _norm(self, max_norm, st):
         import torch
@@ -1195,6 +1218,11 @@ class AdamW:
                 c.d_step = self.d_step.data_ptr()
             _check("df11_adamw_step",
                    LIB.df11_adamw_step(ctypes.byref(c), self._t, len(self._t), st))
+        if stream is not None:
+            _lend(self.device, stream, [x for x in (self.counts, self.d_step, grad_factor,
+                                                    lr if by_tensor else None) if x is not None] +
+                  [x for part in (self.weights, self.grads, self.masters or [], *self.state.values())
+                   for x in part])
         self.steps += 1
         return norm
 
@@ -1219,6 +1247,9 @@ class AdamW:
         with guard:
             _check("df11_adamw_values",
                    LIB.df11_adamw_values(self._t, len(self._t), _type(kind), lists[0], lists[1], st))
+        if stream is not None:
+            _lend(self.device, stream,
+                  [x for part in (m_out or [], v_out or [], *self.state.values()) for x in part])
         return m_out, v_out
 
     def compressed_sizes(self) -> df11_sizes:

@@ -646,3 +646,27 @@ def test_weights_that_overlap_are_refused():
         with pytest.raises(ValueError, match="overlap"):
             ed.AdamW(pair, g[:2])
     ed.AdamW([flat[100:200], flat[:100], flat[50:50]], g).step()  # side by side, and an empty one
+
+
+def test_gradients_freed_while_another_stream_uses_them():
+    w = torch.randn(200_000, device="cuda")
+    g = torch.randn(200_000, device="cuda")
+    plain = ed.AdamW([w.clone()], [g.clone()])
+    plain.step(max_norm=1.0)
+    opt = ed.AdamW([w], [g])
+    a = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    say("[gpu] AdamW step on a busy stream, its gradients freed at once")
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            b = a @ a
+    opt.step(max_norm=1.0, stream=side)
+    at = g.data_ptr()
+    opt.set_grads([torch.zeros(200_000, device="cuda")])
+    del g
+    others = [torch.full((200_000,), 7.0, device="cuda") for _ in range(4)]
+    assert all(o.data_ptr() != at for o in others)
+    torch.cuda.synchronize()
+    assert torch.equal(w, plain.weights[0])
+    del b

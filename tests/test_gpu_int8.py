@@ -521,6 +521,30 @@ def test_linear_takes_one_row_of_codes_for_all():
     assert torch.equal(again, y)
 
 
+def test_activations_freed_while_another_stream_uses_them():
+    w = torch.randn(300, 512).bfloat16()
+    layer = ed.Int8Linear.from_tensors([w.cuda()])
+    x = torch.randn(64, 512).bfloat16()
+    want = linear_reference(x, w, "f32")
+    a = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    for tokens in (1, 64):
+        d = x[:tokens].cuda()
+        torch.cuda.synchronize()
+        say(f"[gpu] Int8Linear of {tokens} tokens on a busy stream, its activations freed at once")
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                b = a @ a
+        y, = layer([d], torch.float32, stream=side)
+        at = d.data_ptr()
+        del d
+        others = [torch.zeros(tokens, 512, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+        assert all(o.data_ptr() != at for o in others)
+        torch.cuda.synchronize()
+        assert torch.equal(y.cpu(), want[:tokens])
+    del b
+
+
 def test_no_tokens():
     layer = ed.Int8Linear.from_tensors([torch.randn(5, 20, device="cuda")])
     say("[gpu] Int8Linear of no tokens")
