@@ -646,7 +646,9 @@ int df11_adamw_values(const df11_adamw_tensor *t, uint32_t n_tensors, uint32_t t
  * so that &d_norm[1] can be df11_adamw_config.d_grad_factor.  Reads g and numel
  * of the tensors.  The sums have a fixed order (deterministic).  scratch:
  * device, 8-byte aligned, df11_grad_norm_scratch_bytes(t, n_tensors) bytes, not
- * shared by calls that may overlap; no initialisation needed.  Asynchronous.
+ * shared by calls that may overlap; no initialisation needed.  One launch
+ * (up to 65536 elements in up to 36 tensors), or one for every 36 tensors that
+ * are not empty and one more.  Asynchronous.
  * Errors: DF11_E_INVALID (null or misaligned pointers, g_type not F32 or BF16,
  * max_norm not above 0, a scratch that is too small), DF11_E_HIP.
  */

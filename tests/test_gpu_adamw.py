@@ -457,6 +457,28 @@ def test_grad_norm(sizes, g):
     assert np.array_equal(got, again)
 
 
+@pytest.mark.parametrize("g", ["f32", "bf16"])
+@pytest.mark.parametrize("sizes", [
+    [65536], [65537], [65535, 0, 1], [32768, 32768, 1], [256] * 35 + [56576], [256] * 36 + [56320],
+    [1] * 36, [1] * 37, [255, 257] * 18, [0] * 40 + [513], [33 * k for k in range(40)]])
+def test_grad_norm_where_its_forms_meet(sizes, g):
+    """Up to 65536 elements in up to 36 tensors one launch, two or more beyond.
+    Every element counts: the norm of ones is the root of their number."""
+    case = Case(sizes, "bf16", g, seed=18)
+    say(f"[gpu] df11_grad_norm {g} {len(sizes)} tensors, {sum(sizes)} elements")
+    got = case.opt().grad_norm(1e-2).cpu().numpy()
+    every = np.concatenate([from_bf16(x) if g == "bf16" else x for x in case.host["g"]]).astype(np.float64)
+    norm = math.sqrt(math.fsum(every * every))
+    assert abs(got[0] - norm) <= norm * 1.01 * U
+    ones = case.opt()
+    for t in ones.grads:
+        t.fill_(1.0)
+    assert ones.grad_norm(1.0).cpu().numpy()[0] == f32(math.sqrt(sum(sizes)))
+    last = [t for t in ones.grads if t.numel()][-1]
+    last[-1] = math.inf
+    assert math.isnan(ones.grad_norm(1.0).cpu().numpy()[1])
+
+
 def test_grad_norm_of_nothing_and_of_large_values():
     case = Case([0, 0], "bf16", "f32", seed=14)
     say("[gpu] df11_grad_norm of nothing, of 1e30, of infinity")
