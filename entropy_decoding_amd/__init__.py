@@ -894,7 +894,7 @@ def quantize_int8(tensors, stream=None):
 class Int8Linear:
     """The matrices of a block as 8-bit integers with a scale for each output
     channel, multiplied with activations that are quantised token by token
-    (df11_linear_int8: two launches a call).
+    (df11_linear_int8: two launches a call, one for a single token).
 
     ``codes``: int8 device tensors [rows, at least cols rounded up to 16];
     ``scales``: float32 [rows]; ``shapes``: (rows, cols) of each matrix.  Codes
@@ -978,7 +978,7 @@ class Int8Linear:
             out_dtype = torch.bfloat16
         x_type, y_type = _type(kind), _type(out_dtype)
         n = len(self.shapes)
-        t = (df11_int8_tensor * n).from_buffer_copy(self._t)
+        t = type(self._t).from_buffer_copy(self._t)
         last = None
         for a, x, (_, c) in zip(t, xs, self.shapes):
             if x is not last:
@@ -1003,9 +1003,10 @@ class Int8Linear:
             if need is None:
                 need = self._bytes[n_tokens] = int(
                     LIB.df11_linear_int8_scratch_bytes(self._t, n, n_tokens))
-            scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
+            scratch = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
             _check("df11_linear_int8",
-                   LIB.df11_linear_int8(x_type, y_type, t, n, n_tokens, scratch.data_ptr(), need, st))
+                   LIB.df11_linear_int8(x_type, y_type, t, n, n_tokens,
+                                        scratch.data_ptr() if need else None, need, st))
         if stream is not None:
             _lend(self.device, stream, [*xs, *out, *self._held, *self.scales])
         return out

@@ -825,9 +825,12 @@ int run_gemm(GemmArgs &a, uint32_t n, hipStream_t st) {
     return run_tiles<Y, 256, 256, 2, 4, 2>(a, n, st);
 }
 
-// Checks the product's arguments and fills the kernels' (used: the matrices with work).
+// Checks the product's arguments and fills the kernels' (used: the matrices with
+// work).  x_align: 16 for codes, an element's bytes for one token's values,
+// which have neither scales nor a stride.
 int prepare_gemm(uint32_t y_type, const df11_int8_tensor *t, uint32_t n_tensors, uint32_t n_tokens,
-                 GemmArgs &a, uint32_t &used) {
+                 uint32_t x_align, GemmArgs &a, uint32_t &used) {
+    const bool codes = x_align == 16;
     if ((n_tensors && !t) || n_tensors > kMax || y_type > DF11_TYPE_F16) return DF11_E_INVALID;
     if (n_tokens > (1u << 20)) return DF11_E_INVALID;
     uint32_t order[kMax];
@@ -840,12 +843,14 @@ int prepare_gemm(uint32_t y_type, const df11_int8_tensor *t, uint32_t n_tensors,
         const df11_int8_tensor &x = t[order[k]];
         if (x.cols > DF11_INT8_MAX_COLS || x.rows > (1u << 24)) return DF11_E_INVALID;
         if (!x.rows || !n_tokens) continue;
-        if (!x.w_scale || !x.x_scale || !x.y || !aligned(x.w_scale, 4) || !aligned(x.x_scale, 4) ||
-            !aligned(x.y, type_bytes(y_type)) || x.y_stride < x.rows || x.y_stride >> 40)
+        if (!x.w_scale || !x.y || !aligned(x.w_scale, 4) || !aligned(x.y, type_bytes(y_type)) ||
+            x.y_stride < x.rows || x.y_stride >> 40 ||
+            (codes && (!x.x_scale || !aligned(x.x_scale, 4))))
             return DF11_E_INVALID;
-        if (x.cols && (!x.w || !x.x || !aligned(x.w, 16) || !aligned(x.x, 16) || x.w_stride % 16 ||
-                       x.x_stride % 16 || x.w_stride < x.cols || x.x_stride < x.cols ||
-                       x.w_stride > DF11_INT8_MAX_STRIDE || x.x_stride > DF11_INT8_MAX_STRIDE))
+        if (x.cols && (!x.w || !x.x || !aligned(x.w, 16) || !aligned(x.x, x_align) || x.w_stride % 16 ||
+                       x.w_stride < x.cols || x.w_stride > DF11_INT8_MAX_STRIDE ||
+                       (codes && (x.x_stride % 16 || x.x_stride < x.cols ||
+                                  x.x_stride > DF11_INT8_MAX_STRIDE))))
             return DF11_E_INVALID;
         a.w[used] = x.w, a.w_scale[used] = x.w_scale, a.x[used] = x.x, a.x_scale[used] = x.x_scale;
         a.y[used] = x.y, a.y_stride[used] = x.y_stride;
@@ -855,6 +860,13 @@ int prepare_gemm(uint32_t y_type, const df11_int8_tensor *t, uint32_t n_tensors,
     }
     a.n_tokens = n_tokens;
     return DF11_OK;
+}
+
+// linear_one's calls
+bool one_token(const df11_int8_tensor *t, uint32_t n, uint32_t n_tokens) {
+    bool one = n && n_tokens == 1;
+    for (uint32_t k = 0; one && k < n; k++) one = t[k].cols >= 1 && t[k].cols <= kOneMaxCols;
+    return one;
 }
 
 int launch_gemm(uint32_t y_type, GemmArgs &a, uint32_t used, hipStream_t st) {
@@ -907,14 +919,15 @@ int df11_gemm_int8(uint32_t y_type, const df11_int8_tensor *t, uint32_t n_tensor
                    uint32_t n_tokens, df11_hip_stream stream) {
     GemmArgs a{};
     uint32_t used = 0;
-    const int rc = prepare_gemm(y_type, t, n_tensors, n_tokens, a, used);
+    const int rc = prepare_gemm(y_type, t, n_tensors, n_tokens, 16, a, used);
     return rc == DF11_OK && used ? launch_gemm(y_type, a, used, static_cast<hipStream_t>(stream)) : rc;
 }
 
 uint64_t df11_linear_int8_scratch_bytes(const df11_int8_tensor *t, uint32_t n_tensors,
                                         uint32_t n_tokens) {
-    uint64_t bytes = 16;
-    for (uint32_t k = 0; t && k < n_tensors; k++)
+    if (!t || one_token(t, n_tensors, n_tokens)) return 0;
+    uint64_t bytes = 0;
+    for (uint32_t k = 0; k < n_tensors; k++)
         bytes += n_tokens * code_stride(t[k].cols) + scale_bytes(n_tokens);
     return bytes;
 }
@@ -922,10 +935,22 @@ uint64_t df11_linear_int8_scratch_bytes(const df11_int8_tensor *t, uint32_t n_te
 int df11_linear_int8(uint32_t x_type, uint32_t y_type, const df11_int8_tensor *t,
                      uint32_t n_tensors, uint32_t n_tokens, void *scratch, uint64_t scratch_bytes,
                      df11_hip_stream stream) {
-    if ((n_tensors && !t) || n_tensors > kMax || n_tokens > (1u << 20)) return DF11_E_INVALID;
-    if (!scratch || !aligned(scratch, 16) ||
-        scratch_bytes < df11_linear_int8_scratch_bytes(t, n_tensors, n_tokens))
+    if ((n_tensors && !t) || n_tensors > kMax || n_tokens > (1u << 20) || x_type > DF11_TYPE_F16)
         return DF11_E_INVALID;
+    const uint64_t need = df11_linear_int8_scratch_bytes(t, n_tensors, n_tokens);
+    if (!aligned(scratch, 16) || scratch_bytes < need || (need && !scratch)) return DF11_E_INVALID;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    GemmArgs a{};
+    uint32_t used = 0;
+    if (one_token(t, n_tensors, n_tokens)) {
+        const int rc = prepare_gemm(y_type, t, n_tensors, n_tokens, type_bytes(x_type), a, used);
+        if (rc != DF11_OK || !used) return rc;
+        switch (x_type) {
+        case DF11_TYPE_F32: return run_one<float>(y_type, a, used, st);
+        case DF11_TYPE_BF16: return run_one<__bf16>(y_type, a, used, st);
+        default: return run_one<_Float16>(y_type, a, used, st);
+        }
+    }
     df11_int8_rows rows[kMax];
     df11_int8_tensor q[kMax];
     uint32_t n_rows = 0;
@@ -950,32 +975,9 @@ int df11_linear_int8(uint32_t x_type, uint32_t y_type, const df11_int8_tensor *t
         q[k].x = rows[j].codes, q[k].x_scale = rows[j].scales, q[k].x_stride = rows[j].code_stride;
     }
     // the product's arguments are checked before the first launch
-    GemmArgs a{};
-    uint32_t used = 0;
-    int rc = prepare_gemm(y_type, q, n_tensors, n_tokens, a, used);
-    bool one = n_tokens == 1 && used;
-    for (uint32_t k = 0; k < n_tensors; k++)
-        one = one && t[k].cols >= 1 && t[k].cols <= kOneMaxCols;
-    if (rc == DF11_OK && one) {
-        // matrices were put in order: find each one's activations by its codes
-        for (uint32_t k = 0; k < used; k++)
-            for (uint32_t j = 0; j < n_rows; j++)
-                if (a.x[k] == rows[j].codes) {
-                    a.x[k] = static_cast<const int8_t *>(rows[j].src);
-                    break;
-                }
-        for (uint32_t j = 0; j < n_rows; j++)
-            if (!rows[j].src || !aligned(rows[j].src, type_bytes(x_type)) || x_type > DF11_TYPE_F16)
-                return DF11_E_INVALID;
-        hipStream_t st = static_cast<hipStream_t>(stream);
-        switch (x_type) {
-        case DF11_TYPE_F32: return run_one<float>(y_type, a, used, st);
-        case DF11_TYPE_BF16: return run_one<__bf16>(y_type, a, used, st);
-        default: return run_one<_Float16>(y_type, a, used, st);
-        }
-    }
+    int rc = prepare_gemm(y_type, q, n_tensors, n_tokens, 16, a, used);
     if (rc == DF11_OK) rc = df11_quantize_int8(x_type, rows, n_rows, stream);
-    return rc == DF11_OK && used ? launch_gemm(y_type, a, used, static_cast<hipStream_t>(stream)) : rc;
+    return rc == DF11_OK && used ? launch_gemm(y_type, a, used, st) : rc;
 }
 
 }  // extern "C"

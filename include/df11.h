@@ -735,8 +735,9 @@ int df11_gemm_int8(uint32_t y_type, const df11_int8_tensor *t, uint32_t n_tensor
  * multiplied.  scratch: device, 16-byte aligned, at least
  * df11_linear_int8_scratch_bytes(t, n_tensors, n_tokens) bytes (enough however
  * the matrices share), not shared by calls that may overlap; no
- * initialisation needed.  Two launches on st.  Errors as df11_gemm_int8, and
- * DF11_E_INVALID for x_type and the scratch.
+ * initialisation needed.  Two launches on st; one token of 1 to 32768 columns
+ * in every matrix takes one, and no scratch (0 bytes; it may be null then).
+ * Errors as df11_gemm_int8, and DF11_E_INVALID for x_type and the scratch.
  */
 uint64_t df11_linear_int8_scratch_bytes(const df11_int8_tensor *t, uint32_t n_tensors,
                                         uint32_t n_tokens);

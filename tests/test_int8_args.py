@@ -127,9 +127,21 @@ def test_linear_refuses_scratch_and_types():
     {"y_stride": 19}, {"cols": 131072}])
 def test_linear_of_one_token_refuses(change):
     assert linear(tensor(**change), tokens=1) == ed.DF11_E_INVALID
-    for bad in ({"x_kind": 3}, {"y_kind": 3}, {"scratch": 0}, {"nbytes": 15}):
+    for bad in ({"x_kind": 3}, {"y_kind": 3}, {"scratch": 4104}):
         assert linear(tensor(), tokens=1, **bad) == ed.DF11_E_INVALID
     assert linear(tensor(x=16386), x_kind=0, tokens=1) == ed.DF11_E_INVALID
+
+
+@pytest.mark.parametrize("cols,none", [(0, False), (1, True), (32768, True), (32769, False)])
+def test_one_token_needs_no_scratch(cols, none):
+    stride = max(16, (cols + 15) // 16 * 16)
+    t = tensor(cols=cols, w_stride=stride, x_stride=stride)
+    need = L.df11_linear_int8_scratch_bytes(t, 1, 1)
+    assert (need == 0) == none
+    assert L.df11_linear_int8_scratch_bytes(t, 1, 2) >= 2 * cols + 8
+    if need:
+        assert linear(t, tokens=1, scratch=0) == ed.DF11_E_INVALID
+        assert linear(t, tokens=1, nbytes=need - 1) == ed.DF11_E_INVALID
 
 
 def test_linear_of_nothing():
