@@ -928,6 +928,7 @@ class Int8Linear:
             self._held.append(q)
             a.w, a.w_scale, a.rows, a.cols = q.data_ptr(), s.data_ptr(), r, c
             a.w_stride = q.stride(0) if r > 1 else whole
+            a.y_stride = r  # of outputs that a call makes
 
     @classmethod
     def from_tensors(cls, tensors, stream=None):
@@ -995,10 +996,14 @@ class Int8Linear:
         guard, st = _on(self.device, stream)
         with guard:
             if out is None:
-                out = [first.new_empty((n_tokens, r), dtype=out_dtype) for r, _ in self.shapes]
-            for a, y in zip(t, out):
-                a.y = y.data_ptr()
-                a.y_stride = y.stride(0) if n_tokens > 1 else y.size(1)
+                dev = self.device
+                out = [torch.empty(n_tokens, r, dtype=out_dtype, device=dev) for r, _ in self.shapes]
+                for a, y in zip(t, out):
+                    a.y = y.data_ptr()
+            else:
+                for a, y in zip(t, out):
+                    a.y = y.data_ptr()
+                    a.y_stride = y.stride(0) if n_tokens > 1 else y.size(1)
             need = self._bytes.get(n_tokens)
             if need is None:
                 need = self._bytes[n_tokens] = int(
