@@ -692,3 +692,20 @@ def test_gradients_freed_while_another_stream_uses_them():
     torch.cuda.synchronize()
     assert torch.equal(w, plain.weights[0])
     del b
+
+
+def test_captured_with_its_stream_named():
+    w, g = torch.randn(70_000, device="cuda"), torch.randn(70_000, device="cuda")
+    side = torch.cuda.Stream()
+    plain, opt = (ed.AdamW([w.clone()], [g.clone()], state_bits=8, device_step=True) for _ in range(2))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    say("[gpu] AdamW step captured, stream named")
+    with torch.cuda.graph(graph, stream=side):
+        opt.step(max_norm=1.0, stream=side)
+    for _ in range(3):
+        graph.replay()
+        plain.step(max_norm=1.0)
+        torch.cuda.synchronize()
+        assert torch.equal(opt.weights[0], plain.weights[0])
+        assert int(opt.d_step) == int(plain.d_step)

@@ -521,6 +521,28 @@ def test_linear_takes_one_row_of_codes_for_all():
     assert torch.equal(again, y)
 
 
+def test_captured_with_its_stream_named():
+    w = torch.randn(700, 272).bfloat16()
+    layer = ed.Int8Linear.from_tensors([w.cuda(), w[:300].cuda()])
+    side = torch.cuda.Stream()
+    for tokens in (1, 90):
+        x = torch.randn(tokens, 272).bfloat16()
+        d = x.cuda()
+        layer([d, d], torch.float32, stream=side)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        say(f"[gpu] Int8Linear of {tokens} tokens captured, stream named")
+        with torch.cuda.graph(graph, stream=side):
+            ys = layer([d, d], torch.float32, stream=side)
+        for k in range(3):
+            d.copy_(x * (k + 1))
+            graph.replay()
+            eager = layer([d, d], torch.float32)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(ys, eager))
+            assert torch.equal(ys[0].cpu(), linear_reference(x * (k + 1), w, "f32"))
+
+
 def test_activations_freed_while_another_stream_uses_them():
     w = torch.randn(300, 512).bfloat16()
     layer = ed.Int8Linear.from_tensors([w.cuda()])
