@@ -954,6 +954,8 @@ class Int8Linear:
             df11_decompress_block(ds, unit, status, st)
             parts = unit.split([r * c for r, c in shapes])
             held = _quantize(_matrices([p.view(s) for p, s in zip(parts, shapes)], "matrices"), st)
+        _lend(ds.stream.device, stream, [ds.stream, ds.sm, ds.gaps, ds.block_out_pos, ds.tables] +
+              ([] if status is None else [status]))
         return cls([q for q, _ in held], [s for _, s in held], shapes)
 
     def __call__(self, xs, out_dtype=None, out=None, stream=None):

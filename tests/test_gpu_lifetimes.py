@@ -1,0 +1,71 @@
+"""GPU tests of tensors that are freed, or reused, while a call on another
+stream is still to run.  A stream is kept busy for some ten milliseconds, the
+call is queued behind, and the memory's owner lets go of it at once: new tensors
+must not lie there, and the results have to be right."""
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import entropy_decoding_amd as ed  # noqa: E402
+
+
+def say(msg):
+    print(msg, flush=True)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    torch.cuda.init()
+    yield
+    torch.cuda.synchronize()
+
+
+def busy(stream, times=20):
+    """Products on the stream; the caller holds the result."""
+    a = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        for _ in range(times):
+            b = a @ a
+    return a, b
+
+
+def refill(sizes, kind, stream=None):
+    """New tensors of the given sizes, filled, whose places are returned."""
+    with torch.cuda.stream(stream or torch.cuda.current_stream()):
+        held = [torch.full((n,), 85, dtype=kind, device="cuda") for n in sizes for _ in range(3)]
+    return held, {t.data_ptr() for t in held}
+
+
+def compressed(shapes, seed):
+    g = torch.Generator().manual_seed(seed)
+    ws = [(torch.randn(*s, generator=g) * 0.02).bfloat16() for s in shapes]
+    tensors = [w.view(torch.int16).numpy().view(np.uint16).reshape(-1) for w in ws]
+    cb = ed.df11_build_codebook(tensors)
+    return ws, ed.DeviceStream(ed.df11_encode(cb, tensors), cb, "cuda")
+
+
+def test_unit_freed_while_another_stream_decodes_it():
+    shapes = [(512, 1024), (300, 512)]
+    ws, ds = compressed(shapes, 1)
+    xs = [torch.randn(20, c).bfloat16().cuda() for _, c in shapes]
+    want = ed.Int8Linear.from_tensors([w.cuda() for w in ws])(xs, torch.float32)
+    side = torch.cuda.Stream()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    held = busy(side)
+    say("[gpu] Int8Linear.from_unit on a busy stream, the unit freed at once")
+    layer = ed.Int8Linear.from_unit(ds, shapes, status, stream=side)
+    arrays = [ds.stream, ds.sm, ds.gaps, ds.block_out_pos, ds.tables]
+    sizes, at = [t.numel() * t.element_size() for t in arrays], {t.data_ptr() for t in arrays}
+    del ds, arrays
+    others, places = refill(sizes, torch.uint8)
+    assert not at & places
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert all(torch.equal(a, b) for a, b in zip(layer(xs, torch.float32), want))
+    del held, others

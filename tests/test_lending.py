@@ -1,0 +1,70 @@
+"""Which tensors the operators' binding lends to a stream, and what it makes on
+one.  The library, the streams and the device are stand-ins here: the tensors
+lie in host memory, and what would be recorded for a stream is written down."""
+
+import contextlib
+import types
+
+import pytest
+
+import entropy_decoding_amd as ed
+
+torch = pytest.importorskip("torch")
+
+
+class Fake:
+    """Stands in for the library: every function succeeds, and is written down."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return 1 << 10 if name.endswith("scratch_bytes") else ed.DF11_OK
+        return call
+
+
+@pytest.fixture
+def gpu(monkeypatch):
+    """lent: the (address, stream) pairs recorded; current: the current stream;
+    inside: the stream whose guard is entered."""
+    s = types.SimpleNamespace(lent=set(), current=1, inside=None, lib=Fake())
+
+    @contextlib.contextmanager
+    def guard(stream):
+        s.inside = stream
+        yield
+        s.inside = None
+
+    def on(device, stream):
+        st = s.current if stream is None else stream
+        return guard(st), st
+
+    monkeypatch.setattr(ed, "LIB", s.lib)
+    monkeypatch.setattr(ed, "_on", on)
+    monkeypatch.setattr(ed, "_stream_of", lambda device, stream: stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: s.current)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: None)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda t, stream: s.lent.add((t.data_ptr(), stream)), raising=False)
+    return s
+
+
+def unit(shapes):
+    """Something like a DeviceStream of a BF16 unit."""
+    n = sum(r * c for r, c in shapes)
+    return types.SimpleNamespace(
+        stream=torch.zeros(64, dtype=torch.uint8), sm=torch.zeros(n, dtype=torch.uint8),
+        gaps=torch.zeros(16, dtype=torch.uint8), block_out_pos=torch.zeros(16, dtype=torch.int32),
+        tables=torch.zeros(64, dtype=torch.uint8), n_weights=n, desc=types.SimpleNamespace(format=0))
+
+
+@pytest.mark.parametrize("stream", [None, 7])
+def test_a_unit_is_lent_to_the_stream_that_decodes_it(gpu, monkeypatch, stream):
+    ds, status = unit([(4, 32), (3, 16)]), torch.zeros(1, dtype=torch.int32)
+    monkeypatch.setattr(ed, "df11_decompress_block", lambda *a: None)
+    ed.Int8Linear.from_unit(ds, [(4, 32), (3, 16)], status, stream)
+    want = {(t.data_ptr(), stream) for t in (ds.stream, ds.sm, ds.gaps, ds.block_out_pos, ds.tables, status)}
+    assert want <= gpu.lent if stream is not None else not gpu.lent
