@@ -913,6 +913,7 @@ class Int8Linear:
         self._t = (df11_int8_tensor * len(codes))()
         self._bytes = {}  # scratch for a number of tokens
         self._held = []   # the codes that the calls read
+        self._lent = set()  # handles of the streams that the codes and scales are lent to
         for a, q, s, (r, c) in zip(self._t, codes, self.scales, self.shapes):
             if q.dtype != torch.int8 or q.size(0) != r or q.size(1) < c:
                 raise ValueError("codes must be int8 of the shape's rows and at least its columns")
@@ -933,9 +934,19 @@ class Int8Linear:
     @classmethod
     def from_tensors(cls, tensors, stream=None):
         """Quantises weight matrices (BF16, F16 or float32, [rows, cols])."""
-        tensors = list(tensors)
-        held = quantize_int8(tensors, stream)
-        return cls([q for q, _ in held], [s for _, s in held], [tuple(t.shape) for t in tensors])
+        tensors = _matrices(tensors, "matrices")
+        guard, st = _on(tensors[0].device, stream)
+        with guard:
+            held = _quantize(tensors, st)
+        _lend(tensors[0].device, stream, tensors)
+        return cls._made(held, [tuple(t.shape) for t in tensors], st)
+
+    @classmethod
+    def _made(cls, held, shapes, st):
+        """A layer of codes and scales that were made on the stream st."""
+        layer = cls([q for q, _ in held], [s for _, s in held], shapes)
+        layer._lent.add(st)
+        return layer
 
     @classmethod
     def from_unit(cls, ds: DeviceStream, shapes, status=None, stream=None):
@@ -956,7 +967,7 @@ class Int8Linear:
             held = _quantize(_matrices([p.view(s) for p, s in zip(parts, shapes)], "matrices"), st)
         _lend(ds.stream.device, stream, [ds.stream, ds.sm, ds.gaps, ds.block_out_pos, ds.tables] +
               ([] if status is None else [status]))
-        return cls([q for q, _ in held], [s for _, s in held], shapes)
+        return cls._made(held, shapes, st)
 
     def __call__(self, xs, out_dtype=None, out=None, stream=None):
         """y = x W^T of every matrix: a list of [n_tokens, rows] tensors of
@@ -1014,8 +1025,12 @@ class Int8Linear:
             _check("df11_linear_int8",
                    LIB.df11_linear_int8(x_type, y_type, t, n, n_tokens,
                                         scratch.data_ptr() if need else None, need, st))
+        if st not in self._lent:  # once: they stay lent until they are freed
+            _lend(self.device, torch.cuda.current_stream(self.device) if stream is None else stream,
+                  [*self._held, *self.scales])
+            self._lent.add(st)
         if stream is not None:
-            _lend(self.device, stream, [*xs, *out, *self._held, *self.scales])
+            _lend(self.device, stream, [*xs, *out])
         return out
 
 

@@ -69,3 +69,29 @@ def test_unit_freed_while_another_stream_decodes_it():
     assert int(status.item()) == 0
     assert all(torch.equal(a, b) for a, b in zip(layer(xs, torch.float32), want))
     del held, others
+
+
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_layer_dropped_while_another_stream_uses_it(tokens):
+    """Made on a side stream, whose memory its codes are; called on the current
+    one without naming it."""
+    shapes = [(512, 1024), (300, 512)]
+    ws = [torch.randn(*s, device="cuda") for s in shapes]
+    xs = [torch.randn(tokens, c, device="cuda").bfloat16() for _, c in shapes]
+    want = ed.Int8Linear.from_tensors(ws)(xs, torch.float32)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    layer = ed.Int8Linear.from_tensors(ws, stream=side)
+    torch.cuda.synchronize()
+    tensors = layer._held + layer.scales
+    sizes = [t.untyped_storage().nbytes() for t in tensors]
+    at = {t.data_ptr() for t in tensors}
+    held = busy(torch.cuda.current_stream())
+    say(f"[gpu] Int8Linear of {tokens} tokens on the busy current stream, the layer dropped at once")
+    got = layer(xs, torch.float32)
+    del layer, tensors
+    others, places = refill(sizes, torch.uint8, side)
+    assert not at & places
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del held, others

@@ -68,3 +68,27 @@ def test_a_unit_is_lent_to_the_stream_that_decodes_it(gpu, monkeypatch, stream):
     ed.Int8Linear.from_unit(ds, [(4, 32), (3, 16)], status, stream)
     want = {(t.data_ptr(), stream) for t in (ds.stream, ds.sm, ds.gaps, ds.block_out_pos, ds.tables, status)}
     assert want <= gpu.lent if stream is not None else not gpu.lent
+
+
+def test_codes_are_lent_to_whatever_stream_multiplies_with_them(gpu):
+    """Made on stream 7, used on the current one without naming it, and on another."""
+    ws = [torch.zeros(4, 32), torch.zeros(3, 32)]
+    layer = ed.Int8Linear.from_tensors(ws, stream=7)
+    held = [t.data_ptr() for t in layer._held + layer.scales]
+    assert len(held) == 4
+    x = torch.zeros(2, 32)
+    layer([x, x], stream=7)
+    for _ in range(2):
+        layer([x, x])
+    assert {(p, gpu.current) for p in held} <= gpu.lent
+    assert (x.data_ptr(), gpu.current) not in gpu.lent  # the caller's, on the caller's stream
+    gpu.current = 5
+    layer([x, x])
+    assert {(p, 5) for p in held} <= gpu.lent
+
+
+def test_codes_given_to_a_layer_are_lent(gpu):
+    (codes, scales), = ed.quantize_int8([torch.zeros(4, 32)])
+    layer = ed.Int8Linear([codes], [scales], [(4, 32)])
+    layer([torch.zeros(2, 32)], stream=7)
+    assert {(t.data_ptr(), 7) for t in layer._held + layer.scales} <= gpu.lent
