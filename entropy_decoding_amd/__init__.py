@@ -1257,17 +1257,18 @@ class AdamW:
         if self.state_bits == 32:
             raise ValueError("32-bit states are their own values")
         sizes = self._sizes
-        if m_out is None and v_out is None:
-            m_out, v_out = ([torch.empty(s, device=self.device) for s in sizes] for _ in range(2))
-        lists = []
-        for out, what in ((m_out, "m_out"), (v_out, "v_out")):
-            kind = (m_out if m_out is not None else v_out)[0].dtype
-            if out is not None:
-                out = _same(out, what, kind, sizes, self.device)
-            lists.append(None if out is None
-                         else (ctypes.c_void_p * len(out))(*[t.data_ptr() for t in out]))
         guard, st = _on(self.device, stream)
         with guard:
+            if m_out is None and v_out is None:
+                # memory of the stream that writes it: its last use there is over by then
+                m_out, v_out = ([torch.empty(s, device=self.device) for s in sizes] for _ in range(2))
+            lists = []
+            for out, what in ((m_out, "m_out"), (v_out, "v_out")):
+                kind = (m_out if m_out is not None else v_out)[0].dtype
+                if out is not None:
+                    out = _same(out, what, kind, sizes, self.device)
+                lists.append(None if out is None
+                             else (ctypes.c_void_p * len(out))(*[t.data_ptr() for t in out]))
             _check("df11_adamw_values",
                    LIB.df11_adamw_values(self._t, len(self._t), _type(kind), lists[0], lists[1], st))
         if stream is not None:

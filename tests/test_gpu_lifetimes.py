@@ -95,3 +95,26 @@ def test_layer_dropped_while_another_stream_uses_it(tokens):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     del held, others
+
+
+def test_values_on_a_stream_take_no_memory_in_use_elsewhere():
+    """The current stream is busy with a buffer that is freed at once; the values
+    written on another stream must not lie there."""
+    n = 3 << 20
+    w = torch.randn(n, device="cuda")
+    opt = ed.AdamW([w], [torch.randn(n, device="cuda")], state_bits=8)
+    opt.step()
+    want = opt.state_values()
+    side = torch.cuda.Stream()
+    held = busy(torch.cuda.current_stream())
+    buffers = [torch.empty(n, device="cuda") for _ in range(2)]
+    for b in buffers:
+        b.fill_(85.0)  # runs after the products
+    at = {b.data_ptr() for b in buffers}
+    say("[gpu] AdamW.state_values on a stream beside the busy current one")
+    del b, buffers
+    got = opt.state_values(stream=side)
+    assert not at & {t.data_ptr() for part in got for t in part}
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for p, q in zip(got, want) for a, b in zip(p, q))
+    del held

@@ -92,3 +92,25 @@ def test_codes_given_to_a_layer_are_lent(gpu):
     layer = ed.Int8Linear([codes], [scales], [(4, 32)])
     layer([torch.zeros(2, 32)], stream=7)
     assert {(t.data_ptr(), 7) for t in layer._held + layer.scales} <= gpu.lent
+
+
+def optimiser(bits=8, sizes=(300, 5), **kw):
+    ws = [torch.zeros(n) for n in sizes]
+    return ed.AdamW(ws, [torch.zeros(n) for n in sizes], state_bits=bits, **kw)
+
+
+@pytest.fixture
+def host_tensors(monkeypatch):
+    """AdamW takes tensors of the host."""
+    monkeypatch.setattr(ed, "_same", lambda tensors, *a: list(tensors))
+
+
+def test_values_are_made_on_the_stream_that_writes_them(gpu, host_tensors, monkeypatch):
+    opt = optimiser()
+    inside, empty = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: (inside.append(gpu.inside), empty(*a, **kw))[1])
+    for stream in (7, None):
+        m, v = opt.state_values(stream=stream)
+        assert [t.numel() for t in m] == [t.numel() for t in v] == [300, 5]
+        assert inside == [7 if stream else gpu.current] * 4
+        inside.clear()
