@@ -280,6 +280,7 @@ def _load():
                                      vp]
     at = ctypes.POINTER(df11_adamw_tensor)
     L.df11_adamw_step.argtypes = [ctypes.POINTER(df11_adamw_config), at, ctypes.c_uint32, vp]
+    L.df11_adamw_step_counted.argtypes = [ctypes.POINTER(df11_adamw_config), at, ctypes.c_uint32, vp, vp]
     L.df11_adamw_values.argtypes = [at, ctypes.c_uint32, ctypes.c_uint32, ctypes.POINTER(vp),
                                     ctypes.POINTER(vp), vp]
     L.df11_grad_norm_scratch_bytes.argtypes = [at, ctypes.c_uint32]
@@ -297,7 +298,8 @@ def _load():
                                    ctypes.POINTER(df11_int8_tensor), ctypes.c_uint32,
                                    ctypes.c_uint32, vp, ctypes.c_uint64, vp]
     for f in (L.df11_build_codebook, L.df11_encode_size, L.df11_encode,
-              L.df11_quantize_int8, L.df11_gemm_int8, L.df11_linear_int8, L.df11_adamw_step, L.df11_adamw_values, L.df11_grad_norm,
+              L.df11_quantize_int8, L.df11_gemm_int8, L.df11_linear_int8, L.df11_adamw_step,
+              L.df11_adamw_step_counted, L.df11_adamw_values, L.df11_grad_norm,
               L.df11_build_codebook_fmt, L.df11_encode_size_fmt, L.df11_encode_fmt,
               L.df11_decompress_block, L.df11_decompress_tensor, L.df11_pipeline_create,
               L.df11_pipeline_destroy, L.df11_pipeline_decompress, L.df11_pipeline_acquire,
@@ -1128,8 +1130,10 @@ class AdamW:
     weights in ``self.counts`` (one row of 256 per tensor).
     ``weight_decay`` and ``lr_scale``: one number, or one per tensor.  ``step``:
     steps already made.  ``device_step``: keep the step's number on the device
-    too (``self.d_step``) and advance it there, so that a captured step counts
-    on when it is replayed.  Used from one host thread at a time.
+    (``self.d_step``) and advance it there, so that a captured step counts on
+    when it is replayed; without it a captured step replays the number it was
+    captured with.  Steps that a gradient factor skips are not counted.  Used
+    from one host thread at a time.
     """
 
     def __init__(self, weights, grads, masters=None, state_bits: int = 32, state=None,
@@ -1167,9 +1171,12 @@ class AdamW:
         self.state = {k: _same(state[k], k, d, blocks if k.endswith("scale") else sizes, dev)
                       for k, d in kinds.items()}
         self.counts = (torch.zeros((n, 256), dtype=torch.int64, device=dev) if counts else None)
-        self.lr, self.steps = float(lr), int(step)
+        self.lr, self._calls = float(lr), int(step)
+        # the step's number, or how many of the calls were skipped (once factors are in use)
         self.d_step = (torch.full((1,), int(step), dtype=torch.int64, device=dev)
                        if device_step else None)
+        self._skipped = None if device_step else torch.zeros(1, dtype=torch.int64, device=dev)
+        self._factors = False
         each = lambda x: [float(v) for v in x] if np.ndim(x) else [float(x)] * n  # noqa: E731
         decays, scales = each(weight_decay), each(lr_scale)
         if len(decays) != n or len(scales) != n:
@@ -1218,7 +1225,10 @@ class AdamW:
         device tensor that the kernel reads).  ``max_norm``: clip the
         gradients' norm; returns grad_norm's tensor then.  ``grad_factor``: a
         float32 device tensor of one element to multiply the gradients with;
-        a factor that is not finite leaves everything as it was."""
+        a factor that is not finite (that of a norm that is not, too) leaves
+        everything as it was, the step's number among it."""
+        import torch
+
         if max_norm is not None and grad_factor is not None:
             raise ValueError("max_norm or grad_factor")
         c = self._c
@@ -1228,26 +1238,51 @@ class AdamW:
                 raise ValueError(f"{what} must be one float32 on {self.device}")
         c.lr = self.lr if lr is None or by_tensor else float(lr)
         c.d_lr = lr.data_ptr() if by_tensor else None
-        c.step = self.steps + 1
+        c.step = self._calls + 1
         guard, st = _on(self.device, stream)
-        norm = None
+        norm = count = None
         with guard:
             c.d_grad_factor = None if grad_factor is None else grad_factor.data_ptr()
             if max_norm is not None:
                 norm = self._norm(max_norm, st)
                 c.d_grad_factor = norm.data_ptr() + 4
+            factor = c.d_grad_factor is not None
             if self.d_step is not None:
                 self.d_step += 1
                 c.d_step = self.d_step.data_ptr()
-            _check("df11_adamw_step",
-                   LIB.df11_adamw_step(ctypes.byref(c), self._t, len(self._t), st))
+                count = self.d_step if factor else None
+            elif (factor or self._factors) and not torch.cuda.is_current_stream_capturing():
+                self._factors, count = True, self._skipped
+            if count is None:
+                _check("df11_adamw_step",
+                       LIB.df11_adamw_step(ctypes.byref(c), self._t, len(self._t), st))
+            else:
+                _check("df11_adamw_step_counted",
+                       LIB.df11_adamw_step_counted(ctypes.byref(c), self._t, len(self._t),
+                                                   count.data_ptr(), st))
         if stream is not None:
-            _lend(self.device, stream, [x for x in (self.counts, self.d_step, grad_factor,
+            _lend(self.device, stream, [x for x in (self.counts, self.d_step, self._skipped, grad_factor,
                                                     lr if by_tensor else None) if x is not None] +
                   [x for part in (self.weights, self.grads, self.masters or [], *self.state.values())
                    for x in part])
-        self.steps += 1
+        self._calls += 1
         return norm
+
+    @property
+    def steps(self) -> int:
+        """Steps made.  Waits for the GPU where only it knows whether some were
+        skipped, or replayed (device_step)."""
+        import torch
+
+        if self.d_step is None and not self._factors:
+            return self._calls
+        torch.cuda.synchronize(self.device)
+        return int(self.d_step) if self.d_step is not None else self._calls - int(self._skipped)
+
+    @steps.setter
+    def steps(self, made: int) -> None:
+        self._calls = int(made)
+        (self._skipped.zero_() if self.d_step is None else self.d_step.fill_(self._calls))
 
     def state_values(self, m_out=None, v_out=None, stream=None):
         """(m, v) as lists of float32 tensors, or written into the given lists
@@ -1282,7 +1317,7 @@ class AdamW:
         memory, to encode them.  Waits for the step, whatever its stream."""
         import torch
 
-        if self.counts is None or not self.steps:
+        if self.counts is None or not self._calls:
             raise ValueError("counts are kept by steps of AdamW(counts=True)")
         torch.cuda.synchronize(self.device)
         counts = self.counts.sum(0).cpu().numpy().view(np.uint64)

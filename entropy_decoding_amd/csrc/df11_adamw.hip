@@ -65,6 +65,12 @@ struct Numbers {
     const float *d_lr;
     const uint64_t *d_step;
     const float *d_factor;
+    uint64_t step;
+    // of a call that counts the steps made: the number of steps skipped, and what
+    // a step that changes nothing adds to which counter (last launch of the call)
+    const uint64_t *d_skipped;
+    unsigned long long *d_count;
+    unsigned long long more;
 };
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -250,6 +256,10 @@ __device__ __forceinline__ const Tensor &find(const Table &a, uint32_t &chunk) {
     return a.t[k];
 }
 
+__device__ __forceinline__ uint64_t counter(const uint64_t *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 template <class W, bool MASTER, class G, int BITS, bool COUNTS>
 __global__ __launch_bounds__(kThreads) void adamw(Table a, Numbers c) {
     __shared__ uint32_t hist[COUNTS ? 256 * (kCopies + 1) : 1];
@@ -264,12 +274,16 @@ __global__ __launch_bounds__(kThreads) void adamw(Table a, Numbers c) {
         __syncthreads();
     }
 
+    // Steps skipped are rare: the host's factors hold while there are none.  The
+    // counters are read by every workgroup and written by one, only in a step
+    // that uses neither.
     float keep = t.keep, size = t.size, inv_root = c.inv_root, f = 1.0f;
-    if (c.d_lr || c.d_step) {
+    const uint64_t skipped = c.d_skipped ? counter(c.d_skipped) : 0;
+    if (c.d_lr || c.d_step || skipped) {
         const double lr = (c.d_lr ? double(*c.d_lr) : c.lr) * t.lr_scale;
         double bias1 = c.bias1;
-        if (c.d_step) {
-            const double step = double(*c.d_step);
+        if (c.d_step || skipped) {
+            const double step = double(c.d_step ? counter(c.d_step) : skipped < c.step ? c.step - skipped : 1);
             bias1 = 1.0 - exp(step * c.log_b1);
             inv_root = float(1.0 / sqrt(1.0 - exp(step * c.log_b2)));
         }
@@ -280,6 +294,7 @@ __global__ __launch_bounds__(kThreads) void adamw(Table a, Numbers c) {
     if (c.d_factor) {
         f = *c.d_factor;
         still = !(fabsf(f) < __builtin_inff());
+        if (still && c.d_count && blockIdx.x == 0 && threadIdx.x == 0) atomicAdd(c.d_count, c.more);
     }
 
     // A wave's next elements from `at` on, all of them or `left`: NG groups of 4
@@ -633,13 +648,9 @@ int pick_step(const Table &a, uint32_t grid, const Numbers &c, hipStream_t st, b
 
 bool finite_at_least_0(double x) { return std::isfinite(x) && x >= 0.0; }
 
-}  // namespace
-
-extern "C" {
-
-int df11_adamw_step(const df11_adamw_config *c, const df11_adamw_tensor *t, uint32_t n_tensors,
-                    df11_hip_stream stream) {
-    hipStream_t st = static_cast<hipStream_t>(stream);
+// The step; d_skipped and d_count as in Numbers.
+int adamw_step(const df11_adamw_config *c, const df11_adamw_tensor *t, uint32_t n_tensors,
+               const uint64_t *d_skipped, uint64_t *d_count, uint64_t more, hipStream_t st) {
     if (!c || (n_tensors && !t)) return DF11_E_INVALID;
     if (c->w_type > DF11_TYPE_BF16 || c->g_type > DF11_TYPE_BF16 || c->reserved ||
         (c->state_bits != 32 && c->state_bits != 8))
@@ -654,6 +665,7 @@ int df11_adamw_step(const df11_adamw_config *c, const df11_adamw_tensor *t, uint
     const bool s8 = c->state_bits == 8;
     const uintptr_t state_size = s8 ? 1 : 4;
     bool masters = false, plain = false, counts = false;
+    uint32_t last = 0;  // the last tensor that is not empty: its launch is the call's last
     for (uint32_t k = 0; k < n_tensors; k++) {
         const df11_adamw_tensor &x = t[k];
         if (x.numel > kMaxNumel || !finite_at_least_0(x.lr_scale) ||
@@ -669,6 +681,7 @@ int df11_adamw_step(const df11_adamw_config *c, const df11_adamw_tensor *t, uint
             !aligned(x.v_scale, 4))
             return DF11_E_INVALID;
         (x.master ? masters : plain) = true;
+        last = k;
     }
     if (masters && plain) return DF11_E_INVALID;  // one kernel serves all tensors
 
@@ -682,9 +695,11 @@ int df11_adamw_step(const df11_adamw_config *c, const df11_adamw_tensor *t, uint
     num.lr = c->lr;
     num.log_b1 = std::log(c->beta1), num.log_b2 = std::log(c->beta2);
     num.d_lr = c->d_lr, num.d_step = c->d_step, num.d_factor = c->d_grad_factor;
+    num.step = c->step, num.d_skipped = d_skipped, num.more = more;
 
     const auto fill = [&](Tensor &a, uint32_t k) {
         const df11_adamw_tensor &x = t[k];
+        if (k == last) num.d_count = reinterpret_cast<unsigned long long *>(d_count);
         a.w = x.w, a.master = x.master, a.g = x.g, a.m = x.m, a.v = x.v;
         a.m_scale = x.m_scale, a.v_scale = x.v_scale;
         a.counts = reinterpret_cast<unsigned long long *>(x.counts);
@@ -712,6 +727,23 @@ int df11_adamw_step(const df11_adamw_config *c, const df11_adamw_tensor *t, uint
                           return counts ? pick_step<__bf16, false, true>(a, grid, num, st, g16, s8)
                                         : pick_step<__bf16, false, false>(a, grid, num, st, g16, s8);
                       });
+}
+
+}  // namespace
+
+extern "C" {
+
+int df11_adamw_step(const df11_adamw_config *c, const df11_adamw_tensor *t, uint32_t n_tensors,
+                    df11_hip_stream stream) {
+    return adamw_step(c, t, n_tensors, nullptr, nullptr, 0, static_cast<hipStream_t>(stream));
+}
+
+int df11_adamw_step_counted(const df11_adamw_config *c, const df11_adamw_tensor *t, uint32_t n_tensors,
+                            uint64_t *d_count, df11_hip_stream stream) {
+    if (!c || !d_count || !aligned(d_count, 8) || (c->d_step && c->d_step != d_count)) return DF11_E_INVALID;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return c->d_step ? adamw_step(c, t, n_tensors, nullptr, d_count, ~uint64_t(0), st)  // one less
+                     : adamw_step(c, t, n_tensors, d_count, d_count, 1, st);
 }
 
 int df11_adamw_values(const df11_adamw_tensor *t, uint32_t n_tensors, uint32_t type,

@@ -630,6 +630,21 @@ int df11_adamw_step(const df11_adamw_config *c, const df11_adamw_tensor *t, uint
                     df11_hip_stream st);
 
 /*
+ * df11_adamw_step for gradient factors that may not be finite: a step that
+ * changes nothing is not counted, so that the bias corrections of later steps
+ * are those of the updates that m and v received.  d_count: device, 8-byte
+ * aligned, for the steps of one set of states in stream order.
+ * Without c->d_step it holds the number of steps skipped so far (0 at first): t
+ * is c->step less *d_count, at least 1, and a step that changes nothing adds 1.
+ * With c->d_step it must be the same address, which the caller has advanced
+ * for this step: a step that changes nothing takes that back (subtracts 1).
+ * Steps of no elements launch nothing and leave it alone.  The same launches
+ * as df11_adamw_step; errors likewise, and DF11_E_INVALID for d_count.
+ */
+int df11_adamw_step_counted(const df11_adamw_config *c, const df11_adamw_tensor *t,
+                            uint32_t n_tensors, uint64_t *d_count, df11_hip_stream st);
+
+/*
  * The values that 8-bit states stand for: m_out[k] and v_out[k] receive tensor
  * k's numel values of m and v in type (DF11_TYPE_F32 or DF11_TYPE_BF16,
  * rounded to nearest); either list may be null.  Reads m, v, m_scale, v_scale

@@ -76,6 +76,23 @@ def test_step_of_nothing_launches_nothing():
     assert step(config(), tensor(numel=0, w=0, g=0, m=0, v=0)) == ed.DF11_OK
 
 
+def counted(c, t, count=4096, n=1):
+    return L.df11_adamw_step_counted(None if c is None else ctypes.byref(c), t, n, count, None)
+
+
+def test_counted_step_refuses():
+    """What the step refuses, and counters that are null, misaligned or beside
+    the step's number on the device."""
+    assert counted(config(), tensor(), None) == ed.DF11_E_INVALID
+    assert counted(config(), tensor(), 4100) == ed.DF11_E_INVALID
+    assert counted(config(d_step=8192), tensor(), 4096) == ed.DF11_E_INVALID
+    assert counted(None, tensor()) == ed.DF11_E_INVALID
+    assert counted(config(), None) == ed.DF11_E_INVALID
+    assert counted(config(step=0), tensor()) == ed.DF11_E_INVALID
+    assert counted(config(), tensor(w=4097)) == ed.DF11_E_INVALID
+    assert counted(config(), None, n=0) == ed.DF11_OK
+
+
 @pytest.mark.parametrize("kind,change", [
     (2, {}), (3, {}), (0, {"m": 0}), (0, {"v": 0}), (0, {"m_scale": 0}), (0, {"v_scale": 4097}),
     (0, {"numel": 2 ** 41})])

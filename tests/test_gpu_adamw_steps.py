@@ -1,0 +1,128 @@
+"""GPU tests of what an AdamW object counts, refuses and tells torch, around
+steps that are skipped, refused or never made."""
+
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import entropy_decoding_amd as ed  # noqa: E402
+
+BETAS = (0.9, 0.95)
+
+
+def say(msg):
+    print(msg, flush=True)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    torch.cuda.init()
+    yield
+    torch.cuda.synchronize()
+
+
+def make(sizes, bits=32, seed=0, **kw):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    ws = [(torch.randn(n, device="cuda", generator=g) * 0.02).bfloat16() for n in sizes]
+    gs = [torch.randn(n, device="cuda", generator=g) * 1e-3 for n in sizes]
+    return ed.AdamW(ws, gs, masters=[w.float() for w in ws], state_bits=bits, lr=1e-2, betas=BETAS, **kw)
+
+
+def parts(opt):
+    return [opt.weights, opt.masters, *opt.state.values()]
+
+
+def equal(a, b):
+    torch.cuda.synchronize()
+    return all(torch.equal(x, y) for p, q in zip(parts(a), parts(b)) for x, y in zip(p, q))
+
+
+def skip(opt, how):
+    if how == "factor":
+        opt.step(grad_factor=torch.tensor([math.nan], device="cuda"))
+        return
+    grads = opt.grads
+    opt.set_grads([torch.full_like(x, math.inf) for x in grads])
+    opt.step(max_norm=0.01)
+    opt.set_grads(grads)
+
+
+def go(opt, how):
+    if how == "factor":
+        opt.step(grad_factor=torch.tensor([0.5], device="cuda"))
+    else:
+        opt.step(max_norm=0.01)
+
+
+@pytest.mark.parametrize("sizes", [[300, 1025], [7] * 75, [500] * 36 + [0, 0]])
+@pytest.mark.parametrize("how", ["factor", "norm"])
+@pytest.mark.parametrize("device_step", [False, True])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_skipped_steps_are_not_counted(bits, device_step, how, sizes):
+    """The updates after them are those of an optimiser that never met them."""
+    a = make(sizes, bits, device_step=device_step)
+    b = make(sizes, bits, device_step=True)
+    say(f"[gpu] AdamW skipped steps bits={bits} device_step={device_step} {how} {len(sizes)} tensors")
+    skip(a, how)
+    assert equal(a, b)
+    for made, skips in ((1, 2), (2, 0), (3, 1)):
+        go(a, how), go(b, how)
+        assert equal(a, b), made
+        for _ in range(skips):
+            skip(a, how)
+        assert equal(a, b), made
+    a.step(), b.step()  # and without a factor
+    assert equal(a, b)
+    assert a.steps == b.steps == 4 and int(b.d_step) == 4
+    if device_step:
+        assert int(a.d_step) == 4
+
+
+@pytest.mark.parametrize("device_step", [False, True])
+def test_skipped_steps_of_a_replayed_graph(device_step):
+    """With the number on the device a replay that is skipped is not counted
+    either; without it every replay is of the number that was captured."""
+    a, b = (make([300, 70_000, 5], 8, device_step=device_step) for _ in range(2))
+    say(f"[gpu] AdamW captured, some replays skipped, device_step={device_step}")
+    for o in (a, b):
+        go(o, "norm"), skip(o, "norm")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm = a.step(max_norm=0.01)
+    number = 2 if device_step else 3  # the host's does not know of the skipped one
+    kept = [x.clone() for x in a.grads]
+    for i, finite in enumerate([True, False, False, True, True, False, True]):
+        for x, y in zip(a.grads, kept):
+            x.copy_(y) if finite else x.fill_(math.nan)
+        if finite:
+            other = ed.AdamW(b.weights, b.grads, masters=b.masters, state_bits=8, state=b.state, lr=1e-2,
+                             betas=BETAS, step=number - 1, device_step=device_step)
+            want = other.step(max_norm=0.01)
+            number += device_step
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert equal(a, b), i
+        assert torch.equal(norm, want) if finite else not torch.isfinite(norm).any()
+    if device_step:
+        assert int(a.d_step) == number - 1 == a.steps
+
+
+def test_steps_can_be_set():
+    """As where a run goes on from saved states."""
+    a, b = make([300], step=7), make([300])
+    say("[gpu] AdamW.steps set")
+    skip(b, "factor"), go(b, "factor")
+    assert b.steps == 1
+    for x, y in zip(parts(b), parts(a)):
+        for p, q in zip(x, y):
+            p.copy_(q)
+    b.steps = 7
+    go(a, "factor"), go(b, "factor")
+    assert a.steps == b.steps == 8 and equal(a, b)
