@@ -1253,13 +1253,11 @@ class AdamW:
                 count = self.d_step if factor else None
             elif (factor or self._factors) and not torch.cuda.is_current_stream_capturing():
                 self._factors, count = True, self._skipped
-            if count is None:
-                _check("df11_adamw_step",
-                       LIB.df11_adamw_step(ctypes.byref(c), self._t, len(self._t), st))
-            else:
-                _check("df11_adamw_step_counted",
-                       LIB.df11_adamw_step_counted(ctypes.byref(c), self._t, len(self._t),
-                                                   count.data_ptr(), st))
+            rc = (LIB.df11_adamw_step(ctypes.byref(c), self._t, len(self._t), st) if count is None else
+                  LIB.df11_adamw_step_counted(ctypes.byref(c), self._t, len(self._t), count.data_ptr(), st))
+            if rc != DF11_OK and self.d_step is not None:
+                self.d_step -= 1  # no step was made
+            _check("df11_adamw_step", rc)
         if stream is not None:
             _lend(self.device, stream, [x for x in (self.counts, self.d_step, self._skipped, grad_factor,
                                                     lr if by_tensor else None) if x is not None] +

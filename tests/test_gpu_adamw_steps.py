@@ -126,3 +126,20 @@ def test_steps_can_be_set():
     b.steps = 7
     go(a, "factor"), go(b, "factor")
     assert a.steps == b.steps == 8 and equal(a, b)
+
+
+@pytest.mark.parametrize("device_step", [False, True])
+def test_a_refused_step_is_not_counted(device_step):
+    a, b = (make([300, 1025], device_step=device_step) for _ in range(2))
+    say(f"[gpu] AdamW refused steps device_step={device_step}")
+    for bad in (-1.0, math.nan):
+        with pytest.raises(ed.Df11Error):
+            a.step(lr=bad)
+        with pytest.raises(ed.Df11Error):
+            a.step(lr=bad, max_norm=1.0)
+    with pytest.raises(ed.Df11Error):
+        a.step(max_norm=-1.0)
+    a.step(), b.step()
+    assert equal(a, b) and a.steps == b.steps == 1
+    if device_step:
+        assert int(a.d_step) == 1
