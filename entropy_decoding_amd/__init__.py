@@ -1190,16 +1190,24 @@ class AdamW:
             a.counts = self.counts[k].data_ptr() if counts else None
             a.numel, a.lr_scale, a.weight_decay = sizes[k], scales[k], decays[k]
         self._c = df11_adamw_config(self.lr, betas[0], betas[1], eps, 0,
-                                    _type(self.weights[0].dtype), 0, state_bits, 0)
+                                    self._kind(self.weights, "weights"), 0, state_bits, 0)
         self._norm_bytes = int(LIB.df11_grad_norm_scratch_bytes(self._t, n))
         self.set_grads(grads)
 
     def set_grads(self, grads) -> None:
         """The gradients that later steps read."""
-        self.grads = _same(grads, "grads", None, self._sizes, self.device)
-        for a, g in zip(self._t, self.grads):
+        grads = _same(grads, "grads", None, self._sizes, self.device)
+        kind = self._kind(grads, "gradients")  # refused before anything is replaced
+        self.grads, self._c.g_type = grads, kind
+        for a, g in zip(self._t, grads):
             a.g = g.data_ptr()
-        self._c.g_type = _type(self.grads[0].dtype)
+
+    @staticmethod
+    def _kind(tensors, what) -> int:
+        kind = _type(tensors[0].dtype)
+        if kind > TYPES["bfloat16"]:
+            raise Df11Error(f"AdamW of {what} in {tensors[0].dtype}", DF11_E_INVALID)
+        return kind
 
     def grad_norm(self, max_norm: float, stream=None):
         """A float32 device tensor [norm, clip factor] of all gradients together."""

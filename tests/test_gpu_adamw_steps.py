@@ -143,3 +143,23 @@ def test_a_refused_step_is_not_counted(device_step):
     assert equal(a, b) and a.steps == b.steps == 1
     if device_step:
         assert int(a.d_step) == 1
+
+
+@pytest.mark.parametrize("kind", [torch.float64, torch.float16, torch.int8])
+def test_refused_gradients_leave_the_old_ones(kind):
+    sizes = [300, 1025]
+    a, b = (make(sizes) for _ in range(2))
+    say(f"[gpu] AdamW.set_grads of {kind}")
+    with pytest.raises((TypeError, ed.Df11Error)):
+        a.set_grads([torch.zeros(n, device="cuda").to(kind) for n in sizes])
+    assert a.grads[0].dtype == torch.float32
+    a.step(), b.step()
+    assert equal(a, b)
+
+
+def test_half_precision_is_refused_at_once():
+    w = torch.zeros(10, dtype=torch.float16, device="cuda")
+    say("[gpu] AdamW of float16")
+    for pair in ((w, w.float()), (w.float(), w)):
+        with pytest.raises(ed.Df11Error, match="float16"):
+            ed.AdamW([pair[0]], [pair[1]])
