@@ -1323,10 +1323,11 @@ class AdamW:
         memory, to encode them.  Waits for the step, whatever its stream."""
         import torch
 
-        if self.counts is None or not self._calls:
+        if self.counts is not None:
+            torch.cuda.synchronize(self.device)
+            counts = self.counts.sum(0).cpu().numpy().view(np.uint64)
+        if self.counts is None or not counts.any():  # every step counts every weight
             raise ValueError("counts are kept by steps of AdamW(counts=True)")
-        torch.cuda.synchronize(self.device)
-        counts = self.counts.sum(0).cpu().numpy().view(np.uint64)
         cb, sz = df11_build_codebook_from_counts(counts), df11_sizes()
         _check("df11_encode_size_from_counts",
                LIB.df11_encode_size_from_counts(_format("bf16"), ctypes.byref(cb),

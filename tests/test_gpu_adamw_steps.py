@@ -163,3 +163,10 @@ def test_half_precision_is_refused_at_once():
     for pair in ((w, w.float()), (w.float(), w)):
         with pytest.raises(ed.Df11Error, match="float16"):
             ed.AdamW([pair[0]], [pair[1]])
+
+
+def test_sizes_before_a_step_are_refused():
+    say("[gpu] AdamW.compressed_sizes before a step")
+    for opt in (make([300], counts=True, step=10), make([300], counts=True), make([300])):
+        with pytest.raises(ValueError, match="counts"):
+            opt.compressed_sizes()
