@@ -1343,7 +1343,8 @@ class AdamW:
         import torch
 
         torch.cuda.synchronize(self.device)
-        return encode_on_device(self.weights, stream=stream)
+        with torch.cuda.device(self.device):  # the encoder works on the current device's streams
+            return encode_on_device(self.weights, stream=stream)
 
 
 def table_bytes(cb: df11_codebook) -> int:

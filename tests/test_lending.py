@@ -114,3 +114,21 @@ def test_values_are_made_on_the_stream_that_writes_them(gpu, host_tensors, monke
         assert [t.numel() for t in m] == [t.numel() for t in v] == [300, 5]
         assert inside == [7 if stream else gpu.current] * 4
         inside.clear()
+
+
+def test_compressing_is_done_on_the_optimisers_device(gpu, host_tensors, monkeypatch):
+    opt = optimiser()
+    entered, at = [], []
+
+    @contextlib.contextmanager
+    def device(d):
+        entered.append(d)
+        yield
+        entered.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(ed, "encode_on_device",
+                        lambda tensors, stream=None: at.append((list(entered), tensors, stream)))
+    for stream in (None, 7):
+        opt.compress(stream)
+        assert at.pop() == ([opt.device], opt.weights, stream) and not entered
