@@ -1191,6 +1191,9 @@ class AdamW:
             a.numel, a.lr_scale, a.weight_decay = sizes[k], scales[k], decays[k]
         self._c = df11_adamw_config(self.lr, betas[0], betas[1], eps, 0,
                                     self._kind(self.weights, "weights"), 0, state_bits, 0)
+        # what a step changes that graphs may have saved; views count with their base
+        bases = [t if t._base is None else t._base for t in self.weights + (self.masters or [])]
+        self._changed = list({id(t): t for t in bases}.values())
         self._norm_bytes = int(LIB.df11_grad_norm_scratch_bytes(self._t, n))
         self.set_grads(grads)
 
@@ -1266,6 +1269,7 @@ class AdamW:
             if rc != DF11_OK and self.d_step is not None:
                 self.d_step -= 1  # no step was made
             _check("df11_adamw_step", rc)
+        torch.autograd.graph.increment_version(self._changed)
         if stream is not None:
             _lend(self.device, stream, [x for x in (self.counts, self.d_step, self._skipped, grad_factor,
                                                     lr if by_tensor else None) if x is not None] +

@@ -170,3 +170,23 @@ def test_sizes_before_a_step_are_refused():
     for opt in (make([300], counts=True, step=10), make([300], counts=True), make([300])):
         with pytest.raises(ValueError, match="counts"):
             opt.compressed_sizes()
+
+
+def test_torch_sees_that_weights_change():
+    """A graph that saved a weight must not go backward with the new one."""
+    w = torch.randn(500, device="cuda", requires_grad=True)
+    flat = torch.randn(900, device="cuda").bfloat16()
+    views = list(flat.split([400, 500]))
+    masters = [v.float() for v in views]
+    one = ed.AdamW([w], [torch.ones(500, device="cuda")])
+    two = ed.AdamW(views, [torch.ones_like(v) for v in views], masters=masters)
+    say("[gpu] AdamW and torch's versions")
+    loss = (w * w).sum()
+    before = [t._version for t in (flat, *masters)]
+    one.step(), two.step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    assert all(t._version > v for t, v in zip((flat, *masters), before))
+    with torch.inference_mode():  # such tensors have no version
+        t = torch.randn(10, device="cuda")
+        ed.AdamW([t], [torch.ones(10, device="cuda")]).step()
