@@ -1146,6 +1146,8 @@ class AdamW:
             raise ValueError("no weights")
         if state_bits not in (32, 8):
             raise ValueError("state_bits must be 32 or 8")
+        if int(step) < 0:
+            raise ValueError("step must be at least 0")
         self.device = dev = self.weights[0].device
         sizes = self._sizes = [t.numel() for t in self.weights]
         n = len(sizes)

@@ -190,3 +190,11 @@ def test_torch_sees_that_weights_change():
     with torch.inference_mode():  # such tensors have no version
         t = torch.randn(10, device="cuda")
         ed.AdamW([t], [torch.ones(10, device="cuda")]).step()
+
+
+def test_numbers_of_steps_below_zero_are_refused():
+    w, g = torch.zeros(10, device="cuda"), torch.zeros(10, device="cuda")
+    say("[gpu] AdamW(step=-5)")
+    for step in (-1, -5):
+        with pytest.raises(ValueError, match="step"):
+            ed.AdamW([w], [g], step=step)
