@@ -1120,8 +1120,9 @@ class AdamW:
     """df11_adamw_step over a list of device tensors (BF16 or float32 weights,
     e.g. a unit's, at any offset of a larger buffer), with what the step keeps.
 
-    Tensors must not overlap: a weight that layers share is given once.
-    ``grads``: one tensor per weight, all BF16 or all float32.  ``masters``:
+    Weights, masters and states must not overlap: a weight that layers share is
+    given once.  ``grads``: one tensor per weight, all BF16 or all float32, apart
+    from what a step writes.  ``masters``:
     float32 copies of BF16 weights that carry the update.  ``state_bits``: 32
     (float32 states) or 8 (codes of blocks of DF11_ADAMW_BLOCK elements, a
     quarter of the memory).  ``state``: lists "m" and "v" (and "m_scale",
@@ -1151,13 +1152,6 @@ class AdamW:
         self.device = dev = self.weights[0].device
         sizes = self._sizes = [t.numel() for t in self.weights]
         n = len(sizes)
-        # a weight that two tensors share would be updated twice, in any order
-        end = 0
-        for lo, hi in sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
-                             for t in self.weights if t.numel()):
-            if lo < end:
-                raise ValueError("weights overlap: give a shared tensor once")
-            end = hi
         blocks = [-(-s // DF11_ADAMW_BLOCK) for s in sizes]
         self.masters = None if masters is None else _same(masters, "masters", torch.float32, sizes, dev)
         self.state_bits = state_bits
@@ -1172,6 +1166,16 @@ class AdamW:
             raise ValueError(f"state must hold {sorted(kinds)}")
         self.state = {k: _same(state[k], k, d, blocks if k.endswith("scale") else sizes, dev)
                       for k, d in kinds.items()}
+        # what two tensors share would be updated twice, in any order
+        for written, what in ((self.weights, "weights overlap: give a shared tensor once"),
+                              (sum(self.state.values(), self.weights + (self.masters or [])),
+                               "weights, masters or states overlap")):
+            end = 0
+            for lo, hi in sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                                 for t in written if t.numel()):
+                if lo < end:
+                    raise ValueError(what)
+                end = hi
         self.counts = (torch.zeros((n, 256), dtype=torch.int64, device=dev) if counts else None)
         self.lr, self._calls = float(lr), int(step)
         # the step's number, or how many of the calls were skipped (once factors are in use)

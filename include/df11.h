@@ -617,8 +617,8 @@ typedef struct df11_adamw_config {
  * One step of the n_tensors tensors, on stream st: one launch for every 36
  * tensors that are not empty, and as many small ones before them where
  * tensors have counts.  Pointers need their element's alignment only, so
- * tensors may lie anywhere in a unit.  The buffers of different tensors must
- * not overlap (counts excepted), and either all of them have masters or none
+ * tensors may lie anywhere in a unit.  No two buffers may
+ * overlap (gradients that tensors share and counts excepted), and either all of them have masters or none
  * does.  Without d_step a captured call replays the
  * step number it was captured with.  Asynchronous.  Errors: DF11_E_INVALID
  * (null or misaligned pointers, a type, state_bits or number out of range:

@@ -198,3 +198,27 @@ def test_numbers_of_steps_below_zero_are_refused():
     for step in (-1, -5):
         with pytest.raises(ValueError, match="step"):
             ed.AdamW([w], [g], step=step)
+
+
+def test_buffers_that_overlap_are_refused():
+    """Whatever a step writes."""
+    w = [torch.zeros(300, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    g = [torch.zeros(300, device="cuda") for _ in range(2)]
+    flat = torch.zeros(900, device="cuda")
+    zeros = lambda: [torch.zeros(300, device="cuda") for _ in range(2)]  # noqa: E731
+    say("[gpu] AdamW of masters and states that overlap")
+    for bad in ([flat[:300], flat[:300]], [flat[:300], flat[299:599]]):
+        with pytest.raises(ValueError, match="overlap"):
+            ed.AdamW(w, g, masters=bad)
+        for name in "mv":
+            with pytest.raises(ValueError, match="overlap"):
+                ed.AdamW(w, g, state={"m": zeros(), "v": zeros(), name: bad})
+    same = zeros()
+    with pytest.raises(ValueError, match="overlap"):
+        ed.AdamW(w, g, state={"m": same, "v": same})
+    with pytest.raises(ValueError, match="overlap"):
+        ed.AdamW(zeros(), g, state={"m": [flat[:300], flat[300:600]], "v": [flat[600:], flat[:300]]})
+    f = zeros()
+    with pytest.raises(ValueError, match="overlap"):
+        ed.AdamW(f, g, state={"m": f, "v": zeros()})
+    ed.AdamW(w, g, masters=[flat[:300], flat[300:600]]).step()  # side by side
