@@ -900,8 +900,10 @@ class Int8Linear:
 
     ``codes``: int8 device tensors [rows, at least cols rounded up to 16];
     ``scales``: float32 [rows]; ``shapes``: (rows, cols) of each matrix.  Codes
-    whose rows start on cache lines (quantize_int8's do) are kept as they are;
-    others are copied here, on the current stream, to rows that do.
+    whose rows start on cache lines (quantize_int8's do) are kept as they are,
+    and so are their scales: later calls read what they hold then.  Others are
+    copied here with their scales, on the current stream, to rows that do: what
+    happens to the given ones later is not seen.
     """
 
     def __init__(self, codes, scales, shapes):
@@ -916,7 +918,7 @@ class Int8Linear:
         self._bytes = {}  # scratch for a number of tokens
         self._held = []   # the codes that the calls read
         self._lent = set()  # handles of the streams that the codes and scales are lent to
-        for a, q, s, (r, c) in zip(self._t, codes, self.scales, self.shapes):
+        for k, (a, q, s, (r, c)) in enumerate(zip(self._t, codes, self.scales, self.shapes)):
             if q.dtype != torch.int8 or q.size(0) != r or q.size(1) < c:
                 raise ValueError("codes must be int8 of the shape's rows and at least its columns")
             if s.dtype != torch.float32 or s.numel() != r or not s.is_contiguous() or s.device != self.device:
@@ -928,6 +930,7 @@ class Int8Linear:
             if q.data_ptr() % 128 or (r > 1 and (q.stride(0) % 128 or q.stride(0) < whole)):
                 lines = torch.empty((r, (c + 127) // 128 * 128), dtype=torch.int8, device=self.device)
                 q = lines[:, :whole].copy_(q[:, :whole])
+                s = self.scales[k] = s.clone()
             self._held.append(q)
             a.w, a.w_scale, a.rows, a.cols = q.data_ptr(), s.data_ptr(), r, c
             a.w_stride = q.stride(0) if r > 1 else whole
