@@ -978,7 +978,9 @@ class Int8Linear:
         """y = x W^T of every matrix: a list of [n_tokens, rows] tensors of
         ``out_dtype`` (BF16 by default, F16 or float32), or written into the
         tensors ``out``.  ``xs``: one [n_tokens, cols] tensor (BF16, F16 or
-        float32) per matrix; a tensor given for several is quantised once."""
+        float32) per matrix; a tensor given for several is quantised once.  The
+        rounding to codes has no derivative: activations that require a
+        gradient are refused (detach them, or call under torch.no_grad())."""
         import torch
 
         if len(xs) != len(self.shapes):
@@ -1004,6 +1006,8 @@ class Int8Linear:
                 if x.shape != (n_tokens, c) or x.dtype != kind or x.device != self.device:
                     raise ValueError("activations must be [n_tokens, cols] of their matrix, of one "
                                      f"type, on {self.device}")
+                if x.requires_grad and torch.is_grad_enabled():
+                    raise RuntimeError("an int8 product gives its activations no gradient: detach them")
                 strides = x.stride()
                 if (strides[1] != 1 and c > 1) or strides[0] < 0:
                     raise ValueError("activations must have contiguous rows")

@@ -41,3 +41,17 @@ def test_codes_and_scales_live_alike(stride):
     again, = layer([x], torch.float32)
     assert torch.equal(again, other if stride % 128 == 0 else first)
     assert not torch.equal(first, other)
+
+
+def test_activations_that_require_a_gradient_are_refused():
+    layer = ed.Int8Linear.from_tensors([torch.nn.Parameter(torch.randn(5, 20, device="cuda")) for _ in "ab"])
+    x = torch.randn(3, 20, device="cuda")
+    p = x.clone().requires_grad_()
+    say("[gpu] Int8Linear of activations that require a gradient")
+    want = layer([x, x])
+    for xs in ([p, x], [x, p], [p * 1.0, x]):
+        with pytest.raises(RuntimeError, match="gradient"):
+            layer(xs)
+        with torch.no_grad():
+            assert all(torch.equal(y, z) for y, z in zip(layer(xs), want))
+        assert all(torch.equal(y, z) for y, z in zip(layer([t.detach() for t in xs]), want))
