@@ -1190,6 +1190,9 @@ class AdamW:
                        if device_step else None)
         self._skipped = None if device_step else torch.zeros(1, dtype=torch.int64, device=dev)
         self._factors = False
+        self._memory = sum(self.state.values(), self.weights + (self.masters or [])) + [
+            t for t in (self.counts, self.d_step, self._skipped) if t is not None]
+        self._lent = set()  # handles of the streams that it is lent to
         each = lambda x: [float(v) for v in x] if np.ndim(x) else [float(x)] * n  # noqa: E731
         decays, scales = each(weight_decay), each(lr_scale)
         if len(decays) != n or len(scales) != n:
@@ -1232,6 +1235,16 @@ class AdamW:
             out = self._norm(max_norm, st)
         _lend(self.device, stream, self.grads)
         return out
+
+    def _lend(self, stream, st):
+        """Lends what steps read and write to the stream of a call (the handle st),
+        once: it stays lent until it is freed."""
+        import torch
+
+        if st not in self._lent:
+            _lend(self.device, torch.cuda.current_stream(self.device) if stream is None else stream,
+                  self._memory)
+            self._lent.add(st)
 
     def _norm(self, max_norm, st):
         import torch
@@ -1283,11 +1296,10 @@ class AdamW:
                 self.d_step -= 1  # no step was made
             _check("df11_adamw_step", rc)
         torch.autograd.graph.increment_version(self._changed)
+        self._lend(stream, st)
         if stream is not None:
-            _lend(self.device, stream, [x for x in (self.counts, self.d_step, self._skipped, grad_factor,
-                                                    lr if by_tensor else None) if x is not None] +
-                  [x for part in (self.weights, self.grads, self.masters or [], *self.state.values())
-                   for x in part])
+            _lend(self.device, stream, self.grads + [x for x in (grad_factor, lr if by_tensor else None)
+                                                     if x is not None])
         self._calls += 1
         return norm
 
@@ -1330,8 +1342,8 @@ class AdamW:
             _check("df11_adamw_values",
                    LIB.df11_adamw_values(self._t, len(self._t), _type(kind), lists[0], lists[1], st))
         if stream is not None:
-            _lend(self.device, stream,
-                  [x for part in (m_out or [], v_out or [], *self.state.values()) for x in part])
+            _lend(self.device, stream, [*(m_out or []), *(v_out or [])])
+        self._lend(stream, st)
         return m_out, v_out
 
     def compressed_sizes(self) -> df11_sizes:

@@ -118,3 +118,25 @@ def test_values_on_a_stream_take_no_memory_in_use_elsewhere():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for p, q in zip(got, want) for a, b in zip(p, q))
     del held
+
+
+def test_optimiser_dropped_while_another_stream_steps():
+    """A step on a side stream that is current but not named."""
+    n = 3 << 20
+    w, g = torch.randn(n, device="cuda"), torch.randn(n, device="cuda")
+    plain = ed.AdamW([w.clone()], [g])
+    plain.step(max_norm=1.0)
+    opt = ed.AdamW([w], [g])
+    side = torch.cuda.Stream()
+    held = busy(side)
+    say("[gpu] AdamW step on a busy current stream, the optimiser dropped at once")
+    with torch.cuda.stream(side):
+        opt.step(max_norm=1.0)
+    at = {t.data_ptr() for part in opt.state.values() for t in part}
+    del opt
+    others, places = refill([4 * n], torch.uint8)
+    assert not at & places
+    torch.cuda.synchronize()
+    assert torch.equal(w, plain.weights[0])
+    assert all((o == 85).all() for o in others)
+    del held, others

@@ -46,6 +46,7 @@ def gpu(monkeypatch):
     monkeypatch.setattr(ed, "_stream_of", lambda device, stream: stream)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: s.current)
     monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: None)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
     monkeypatch.setattr(torch.Tensor, "record_stream",
                         lambda t, stream: s.lent.add((t.data_ptr(), stream)), raising=False)
@@ -132,3 +133,26 @@ def test_compressing_is_done_on_the_optimisers_device(gpu, host_tensors, monkeyp
     for stream in (None, 7):
         opt.compress(stream)
         assert at.pop() == ([opt.device], opt.weights, stream) and not entered
+
+
+def test_an_optimisers_memory_is_lent_to_every_stream_that_steps(gpu, host_tensors):
+    """Its states are made by the constructor: whoever drops it on another stream
+    than that has no other hand on them."""
+    opt = optimiser(counts=True)
+    own = [t.data_ptr() for part in opt.state.values() for t in part]
+    own += [opt.counts.data_ptr(), opt._skipped.data_ptr()]
+    for current in (1, 5):
+        gpu.current = current
+        opt.step(max_norm=1.0)
+        assert {(p, current) for p in own} <= gpu.lent
+    opt = optimiser(device_step=True)
+    gpu.current = 6
+    opt.state_values()
+    assert {(t.data_ptr(), 6) for part in opt.state.values() for t in part} <= gpu.lent
+    opt.step(stream=9)
+    given = [*opt.weights, *opt.grads, opt.d_step]
+    assert {(t.data_ptr(), 9) for t in given} <= gpu.lent
+    others = [torch.zeros(n) for n in (300, 5)]
+    opt.set_grads(others)
+    opt.step(stream=9)
+    assert {(t.data_ptr(), 9) for t in others} <= gpu.lent
