@@ -916,8 +916,9 @@ class Int8Linear:
             raise ValueError("one codes tensor, scales tensor and shape per matrix")
         self._t = (df11_int8_tensor * len(codes))()
         self._bytes = {}  # scratch for a number of tokens
-        self._held = []   # the codes that the calls read
-        self._lent = set()  # handles of the streams that the codes and scales are lent to
+        # what the calls read: its memory, whatever the tensors are given later
+        self._held, self._held_scales = [], []
+        self._lent = set()  # handles of the streams that it is lent to
         for k, (a, q, s, (r, c)) in enumerate(zip(self._t, codes, self.scales, self.shapes)):
             if q.dtype != torch.int8 or q.size(0) != r or q.size(1) < c:
                 raise ValueError("codes must be int8 of the shape's rows and at least its columns")
@@ -931,7 +932,8 @@ class Int8Linear:
                 lines = torch.empty((r, (c + 127) // 128 * 128), dtype=torch.int8, device=self.device)
                 q = lines[:, :whole].copy_(q[:, :whole])
                 s = self.scales[k] = s.clone()
-            self._held.append(q)
+            self._held.append(q.detach())
+            self._held_scales.append(s.detach())
             a.w, a.w_scale, a.rows, a.cols = q.data_ptr(), s.data_ptr(), r, c
             a.w_stride = q.stride(0) if r > 1 else whole
             a.y_stride = r  # of outputs that a call makes
@@ -1036,7 +1038,7 @@ class Int8Linear:
                                         scratch.data_ptr() if need else None, need, st))
         if st not in self._lent:  # once: they stay lent until they are freed
             _lend(self.device, torch.cuda.current_stream(self.device) if stream is None else stream,
-                  [*self._held, *self.scales])
+                  self._held + self._held_scales)
             self._lent.add(st)
         if stream is not None:
             _lend(self.device, stream, [*xs, *out])
@@ -1140,8 +1142,10 @@ class AdamW:
     steps already made.  ``device_step``: keep the step's number on the device
     (``self.d_step``) and advance it there, so that a captured step counts on
     when it is replayed; without it a captured step replays the number it was
-    captured with.  Steps that a gradient factor skips are not counted.  Used
-    from one host thread at a time.
+    captured with.  Steps that a gradient factor skips are not counted.  Steps
+    work on the memory that the tensors have when they are given: one that gets
+    other memory later (``t.data = ...``) is not followed there.  Used from one
+    host thread at a time.
     """
 
     def __init__(self, weights, grads, masters=None, state_bits: int = 32, state=None,
@@ -1190,8 +1194,9 @@ class AdamW:
                        if device_step else None)
         self._skipped = None if device_step else torch.zeros(1, dtype=torch.int64, device=dev)
         self._factors = False
-        self._memory = sum(self.state.values(), self.weights + (self.masters or [])) + [
-            t for t in (self.counts, self.d_step, self._skipped) if t is not None]
+        # the memory of all that steps write, whatever the tensors are given later
+        self._memory = [t.detach() for t in sum(self.state.values(), self.weights + (self.masters or [])) +
+                        [self.counts, self.d_step, self._skipped] if t is not None]
         self._lent = set()  # handles of the streams that it is lent to
         each = lambda x: [float(v) for v in x] if np.ndim(x) else [float(x)] * n  # noqa: E731
         decays, scales = each(weight_decay), each(lr_scale)
@@ -1218,6 +1223,7 @@ class AdamW:
         grads = _same(grads, "grads", None, self._sizes, self.device)
         kind = self._kind(grads, "gradients")  # refused before anything is replaced
         self.grads, self._c.g_type = grads, kind
+        self._grad_memory = [g.untyped_storage() for g in grads]
         for a, g in zip(self._t, grads):
             a.g = g.data_ptr()
 

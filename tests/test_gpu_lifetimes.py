@@ -140,3 +140,21 @@ def test_optimiser_dropped_while_another_stream_steps():
     assert torch.equal(w, plain.weights[0])
     assert all((o == 85).all() for o in others)
     del held, others
+
+
+def test_weights_given_other_memory():
+    """As a module's to() does: a step after that must not write memory that is
+    someone else's by then."""
+    n = 1 << 20
+    w, g = torch.nn.Parameter(torch.randn(n, device="cuda")), torch.randn(n, device="cuda")
+    plain = ed.AdamW([w.detach().clone()], [g])
+    opt = ed.AdamW([w], [g])
+    old = w.data_ptr()
+    w.data = torch.zeros(n, device="cuda")
+    others, places = refill([4 * n], torch.uint8)
+    assert old not in places
+    say("[gpu] AdamW step after its weight was given other memory")
+    opt.step(), plain.step()
+    torch.cuda.synchronize()
+    assert all((o == 85).all() for o in others) and not w.any()
+    assert all(torch.equal(a, b) for a, b in zip(opt.state["m"], plain.state["m"]))

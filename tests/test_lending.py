@@ -11,6 +11,8 @@ import entropy_decoding_amd as ed
 
 torch = pytest.importorskip("torch")
 
+from torch.multiprocessing.reductions import StorageWeakRef  # noqa: E402
+
 
 class Fake:
     """Stands in for the library: every function succeeds, and is written down."""
@@ -156,3 +158,22 @@ def test_an_optimisers_memory_is_lent_to_every_stream_that_steps(gpu, host_tenso
     opt.set_grads(others)
     opt.step(stream=9)
     assert {(t.data_ptr(), 9) for t in others} <= gpu.lent
+
+
+def test_memory_that_calls_use_is_held(gpu, host_tensors):
+    """Not only the tensors, which may be given other memory (t.data = ..., as a
+    module's to() does): calls go on with the addresses that were given."""
+    opt = optimiser(masters=[torch.zeros(n) for n in (300, 5)])
+    room, scales = torch.zeros(8 * 128, dtype=torch.int8), torch.zeros(4)
+    codes = room[-room.data_ptr() % 128:][:4 * 128].view(4, 128)
+    layer = ed.Int8Linear([codes], [scales], [(4, 128)])  # on cache lines: not copied
+    given = [*opt.weights, *opt.masters, *opt.grads, *opt.state["m"], room, scales]
+    del codes
+    memory = [StorageWeakRef(t.untyped_storage()) for t in given]
+    for t in given:
+        t.data = torch.zeros_like(t)
+    assert not any(m.expired() for m in memory)
+    opt.set_grads([torch.zeros(n) for n in (300, 5)])
+    assert sum(m.expired() for m in memory) == 2  # the gradients before
+    del opt, layer
+    assert all(m.expired() for m in memory)
