@@ -3,6 +3,7 @@ steps that are skipped, refused or never made."""
 
 import math
 
+import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -222,3 +223,29 @@ def test_buffers_that_overlap_are_refused():
     with pytest.raises(ValueError, match="overlap"):
         ed.AdamW(f, g, state={"m": f, "v": zeros()})
     ed.AdamW(w, g, masters=[flat[:300], flat[300:600]]).step()  # side by side
+
+
+@pytest.mark.parametrize("exponent", [-96, 0, 94])
+def test_roots_of_every_mantissa(exponent):
+    """The step's roots are correctly rounded: all 2^24 values of two binades, in
+    the middle and at the ends of where they are formed without sqrtf.  Betas of
+    1/2, late steps, no gradient and lr 1 make the new weight m / (2 sqrt(v / 2)) with
+    one rounding for the root and one for the quotient (eps vanishes beside the
+    root).  The quotient is just below 2, where its last place is the finest beside
+    the root's: a root that is one off shows."""
+    bits = np.arange(2 ** 24, dtype=np.uint32) + np.uint32((127 + exponent) << 23)
+    v = bits.view(np.float32)
+    r = np.sqrt(v)
+    m = r * np.float32(1.999)
+    n = v.size
+    w = torch.zeros(n, device="cuda")
+    state = {"m": [torch.from_numpy(m * np.float32(2)).cuda()], "v": [torch.from_numpy(v * np.float32(2)).cuda()]}
+    opt = ed.AdamW([w], [torch.zeros(n, device="cuda")], state=state, lr=1.0, betas=(0.5, 0.5), eps=1e-30,
+                   weight_decay=0.0, step=2999)
+    say(f"[gpu] AdamW roots of [2^{exponent}, 2^{exponent + 2})")
+    opt.step()
+    torch.cuda.synchronize()
+    assert np.array_equal(opt.state["v"][0].cpu().numpy(), v) and np.array_equal(opt.state["m"][0].cpu().numpy(), m)
+    assert np.array_equal(w.cpu().numpy(), -(m / r))
+    for other in (np.inf, -np.inf):  # one off either way would have been seen, but for 8 values
+        assert (m / np.nextafter(r, np.float32(other)) == m / r).sum() <= 8
