@@ -1117,7 +1117,7 @@ def _on(device, stream):
     import torch
 
     if stream is None:
-        guard = _AS_IS if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        guard = _AS_IS if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
         return guard, torch._C._cuda_getCurrentRawStream(device.index)
     stream = _stream_of(device, stream)
     if stream.device != device:
@@ -1212,6 +1212,7 @@ class AdamW:
             a.numel, a.lr_scale, a.weight_decay = sizes[k], scales[k], decays[k]
         self._c = df11_adamw_config(self.lr, betas[0], betas[1], eps, 0,
                                     self._kind(self.weights, "weights"), 0, state_bits, 0)
+        self._c_ref = ctypes.byref(self._c)
         # what a step changes that graphs may have saved; views count with their base
         bases = [t if t._base is None else t._base for t in self.weights + (self.masters or [])]
         self._changed = list({id(t): t for t in bases}.values())
@@ -1247,10 +1248,9 @@ class AdamW:
         once: it stays lent until it is freed."""
         import torch
 
-        if st not in self._lent:
-            _lend(self.device, torch.cuda.current_stream(self.device) if stream is None else stream,
-                  self._memory)
-            self._lent.add(st)
+        _lend(self.device, torch.cuda.current_stream(self.device) if stream is None else stream,
+              self._memory)
+        self._lent.add(st)
 
     def _norm(self, max_norm, st):
         import torch
@@ -1276,33 +1276,37 @@ class AdamW:
             raise ValueError("max_norm or grad_factor")
         c = self._c
         by_tensor = hasattr(lr, "data_ptr")
-        for x, what in ((grad_factor, "grad_factor"), (lr if by_tensor else None, "lr")):
-            if x is not None and (_type(x.dtype) != 0 or x.numel() != 1 or x.device != self.device):
-                raise ValueError(f"{what} must be one float32 on {self.device}")
+        if by_tensor or grad_factor is not None:
+            for x, what in ((grad_factor, "grad_factor"), (lr if by_tensor else None, "lr")):
+                if x is not None and (_type(x.dtype) != 0 or x.numel() != 1 or x.device != self.device):
+                    raise ValueError(f"{what} must be one float32 on {self.device}")
         c.lr = self.lr if lr is None or by_tensor else float(lr)
         c.d_lr = lr.data_ptr() if by_tensor else None
         c.step = self._calls + 1
         guard, st = _on(self.device, stream)
         norm = count = None
         with guard:
-            c.d_grad_factor = None if grad_factor is None else grad_factor.data_ptr()
             if max_norm is not None:
                 norm = self._norm(max_norm, st)
-                c.d_grad_factor = norm.data_ptr() + 4
-            factor = c.d_grad_factor is not None
+                factor = norm.data_ptr() + 4
+            else:
+                factor = None if grad_factor is None else grad_factor.data_ptr()
+            c.d_grad_factor = factor
             if self.d_step is not None:
                 self.d_step += 1
                 c.d_step = self.d_step.data_ptr()
-                count = self.d_step if factor else None
-            elif (factor or self._factors) and not torch.cuda.is_current_stream_capturing():
-                self._factors, count = True, self._skipped
-            rc = (LIB.df11_adamw_step(ctypes.byref(c), self._t, len(self._t), st) if count is None else
-                  LIB.df11_adamw_step_counted(ctypes.byref(c), self._t, len(self._t), count.data_ptr(), st))
-            if rc != DF11_OK and self.d_step is not None:
-                self.d_step -= 1  # no step was made
-            _check("df11_adamw_step", rc)
-        torch.autograd.graph.increment_version(self._changed)
-        self._lend(stream, st)
+                count = c.d_step if factor else None
+            elif (factor or self._factors) and not torch._C._cuda_isCurrentStreamCapturing():
+                self._factors, count = True, self._skipped.data_ptr()
+            rc = (LIB.df11_adamw_step(self._c_ref, self._t, len(self._t), st) if count is None else
+                  LIB.df11_adamw_step_counted(self._c_ref, self._t, len(self._t), count, st))
+            if rc != DF11_OK:
+                if self.d_step is not None:
+                    self.d_step -= 1  # no step was made
+                _check("df11_adamw_step", rc)
+        torch._C._increment_version(self._changed)
+        if st not in self._lent:
+            self._lend(stream, st)
         if stream is not None:
             _lend(self.device, stream, self.grads + [x for x in (grad_factor, lr if by_tensor else None)
                                                      if x is not None])
@@ -1349,7 +1353,8 @@ class AdamW:
                    LIB.df11_adamw_values(self._t, len(self._t), _type(kind), lists[0], lists[1], st))
         if stream is not None:
             _lend(self.device, stream, [*(m_out or []), *(v_out or [])])
-        self._lend(stream, st)
+        if st not in self._lent:
+            self._lend(stream, st)
         return m_out, v_out
 
     def compressed_sizes(self) -> df11_sizes:

@@ -48,7 +48,7 @@ def gpu(monkeypatch):
     monkeypatch.setattr(ed, "_stream_of", lambda device, stream: stream)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: s.current)
     monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: None)
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False)
     monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
     monkeypatch.setattr(torch.Tensor, "record_stream",
                         lambda t, stream: s.lent.add((t.data_ptr(), stream)), raising=False)
