@@ -893,7 +893,21 @@ def quantize_int8(tensors, stream=None):
     return out
 
 
-class Int8Linear:
+class _Lender:
+    """What calls use for longer than one of them.  ``_memory`` was made on the
+    stream ``_home``, or given there; a call on another stream, or on one that it
+    names, lends it to that stream (``_lent``: those that have it), once: it stays
+    lent until it is freed."""
+
+    def _lend(self, stream, st):
+        import torch
+
+        _lend(self.device, torch.cuda.current_stream(self.device) if stream is None else stream,
+              self._memory)
+        self._lent.add(st)
+
+
+class Int8Linear(_Lender):
     """The matrices of a block as 8-bit integers with a scale for each output
     channel, multiplied with activations that are quantised token by token
     (df11_linear_int8: two launches a call, one for a single token).
@@ -916,9 +930,10 @@ class Int8Linear:
             raise ValueError("one codes tensor, scales tensor and shape per matrix")
         self._t = (df11_int8_tensor * len(codes))()
         self._bytes = {}  # scratch for a number of tokens
-        # what the calls read: its memory, whatever the tensors are given later
-        self._held, self._held_scales = [], []
-        self._lent = set()  # handles of the streams that it is lent to
+        # what the calls read, codes and scales in turn: its memory, whatever the
+        # tensors are given later
+        self._memory = []
+        self._home, self._lent = _on(self.device, None)[1], set()  # streams' handles: see _Lender
         for k, (a, q, s, (r, c)) in enumerate(zip(self._t, codes, self.scales, self.shapes)):
             if q.dtype != torch.int8 or q.size(0) != r or q.size(1) < c:
                 raise ValueError("codes must be int8 of the shape's rows and at least its columns")
@@ -932,8 +947,7 @@ class Int8Linear:
                 lines = torch.empty((r, (c + 127) // 128 * 128), dtype=torch.int8, device=self.device)
                 q = lines[:, :whole].copy_(q[:, :whole])
                 s = self.scales[k] = s.clone()
-            self._held.append(q.detach())
-            self._held_scales.append(s.detach())
+            self._memory += q.detach(), s.detach()
             a.w, a.w_scale, a.rows, a.cols = q.data_ptr(), s.data_ptr(), r, c
             a.w_stride = q.stride(0) if r > 1 else whole
             a.y_stride = r  # of outputs that a call makes
@@ -952,6 +966,7 @@ class Int8Linear:
     def _made(cls, held, shapes, st):
         """A layer of codes and scales that were made on the stream st."""
         layer = cls([q for q, _ in held], [s for _, s in held], shapes)
+        layer._home = st
         layer._lent.add(st)
         return layer
 
@@ -1036,10 +1051,8 @@ class Int8Linear:
             _check("df11_linear_int8",
                    LIB.df11_linear_int8(x_type, y_type, t, n, n_tokens,
                                         scratch.data_ptr() if need else None, need, st))
-        if st not in self._lent:  # once: they stay lent until they are freed
-            _lend(self.device, torch.cuda.current_stream(self.device) if stream is None else stream,
-                  self._held + self._held_scales)
-            self._lent.add(st)
+        if (st != self._home or stream is not None) and st not in self._lent:
+            self._lend(stream, st)
         if stream is not None:
             _lend(self.device, stream, [*xs, *out])
         return out
@@ -1125,7 +1138,7 @@ def _on(device, stream):
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
-class AdamW:
+class AdamW(_Lender):
     """df11_adamw_step over a list of device tensors (BF16 or float32 weights,
     e.g. a unit's, at any offset of a larger buffer), with what the step keeps.
 
@@ -1178,15 +1191,13 @@ class AdamW:
         self.state = {k: _same(state[k], k, d, blocks if k.endswith("scale") else sizes, dev)
                       for k, d in kinds.items()}
         # what two tensors share would be updated twice, in any order
-        for written, what in ((self.weights, "weights overlap: give a shared tensor once"),
-                              (sum(self.state.values(), self.weights + (self.masters or [])),
-                               "weights, masters or states overlap")):
-            end = 0
-            for lo, hi in sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
-                                 for t in written if t.numel()):
-                if lo < end:
-                    raise ValueError(what)
-                end = hi
+        spans = []
+        for part in (self.weights, self.masters or [], *self.state.values()):
+            spans += [(t.data_ptr(), t.data_ptr() + t.numel() * part[0].element_size())
+                      for t in part if t.numel()]
+        spans.sort()
+        if any(lo < end for (_, end), (lo, _) in zip(spans, spans[1:])):
+            raise ValueError("weights, masters or states overlap: give a shared tensor once")
         self.counts = (torch.zeros((n, 256), dtype=torch.int64, device=dev) if counts else None)
         self.lr, self._calls = float(lr), int(step)
         # the step's number, or how many of the calls were skipped (once factors are in use)
@@ -1194,10 +1205,13 @@ class AdamW:
                        if device_step else None)
         self._skipped = None if device_step else torch.zeros(1, dtype=torch.int64, device=dev)
         self._factors = False
-        # the memory of all that steps write, whatever the tensors are given later
-        self._memory = [t.detach() for t in sum(self.state.values(), self.weights + (self.masters or [])) +
-                        [self.counts, self.d_step, self._skipped] if t is not None]
-        self._lent = set()  # handles of the streams that it is lent to
+        # the memory of all that steps write, whatever the tensors are given later:
+        # one tensor of each storage
+        parts = sum(self.state.values(), self.weights + (self.masters or []))
+        parts += [t for t in (self.counts, self.d_step, self._skipped) if t is not None]
+        self._memory = [t.detach() for t in
+                        {t.untyped_storage().data_ptr(): t for t in parts}.values()]
+        self._home, self._lent = _on(dev, None)[1], set()  # streams' handles: see _Lender
         each = lambda x: [float(v) for v in x] if np.ndim(x) else [float(x)] * n  # noqa: E731
         decays, scales = each(weight_decay), each(lr_scale)
         if len(decays) != n or len(scales) != n:
@@ -1242,15 +1256,6 @@ class AdamW:
             out = self._norm(max_norm, st)
         _lend(self.device, stream, self.grads)
         return out
-
-    def _lend(self, stream, st):
-        """Lends what steps read and write to the stream of a call (the handle st),
-        once: it stays lent until it is freed."""
-        import torch
-
-        _lend(self.device, torch.cuda.current_stream(self.device) if stream is None else stream,
-              self._memory)
-        self._lent.add(st)
 
     def _norm(self, max_norm, st):
         import torch
@@ -1305,7 +1310,7 @@ class AdamW:
                     self.d_step -= 1  # no step was made
                 _check("df11_adamw_step", rc)
         torch._C._increment_version(self._changed)
-        if st not in self._lent:
+        if (st != self._home or stream is not None) and st not in self._lent:
             self._lend(stream, st)
         if stream is not None:
             _lend(self.device, stream, self.grads + [x for x in (grad_factor, lr if by_tensor else None)
@@ -1353,7 +1358,7 @@ class AdamW:
                    LIB.df11_adamw_values(self._t, len(self._t), _type(kind), lists[0], lists[1], st))
         if stream is not None:
             _lend(self.device, stream, [*(m_out or []), *(v_out or [])])
-        if st not in self._lent:
+        if (st != self._home or stream is not None) and st not in self._lent:
             self._lend(stream, st)
         return m_out, v_out
 

@@ -83,7 +83,7 @@ def test_layer_dropped_while_another_stream_uses_it(tokens):
     torch.cuda.synchronize()
     layer = ed.Int8Linear.from_tensors(ws, stream=side)
     torch.cuda.synchronize()
-    tensors = layer._held + layer.scales
+    tensors = layer._memory
     sizes = [t.untyped_storage().nbytes() for t in tensors]
     at = {t.data_ptr() for t in tensors}
     held = busy(torch.cuda.current_stream())

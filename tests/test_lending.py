@@ -77,7 +77,7 @@ def test_codes_are_lent_to_whatever_stream_multiplies_with_them(gpu):
     """Made on stream 7, used on the current one without naming it, and on another."""
     ws = [torch.zeros(4, 32), torch.zeros(3, 32)]
     layer = ed.Int8Linear.from_tensors(ws, stream=7)
-    held = [t.data_ptr() for t in layer._held + layer.scales]
+    held = [t.data_ptr() for t in layer._memory]
     assert len(held) == 4
     x = torch.zeros(2, 32)
     layer([x, x], stream=7)
@@ -93,8 +93,9 @@ def test_codes_are_lent_to_whatever_stream_multiplies_with_them(gpu):
 def test_codes_given_to_a_layer_are_lent(gpu):
     (codes, scales), = ed.quantize_int8([torch.zeros(4, 32)])
     layer = ed.Int8Linear([codes], [scales], [(4, 32)])
-    layer([torch.zeros(2, 32)], stream=7)
-    assert {(t.data_ptr(), 7) for t in layer._held + layer.scales} <= gpu.lent
+    for stream in (7, gpu.current):  # named: the caller may have made them elsewhere
+        layer([torch.zeros(2, 32)], stream=stream)
+        assert {(t.data_ptr(), stream) for t in layer._memory} <= gpu.lent
 
 
 def optimiser(bits=8, sizes=(300, 5), **kw):
@@ -143,7 +144,8 @@ def test_an_optimisers_memory_is_lent_to_every_stream_that_steps(gpu, host_tenso
     opt = optimiser(counts=True)
     own = [t.data_ptr() for part in opt.state.values() for t in part]
     own += [opt.counts.data_ptr(), opt._skipped.data_ptr()]
-    for current in (1, 5):
+    opt.step(max_norm=1.0)  # on the constructor's
+    for current in (3, 5):
         gpu.current = current
         opt.step(max_norm=1.0)
         assert {(p, current) for p in own} <= gpu.lent
@@ -158,6 +160,18 @@ def test_an_optimisers_memory_is_lent_to_every_stream_that_steps(gpu, host_tenso
     opt.set_grads(others)
     opt.step(stream=9)
     assert {(t.data_ptr(), 9) for t in others} <= gpu.lent
+
+
+def test_views_of_one_storage_are_lent_with_it(gpu, host_tensors, monkeypatch):
+    """Recording one tensor records the memory of all that share it."""
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda t, stream: gpu.lent.add((t.untyped_storage().data_ptr(), stream)))
+    flat = torch.zeros(900)
+    opt = ed.AdamW(list(flat.split([300, 599, 1])), [torch.zeros(n) for n in (300, 599, 1)])
+    gpu.current = 5
+    opt.step()
+    want = [flat, *opt.state["m"], *opt.state["v"], opt._skipped]
+    assert {(t.untyped_storage().data_ptr(), gpu.current) for t in want} <= gpu.lent
 
 
 def test_memory_that_calls_use_is_held(gpu, host_tensors):
