@@ -894,10 +894,9 @@ def quantize_int8(tensors, stream=None):
 
 
 class _Lender:
-    """What calls use for longer than one of them.  ``_memory`` was made on the
-    stream ``_home``, or given there; a call on another stream, or on one that it
-    names, lends it to that stream (``_lent``: those that have it), once: it stays
-    lent until it is freed."""
+    """What calls use for longer than one of them: the first call on each stream
+    lends it ``_memory``, which stays lent until it is freed.  ``_lent``: the
+    handles of the streams that have it."""
 
     def _lend(self, stream, st):
         import torch
@@ -933,7 +932,7 @@ class Int8Linear(_Lender):
         # what the calls read, codes and scales in turn: its memory, whatever the
         # tensors are given later
         self._memory = []
-        self._home, self._lent = _on(self.device, None)[1], set()  # streams' handles: see _Lender
+        self._lent = set()
         for k, (a, q, s, (r, c)) in enumerate(zip(self._t, codes, self.scales, self.shapes)):
             if q.dtype != torch.int8 or q.size(0) != r or q.size(1) < c:
                 raise ValueError("codes must be int8 of the shape's rows and at least its columns")
@@ -966,7 +965,6 @@ class Int8Linear(_Lender):
     def _made(cls, held, shapes, st):
         """A layer of codes and scales that were made on the stream st."""
         layer = cls([q for q, _ in held], [s for _, s in held], shapes)
-        layer._home = st
         layer._lent.add(st)
         return layer
 
@@ -1051,7 +1049,7 @@ class Int8Linear(_Lender):
             _check("df11_linear_int8",
                    LIB.df11_linear_int8(x_type, y_type, t, n, n_tokens,
                                         scratch.data_ptr() if need else None, need, st))
-        if (st != self._home or stream is not None) and st not in self._lent:
+        if st not in self._lent:
             self._lend(stream, st)
         if stream is not None:
             _lend(self.device, stream, [*xs, *out])
@@ -1211,7 +1209,7 @@ class AdamW(_Lender):
         parts += [t for t in (self.counts, self.d_step, self._skipped) if t is not None]
         self._memory = [t.detach() for t in
                         {t.untyped_storage().data_ptr(): t for t in parts}.values()]
-        self._home, self._lent = _on(dev, None)[1], set()  # streams' handles: see _Lender
+        self._lent = set()
         each = lambda x: [float(v) for v in x] if np.ndim(x) else [float(x)] * n  # noqa: E731
         decays, scales = each(weight_decay), each(lr_scale)
         if len(decays) != n or len(scales) != n:
@@ -1310,7 +1308,7 @@ class AdamW(_Lender):
                     self.d_step -= 1  # no step was made
                 _check("df11_adamw_step", rc)
         torch._C._increment_version(self._changed)
-        if (st != self._home or stream is not None) and st not in self._lent:
+        if st not in self._lent:
             self._lend(stream, st)
         if stream is not None:
             _lend(self.device, stream, self.grads + [x for x in (grad_factor, lr if by_tensor else None)
@@ -1358,7 +1356,7 @@ class AdamW(_Lender):
                    LIB.df11_adamw_values(self._t, len(self._t), _type(kind), lists[0], lists[1], st))
         if stream is not None:
             _lend(self.device, stream, [*(m_out or []), *(v_out or [])])
-        if (st != self._home or stream is not None) and st not in self._lent:
+        if st not in self._lent:
             self._lend(stream, st)
         return m_out, v_out
 
