@@ -1344,7 +1344,8 @@ class AdamW(_Lender):
         with guard:
             if m_out is None and v_out is None:
                 # memory of the stream that writes it: its last use there is over by then
-                m_out, v_out = ([torch.empty(s, device=self.device) for s in sizes] for _ in range(2))
+                m_out, v_out = ([torch.empty(s, dtype=torch.float32, device=self.device) for s in sizes]
+                                for _ in range(2))
             lists = []
             for out, what in ((m_out, "m_out"), (v_out, "v_out")):
                 kind = (m_out if m_out is not None else v_out)[0].dtype

@@ -138,6 +138,18 @@ def test_compressing_is_done_on_the_optimisers_device(gpu, host_tensors, monkeyp
         assert at.pop() == ([opt.device], opt.weights, stream) and not entered
 
 
+@pytest.mark.parametrize("kind", [torch.float16, torch.float64])
+def test_values_are_float32_whatever_torchs_default(gpu, host_tensors, kind):
+    opt = optimiser()
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(kind)
+    try:
+        values = opt.state_values()
+    finally:
+        torch.set_default_dtype(before)
+    assert {t.dtype for part in values for t in part} == {torch.float32}
+
+
 def test_an_optimisers_memory_is_lent_to_every_stream_that_steps(gpu, host_tensors):
     """Its states are made by the constructor: whoever drops it on another stream
     than that has no other hand on them."""
