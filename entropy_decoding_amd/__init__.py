@@ -761,6 +761,8 @@ def encode_on_device(tensors, fmt: str = "bf16", tile_windows: int = DEFAULT_TIL
             st.wait_stream(cur)  # the work that wrote the tensors comes first
         flat = [t.reshape(-1).view(torch.int16 if size == 2 else torch.uint8).contiguous()
                 for t in tensors]
+        # the histogram and the encoder read 16 bytes at a time
+        flat = [t.clone() if t.data_ptr() % 16 else t for t in flat]
         unit = torch.cat(flat) if len(flat) != 1 else flat[0]
         n = unit.numel()
         dev = unit.device
