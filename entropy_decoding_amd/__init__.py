@@ -886,7 +886,7 @@ def quantize_int8(tensors, stream=None):
     """df11_quantize_int8 of up to DF11_INT8_MAX_TENSORS matrices (BF16, F16 or
     float32 device tensors, contiguous rows): a list of (codes, scales), the
     codes int8 [rows, cols rounded up to 16] with zeros behind the columns, the
-    rows 128-byte aligned."""
+    rows 128-byte aligned; memory of the stream, where one is named."""
     tensors = _matrices(tensors, "matrices")
     guard, st = _on(tensors[0].device, stream)
     with guard:

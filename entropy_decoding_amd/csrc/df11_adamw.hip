@@ -11,8 +11,8 @@
 // What bounds it (8B block, 218 M elements): HBM with 32-bit states, 5.4 - 5.5
 // TB/s where a copy of 1 GiB moves 5.1 (BF16 with masters 1120 us, BF16 alone
 // 874 us, float32 1123 us); with 8-bit states and masters HBM too (638 us,
-// 5.5 TB/s), without masters the vector units (458 us, 4.8 TB/s; 75
-// instructions an element).  The norm reads at 6.1 TB/s (71 us), the reader of
+// 5.5 TB/s), without masters the vector units (424 - 472 us from run to run, 5.2 -
+// 4.6 TB/s; 75 instructions an element).  The norm reads at 6.1 TB/s (71 us), the reader of
 // states takes 244 us (5.4 TB/s).  Tensors at odd offsets cost 3 - 7%.
 // Streams that pass the caches by gained 4%; one block at a time in a whole
 // wave, sqrtf and integer conversions for the codes took 663 us without masters.

@@ -617,10 +617,10 @@ typedef struct df11_adamw_config {
  * One step of the n_tensors tensors, on stream st: one launch for every 36
  * tensors that are not empty, and as many small ones before them where
  * tensors have counts.  Pointers need their element's alignment only, so
- * tensors may lie anywhere in a unit.  No two buffers may
- * overlap (gradients that tensors share and counts excepted), and either all of them have masters or none
- * does.  Without d_step a captured call replays the
- * step number it was captured with.  Asynchronous.  Errors: DF11_E_INVALID
+ * tensors may lie anywhere in a unit.  No two buffers may overlap (gradients
+ * that tensors share and counts excepted), and either all tensors have masters
+ * or none does.  Without d_step a captured call replays the step number it was
+ * captured with.  Asynchronous.  Errors: DF11_E_INVALID
  * (null or misaligned pointers, a type, state_bits or number out of range:
  * lr, lr_scale and weight_decay finite and at least 0, beta1 and beta2 in
  * [0, 1), eps above 0 in float32, step at least 1; a master or counts of
@@ -647,8 +647,9 @@ int df11_adamw_step_counted(const df11_adamw_config *c, const df11_adamw_tensor 
 /*
  * The values that 8-bit states stand for: m_out[k] and v_out[k] receive tensor
  * k's numel values of m and v in type (DF11_TYPE_F32 or DF11_TYPE_BF16,
- * rounded to nearest); either list may be null.  Reads m, v, m_scale, v_scale
- * and numel of the tensors.  Asynchronous.  Errors as df11_adamw_step.
+ * rounded to nearest); either list may be null, and no two outputs may
+ * overlap.  Reads m, v, m_scale, v_scale and numel of the tensors.
+ * Asynchronous.  Errors as df11_adamw_step.
  */
 int df11_adamw_values(const df11_adamw_tensor *t, uint32_t n_tensors, uint32_t type,
                       void *const *m_out, void *const *v_out, df11_hip_stream st);
@@ -722,8 +723,9 @@ int df11_quantize_int8(uint32_t src_type, const df11_int8_rows *m, uint32_t n, d
  * y_stride at least rows; elements of y between rows and y_stride are left as
  * they were.  y must not overlap anything.  rows up to 2^24, n_tokens up to
  * 2^20, and no more results than the tiles of one grid of 2^32 threads cover
- * (2^35 always fit).  cols 0 gives zeros times the scales.  One launch on st, asynchronous, no workspace; the result does not
- * depend on how the work is split.  Errors: DF11_E_INVALID (null or misaligned
+ * (2^35 always fit).  cols 0 gives zeros times the scales.  One launch on st,
+ * asynchronous, no workspace; the result does not depend on how the work is
+ * split.  Errors: DF11_E_INVALID (null or misaligned
  * pointers, y_type, n_tensors, strides, sizes), DF11_E_HIP.
  */
 typedef struct df11_int8_tensor {
@@ -747,9 +749,9 @@ int df11_gemm_int8(uint32_t y_type, const df11_int8_tensor *t, uint32_t n_tensor
  * x_stride in elements of that type, rows contiguous, element alignment;
  * x_scale is not used): the tokens' rows are quantised into scratch, matrices
  * that name the same x (pointer, x_stride and cols) sharing the codes, and
- * multiplied.  scratch: device, 16-byte aligned, at least
- * df11_linear_int8_scratch_bytes(t, n_tensors, n_tokens) bytes (enough however
- * the matrices share), not shared by calls that may overlap; no
+ * multiplied; n_tokens rows of each x, less than 2^24 in all.  scratch: device,
+ * 16-byte aligned, at least df11_linear_int8_scratch_bytes(t, n_tensors,
+ * n_tokens) bytes (enough however the matrices share), not shared by calls that may overlap; no
  * initialisation needed.  Two launches on st; one token of 1 to 32768 columns
  * in every matrix takes one, and no scratch (0 bytes; it may be null then).
  * Errors as df11_gemm_int8, and DF11_E_INVALID for x_type and the scratch.
