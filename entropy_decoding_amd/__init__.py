@@ -196,11 +196,50 @@ class df11_int8_tensor(ctypes.Structure):
     ]
 
 
+class df11_embedding_lookup(ctypes.Structure):
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("tokens", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("table_stride", ctypes.c_uint64),
+        ("out_stride", ctypes.c_uint64),
+        ("rows", ctypes.c_uint64),
+        ("n", ctypes.c_uint64),
+        ("cols", ctypes.c_uint32),
+        ("table_type", ctypes.c_uint32),
+        ("out_type", ctypes.c_uint32),
+        ("token_bits", ctypes.c_uint32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class df11_embedding_grad(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_void_p),
+        ("dy", ctypes.c_void_p),
+        ("dw", ctypes.c_void_p),
+        ("dy_stride", ctypes.c_uint64),
+        ("dw_stride", ctypes.c_uint64),
+        ("rows", ctypes.c_uint64),
+        ("n", ctypes.c_uint64),
+        ("padding", ctypes.c_int64),
+        ("cols", ctypes.c_uint32),
+        ("dy_type", ctypes.c_uint32),
+        ("dw_type", ctypes.c_uint32),
+        ("token_bits", ctypes.c_uint32),
+        ("accumulate", ctypes.c_uint32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 DF11_INT8_MAX_TENSORS = 16
 DF11_INT8_MAX_COLS = 131071
 DF11_INT8_MAX_STRIDE = 1 << 22
 DF11_PIPELINE_MAX_SLOTS = 4
 DF11_ADAMW_BLOCK = 256
+DF11_EMBEDDING_MAX_TOKENS = 1 << 24
+DF11_EMBEDDING_MAX_ROWS = 1 << 24
+DF11_EMBEDDING_MAX_COLS = 1 << 20
 # df11_type, by the names of torch's types
 TYPES = {"float32": 0, "bfloat16": 1, "float16": 2}
 # df11_format; the names are what the binding's ``fmt`` arguments accept
@@ -297,9 +336,14 @@ def _load():
     L.df11_linear_int8.argtypes = [ctypes.c_uint32, ctypes.c_uint32,
                                    ctypes.POINTER(df11_int8_tensor), ctypes.c_uint32,
                                    ctypes.c_uint32, vp, ctypes.c_uint64, vp]
+    L.df11_embedding.argtypes = [ctypes.POINTER(df11_embedding_lookup), vp]
+    L.df11_embedding_gradient_scratch_bytes.argtypes = [ctypes.c_uint64, ctypes.c_uint32]
+    L.df11_embedding_gradient_scratch_bytes.restype = ctypes.c_uint64
+    L.df11_embedding_gradient.argtypes = [ctypes.POINTER(df11_embedding_grad), vp, ctypes.c_uint64, vp]
     for f in (L.df11_build_codebook, L.df11_encode_size, L.df11_encode,
               L.df11_quantize_int8, L.df11_gemm_int8, L.df11_linear_int8, L.df11_adamw_step,
               L.df11_adamw_step_counted, L.df11_adamw_values, L.df11_grad_norm,
+              L.df11_embedding, L.df11_embedding_gradient,
               L.df11_build_codebook_fmt, L.df11_encode_size_fmt, L.df11_encode_fmt,
               L.df11_decompress_block, L.df11_decompress_tensor, L.df11_pipeline_create,
               L.df11_pipeline_destroy, L.df11_pipeline_decompress, L.df11_pipeline_acquire,
@@ -1391,6 +1435,136 @@ class AdamW(_Lender):
         torch.cuda.synchronize(self.device)
         with torch.cuda.device(self.device):  # the encoder works on the current device's streams
             return encode_on_device(self.weights, stream=stream)
+
+
+# ---------------------------------------------------------------- embedding and output head
+
+
+def _rows_apart(t, what, device=None):
+    """Checks a 2-D device tensor whose rows are contiguous; returns its row stride."""
+    if t.dim() != 2 or not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{what} must be a 2-D tensor on {'a device' if device is None else device}")
+    if (t.size(1) > 1 and t.stride(1) != 1) or t.stride(0) < 0:
+        raise ValueError(f"{what} must have contiguous rows")
+    return t.stride(0) if t.size(0) > 1 else t.size(1)
+
+
+def _output(t, what, shape, dtype, device):
+    """Checks a given output: rows that lie apart, of the shape and type; returns its row stride."""
+    stride = _rows_apart(t, what, device)
+    if tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what} must be {list(shape)}" + (f" of {dtype}" if dtype is not None else ""))
+    if stride < t.size(1):
+        raise ValueError(f"{what} must have rows of their own")
+    return stride
+
+
+def _token_bits(tokens, device) -> int:
+    bits = _TOKEN_BITS.get(str(tokens.dtype))
+    if bits is None:
+        raise TypeError("tokens must be int32 or int64")
+    if tokens.device != device:
+        raise ValueError(f"tokens must be on {device}")
+    return bits
+
+
+_TOKEN_BITS = {"torch.int32": 32, "torch.int64": 64}
+
+
+class Embedding(_Lender):
+    """Rows of a table [rows, cols] (BF16, F16 or float32, contiguous rows), looked
+    up by token and multiplied with ``scale`` (df11_embedding: one launch).  The
+    table is used in place: a step of AdamW on it is seen by later calls."""
+
+    def __init__(self, table, scale: float = 1.0, padding_idx: int | None = None):
+        stride = _rows_apart(table, "the table")
+        self.table, self.scale, self.padding_idx = table, float(scale), padding_idx
+        self.device, self._memory, self._lent = table.device, [table.detach()], set()
+        self._a = df11_embedding_lookup(table=table.data_ptr(), table_stride=stride, rows=table.size(0),
+                                        cols=table.size(1), table_type=_type(table.dtype), scale=scale)
+
+    def __call__(self, tokens, out_dtype=None, out=None, stream=None):
+        """The tokens' rows: [*tokens.shape, cols] of ``out_dtype`` (the table's by
+        default), or written into ``out`` [number of tokens, cols].  ``tokens``:
+        int32 or int64; one outside the table gives a row of NaN.  The call
+        records no graph: a table that requires a gradient is refused (call
+        under torch.no_grad(), and ``gradient`` makes the table's)."""
+        import torch
+
+        if self.table.requires_grad and torch.is_grad_enabled():
+            raise RuntimeError("a lookup records no gradient for its table: call it under torch.no_grad()")
+        a = df11_embedding_lookup.from_buffer_copy(self._a)
+        a.token_bits, a.n = _token_bits(tokens, self.device), tokens.numel()
+        if out is not None:
+            a.out_stride = _output(out, "out", (a.n, a.cols), out_dtype, self.device)
+            out_dtype = out.dtype
+        elif out_dtype is None:
+            out_dtype = self.table.dtype
+        a.out_type = _type(out_dtype)
+        guard, st = _on(self.device, stream)
+        with guard:
+            given, tokens = tokens, tokens.contiguous()
+            if out is None:
+                out, a.out_stride = torch.empty(*tokens.shape, a.cols, dtype=out_dtype, device=self.device), a.cols
+            a.tokens, a.out = tokens.data_ptr(), out.data_ptr()
+            _check("df11_embedding", LIB.df11_embedding(ctypes.byref(a), st))
+        if st not in self._lent:
+            self._lend(stream, st)
+        if stream is not None:
+            _lend(self.device, stream, [given, out])
+        return out
+
+    def gradient(self, tokens, dy, out=None, dtype=None, accumulate: bool = False, stream=None):
+        """The table's gradient of a call with these tokens whose output's gradient
+        is ``dy``: embedding_gradient with the table's rows, scale and padding."""
+        return embedding_gradient(tokens, dy, self.table.size(0), dtype or self.table.dtype, out, accumulate,
+                                  self.scale, self.padding_idx, stream)
+
+
+def embedding_gradient(tokens, dy, rows: int, dtype=None, out=None, accumulate: bool = False,
+                       scale: float = 1.0, padding_idx: int | None = None, stream=None):
+    """df11_embedding_gradient: the gradient [rows, cols] of a table whose lookup of
+    ``tokens`` (int32 or int64, any shape) has the output gradient ``dy``
+    [*tokens.shape, cols] or [number of tokens, cols] (BF16, F16 or float32), as
+    a new tensor of ``dtype`` (dy's by default), or written into ``out``, or with
+    ``accumulate`` added to it.  Tokens equal to ``padding_idx``, and tokens
+    outside the table, add nothing.  Deterministic."""
+    import torch
+
+    device = dy.device
+    if dy.dim() != 2:
+        if dy.dim() < 2 or tuple(dy.shape[:-1]) != tuple(tokens.shape):
+            raise ValueError("dy must be [number of tokens, cols]")
+        dy = dy.view(tokens.numel(), dy.size(-1))
+    g = df11_embedding_grad(dy_stride=_rows_apart(dy, "dy", device), rows=rows, n=tokens.numel(),
+                            padding=-1 if padding_idx is None else padding_idx, cols=dy.size(1),
+                            dy_type=_type(dy.dtype), token_bits=_token_bits(tokens, device),
+                            accumulate=bool(accumulate), scale=scale)
+    if dy.size(0) != g.n or rows < 0:
+        raise ValueError("dy must be [number of tokens, cols]")
+    if padding_idx is not None and not 0 <= padding_idx < rows:
+        raise ValueError("padding_idx must be a row of the table")
+    if out is not None:
+        g.dw_stride = _output(out, "out", (rows, g.cols), dtype, device)
+    elif accumulate:
+        raise ValueError("accumulate adds to out")
+    guard, st = _on(device, stream)
+    with guard:
+        given, tokens = tokens, tokens.contiguous()
+        made = out is None
+        if made:
+            out, g.dw_stride = torch.empty(rows, g.cols, dtype=dtype or dy.dtype, device=device), g.cols
+        g.dw_type = _type(out.dtype)
+        need = int(LIB.df11_embedding_gradient_scratch_bytes(g.n, g.cols))
+        scratch = torch.empty(need, dtype=torch.uint8, device=device)
+        g.tokens, g.dy, g.dw = tokens.data_ptr(), dy.data_ptr(), out.data_ptr()
+        _check("df11_embedding_gradient",
+               LIB.df11_embedding_gradient(ctypes.byref(g), scratch.data_ptr(), need, st))
+    if not made:
+        torch._C._increment_version([out])
+    if stream is not None:
+        _lend(device, stream, [given, dy, out])
+    return out
 
 
 def table_bytes(cb: df11_codebook) -> int:

@@ -762,6 +762,81 @@ int df11_linear_int8(uint32_t x_type, uint32_t y_type, const df11_int8_tensor *t
                      uint32_t n_tensors, uint32_t n_tokens, void *scratch, uint64_t scratch_bytes,
                      df11_hip_stream st);
 
+/*
+ * The two ends of a model, where the vocabulary is -- device.  The embedding
+ * table and the output head have a row for every token of the vocabulary and
+ * are the largest matrices of a checkpoint; the operators below read them and
+ * make the gradients that df11_adamw_step takes.
+ *
+ * df11_embedding: rows of a table looked up by token and scaled,
+ *   out[i][c] = scale * table[tokens[i]][c]      (float32, rounded once to out_type)
+ * A token outside 0 .. rows - 1 gets a row of NaN.  Rows of the table begin
+ * table_stride elements apart, those of out out_stride; columns between cols
+ * and the stride are left as they were.  Every pointer needs its element's
+ * alignment only.  out must not overlap anything.  One launch on st,
+ * asynchronous.  Errors: DF11_E_INVALID (null or misaligned pointers, types,
+ * token_bits, sizes, a stride of 2^40 and more, or of what is written below
+ * cols, 2^26 parts of 2048 columns and more), DF11_E_HIP.
+ */
+#define DF11_EMBEDDING_MAX_TOKENS (1u << 24)
+#define DF11_EMBEDDING_MAX_ROWS (1u << 24)
+#define DF11_EMBEDDING_MAX_COLS (1u << 20)
+typedef struct df11_embedding_lookup {
+    const void *table;       /* rows x cols of table_type */
+    const void *tokens;      /* n integers of token_bits, signed */
+    void *out;               /* n x cols of out_type */
+    uint64_t table_stride;
+    uint64_t out_stride;
+    uint64_t rows;           /* 0 .. DF11_EMBEDDING_MAX_ROWS */
+    uint64_t n;              /* 0 .. DF11_EMBEDDING_MAX_TOKENS */
+    uint32_t cols;           /* 0 .. DF11_EMBEDDING_MAX_COLS */
+    uint32_t table_type;     /* df11_type */
+    uint32_t out_type;       /* df11_type */
+    uint32_t token_bits;     /* 32 or 64 */
+    float scale;
+} df11_embedding_lookup;
+
+int df11_embedding(const df11_embedding_lookup *e, df11_hip_stream st);
+
+/*
+ * df11_embedding_gradient: what the table of such a lookup receives,
+ *   dw[v][c] = scale * sum over the i with tokens[i] = v of dy[i][c]
+ * or, with accumulate, dw[v][c] + that (as where microbatches add up, or an
+ * output head shares the table's memory).  Sums are float32: chunks of 16 to
+ * 128 tokens of a row (a number that depends on n alone), each in the order of
+ * their positions, then the chunks in order; scaled, added and rounded once to
+ * dw_type.  No atomics on floats: the same inputs give the same bits.  Rows
+ * without a token are set to zeros; with accumulate they are neither read nor
+ * written.  Tokens equal to padding (-1: none) and tokens outside
+ * 0 .. rows - 1 add nothing.  Alignment and strides as df11_embedding's; dw
+ * must not overlap anything; dy's rows may be one and the same (stride 0).
+ * scratch: device, 128-byte aligned, at least
+ * df11_embedding_gradient_scratch_bytes(n, cols) bytes, not shared by calls
+ * that may overlap; no initialisation needed.  Three launches on st (two for
+ * up to 16 tokens), asynchronous.  Errors as df11_embedding's, and
+ * DF11_E_INVALID for accumulate and the scratch.
+ */
+typedef struct df11_embedding_grad {
+    const void *tokens;      /* n integers of token_bits, signed */
+    const void *dy;          /* n x cols of dy_type */
+    void *dw;                /* rows x cols of dw_type */
+    uint64_t dy_stride;
+    uint64_t dw_stride;
+    uint64_t rows;
+    uint64_t n;
+    int64_t padding;
+    uint32_t cols;
+    uint32_t dy_type;        /* df11_type */
+    uint32_t dw_type;        /* df11_type */
+    uint32_t token_bits;     /* 32 or 64 */
+    uint32_t accumulate;     /* 0 or 1 */
+    float scale;
+} df11_embedding_grad;
+
+uint64_t df11_embedding_gradient_scratch_bytes(uint64_t n, uint32_t cols);
+int df11_embedding_gradient(const df11_embedding_grad *g, void *scratch, uint64_t scratch_bytes,
+                            df11_hip_stream st);
+
 #ifdef __cplusplus
 }
 #endif
