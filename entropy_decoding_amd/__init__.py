@@ -232,6 +232,47 @@ class df11_embedding_grad(ctypes.Structure):
     ]
 
 
+class df11_vocab_piece(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("targets", ctypes.c_void_p),
+        ("w", ctypes.c_void_p),
+        ("x_stride", ctypes.c_uint64),
+        ("w_stride", ctypes.c_uint64),
+        ("ignored", ctypes.c_int64),
+        ("n", ctypes.c_uint32),
+        ("cols", ctypes.c_uint32),
+        ("vocab", ctypes.c_uint32),
+        ("first", ctypes.c_uint32),
+        ("rows", ctypes.c_uint32),
+        ("target_bits", ctypes.c_uint32),
+        ("begin", ctypes.c_uint32),
+        ("end", ctypes.c_uint32),
+    ]
+
+
+class df11_vocab_sizes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint32) for n in ("n", "cols", "rows", "dx", "two_terms")]
+
+
+class df11_vocab_grad(ctypes.Structure):
+    _fields_ = [
+        ("lse", ctypes.c_void_p),
+        ("loss_grad", ctypes.c_void_p),
+        ("lse_grad", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p),
+        ("dw", ctypes.c_void_p),
+        ("dx_stride", ctypes.c_uint64),
+        ("dw_stride", ctypes.c_uint64),
+        ("loss_grads", ctypes.c_uint32),
+        ("lse_grads", ctypes.c_uint32),
+        ("dx_type", ctypes.c_uint32),
+        ("dw_type", ctypes.c_uint32),
+        ("accumulate", ctypes.c_uint32),
+        ("loss_grad_all", ctypes.c_float),
+    ]
+
+
 DF11_INT8_MAX_TENSORS = 16
 DF11_INT8_MAX_COLS = 131071
 DF11_INT8_MAX_STRIDE = 1 << 22
@@ -240,6 +281,10 @@ DF11_ADAMW_BLOCK = 256
 DF11_EMBEDDING_MAX_TOKENS = 1 << 24
 DF11_EMBEDDING_MAX_ROWS = 1 << 24
 DF11_EMBEDDING_MAX_COLS = 1 << 20
+DF11_VOCAB_MAX_TOKENS = 1 << 20
+DF11_VOCAB_MAX_ROWS = 1 << 24
+DF11_VOCAB_MAX_COLS = 1 << 20
+DF11_VOCAB_MAX_STRIDE = 1 << 21
 # df11_type, by the names of torch's types
 TYPES = {"float32": 0, "bfloat16": 1, "float16": 2}
 # df11_format; the names are what the binding's ``fmt`` arguments accept
@@ -340,10 +385,17 @@ def _load():
     L.df11_embedding_gradient_scratch_bytes.argtypes = [ctypes.c_uint64, ctypes.c_uint32]
     L.df11_embedding_gradient_scratch_bytes.restype = ctypes.c_uint64
     L.df11_embedding_gradient.argtypes = [ctypes.POINTER(df11_embedding_grad), vp, ctypes.c_uint64, vp]
+    vs = ctypes.POINTER(df11_vocab_sizes)
+    for f in (L.df11_vocab_loss_scratch_bytes, L.df11_vocab_loss_gradient_scratch_bytes):
+        f.argtypes, f.restype = [vs], ctypes.c_uint64
+    L.df11_vocab_loss.argtypes = [ctypes.POINTER(df11_vocab_piece), vp, vp, vp, ctypes.c_uint64, vp]
+    L.df11_vocab_loss_gradient.argtypes = [ctypes.POINTER(df11_vocab_piece),
+                                           ctypes.POINTER(df11_vocab_grad), vs, vp, ctypes.c_uint64, vp]
     for f in (L.df11_build_codebook, L.df11_encode_size, L.df11_encode,
               L.df11_quantize_int8, L.df11_gemm_int8, L.df11_linear_int8, L.df11_adamw_step,
               L.df11_adamw_step_counted, L.df11_adamw_values, L.df11_grad_norm,
-              L.df11_embedding, L.df11_embedding_gradient,
+              L.df11_embedding, L.df11_embedding_gradient, L.df11_vocab_loss,
+              L.df11_vocab_loss_gradient,
               L.df11_build_codebook_fmt, L.df11_encode_size_fmt, L.df11_encode_fmt,
               L.df11_decompress_block, L.df11_decompress_tensor, L.df11_pipeline_create,
               L.df11_pipeline_destroy, L.df11_pipeline_decompress, L.df11_pipeline_acquire,
@@ -1565,6 +1617,195 @@ def embedding_gradient(tokens, dy, rows: int, dtype=None, out=None, accumulate: 
     if stream is not None:
         _lend(device, stream, [given, dy, out])
     return out
+
+
+class VocabLoss(_Lender):
+    """Softmax cross entropy of hidden states under an output head, without keeping
+    the logits (df11_vocab_loss), and its gradients (df11_vocab_loss_gradient).
+
+    ``pieces``: BF16 device tensors [rows, cols] that hold consecutive rows of the
+    head (one tensor for a whole one), cols and row strides multiples of 8, on 16
+    bytes.  They are used in place: a step of AdamW on them is seen by later calls.
+    """
+
+    def __init__(self, pieces):
+        import torch
+
+        pieces = list(pieces)
+        if not pieces:
+            raise ValueError("no pieces")
+        strides = [_rows_apart(w, "pieces", pieces[0].device) for w in pieces]
+        for w in pieces:
+            if w.dtype != torch.bfloat16 or w.size(1) != pieces[0].size(1):
+                raise ValueError("pieces must be bfloat16 with equal columns")
+        self._hold([tuple(w.shape) for w in pieces], pieces[0].device, [w.detach() for w in pieces])
+        self.pieces = pieces
+        self._held = [(w.data_ptr(), stride) for w, stride in zip(pieces, strides)]
+
+    @classmethod
+    def from_unit(cls, ds: DeviceStream, shapes):
+        """A head that stays compressed: a BF16 unit whose tensors are its pieces, of
+        ``shapes``.  Every call decompresses one at a time into memory of the
+        largest one's size, a gradient's call too."""
+        shapes = [(int(r), int(c)) for r, c in shapes]
+        if ds.desc.format != 0 or ds.desc.n_tensors != len(shapes) or not shapes:
+            raise ValueError("one shape for each tensor of a BF16 unit")
+        ends = np.cumsum([0] + [r * c for r, c in shapes])
+        if any(int(ds.desc.tensor_offsets[k]) != e for k, e in enumerate(ends)):
+            raise ValueError("the shapes must be those of the unit's tensors")
+        head = cls.__new__(cls)
+        head._hold(shapes, ds.stream.device, [ds.stream, ds.sm, ds.gaps, ds.block_out_pos, ds.tables])
+        head.unit, head.pieces = ds, None
+        return head
+
+    def _hold(self, shapes, device, memory):
+        self.shapes, self.device, self._memory, self._lent = shapes, device, memory, set()
+        self.vocab, self.cols = sum(r for r, _ in shapes), shapes[0][1]
+        if any(c != self.cols for _, c in shapes):
+            raise ValueError("pieces must have equal columns")
+        self._first = np.cumsum([0] + [r for r, _ in shapes]).tolist()
+        self._rows = max(r for r, _ in shapes)
+
+    def _each(self, p, status, st):
+        """Sets p to each piece in turn, decompressed where it has to be."""
+        import torch
+
+        slot = None
+        if self.pieces is None:
+            slot = torch.empty(self._rows * self.cols, dtype=torch.bfloat16, device=self.device)
+        last = len(self.shapes) - 1
+        for k, (rows, cols) in enumerate(self.shapes):
+            p.first, p.rows, p.begin, p.end = self._first[k], rows, k == 0, k == last
+            if slot is None:
+                p.w, p.w_stride = self._held[k]
+            else:
+                df11_decompress_tensor(self.unit, k, slot[:rows * cols], status, st)
+                p.w, p.w_stride = slot.data_ptr(), cols
+            yield k
+
+    def _piece(self, x, targets, ignore_index):
+        """x as [n, cols], and what all pieces of a call share."""
+        import torch
+
+        if x.dtype != torch.bfloat16:
+            raise TypeError("hidden states must be bfloat16")
+        if x.dim() != 2:
+            if x.dim() < 1 or x.shape[:-1] != targets.shape:
+                raise ValueError("hidden states must be [*targets.shape, cols]")
+            x = x.view(targets.numel(), x.size(-1))
+        stride = _rows_apart(x, "hidden states", self.device)
+        if x.shape != (targets.numel(), self.cols):
+            raise ValueError("hidden states must be [number of targets, cols]")
+        return x, df11_vocab_piece(x=x.data_ptr(), x_stride=stride, n=x.size(0), cols=self.cols,
+                                   vocab=self.vocab, ignored=ignore_index,
+                                   target_bits=_token_bits(targets, self.device))
+
+    def __call__(self, x, targets, ignore_index: int = -100, status=None, stream=None):
+        """(losses, lse), float32 like ``targets`` (int32 or int64): the cross entropy
+        of each token, and the logarithm of its sum of exponentials.  ``x``: BF16
+        hidden states [*targets.shape, cols] or [number of targets, cols].  A target
+        of ``ignore_index`` has loss 0, another one outside the vocabulary NaN.
+        ``status``: for a compressed head, as in df11_decompress_tensor.  The call
+        records no graph: hidden states that require a gradient are refused (detach
+        them; ``gradient`` makes it)."""
+        import torch
+
+        if x.requires_grad and torch.is_grad_enabled():
+            raise RuntimeError("a loss records no gradient for its hidden states: detach them")
+        x, p = self._piece(x, targets, ignore_index)
+        guard, st = _on(self.device, stream)
+        with guard:
+            given, targets = targets, targets.contiguous()
+            p.targets = targets.data_ptr()
+            losses = torch.empty(targets.shape, dtype=torch.float32, device=self.device)
+            lse = torch.empty_like(losses)
+            need = int(LIB.df11_vocab_loss_scratch_bytes(df11_vocab_sizes(p.n, p.cols, self._rows, 0, 0)))
+            scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
+            for _ in self._each(p, status, st):
+                _check("df11_vocab_loss",
+                       LIB.df11_vocab_loss(p, losses.data_ptr(), lse.data_ptr(), scratch.data_ptr(), need, st))
+        self._used(stream, st, [x, given, losses, lse] + ([] if status is None else [status]))
+        return losses, lse
+
+    def _used(self, stream, st, tensors):
+        if st not in self._lent:
+            self._lend(stream, st)
+        if stream is not None:
+            _lend(self.device, stream, tensors)
+
+    def gradient(self, x, targets, lse, loss_grad=1.0, lse_grad=None, ignore_index: int = -100,
+                 dx_dtype=None, dw_dtype=None, dx=None, dws=None, accumulate: bool = False,
+                 needs_dx: bool = True, needs_dw: bool = True, status=None, stream=None):
+        """(dx, dws) of a call with these arguments that returned ``lse``: the hidden
+        states' gradient [n, cols] and a list of the pieces' gradients, BF16 or
+        float32 (``dx_dtype``, ``dw_dtype``: BF16 by default; float32 doubles that
+        product's work), as new tensors or written into ``dx`` and ``dws``, with
+        ``accumulate`` added to dws.  ``loss_grad``: the gradient that the losses
+        have, a number or a float32 device tensor of one or of n elements;
+        ``lse_grad``: that of lse, such a tensor or None.  Ignored tokens have no
+        gradient and add none.  Without ``needs_dx`` or ``needs_dw`` that one is None."""
+        import torch
+
+        x, p = self._piece(x, targets, ignore_index)
+        n, cols = p.n, p.cols
+        g = df11_vocab_grad(accumulate=bool(accumulate))
+        factors = []
+        for name, value in (("lse", lse), ("loss_grad", loss_grad), ("lse_grad", lse_grad)):
+            if value is None or (name == "loss_grad" and not hasattr(value, "data_ptr")):
+                continue
+            if (value.dtype != torch.float32 or value.device != self.device or not value.is_contiguous()
+                    or value.numel() not in ((n,) if name == "lse" else (1, n))):
+                raise ValueError(f"{name} must be contiguous float32 on {self.device}, one for each token")
+            factors.append(value)
+            setattr(g, name, value.data_ptr())
+            if name != "lse":
+                setattr(g, name + "s", value.numel())
+        if not hasattr(loss_grad, "data_ptr"):
+            g.loss_grad_all = loss_grad
+        kinds = {}
+        for name, needed, given, shapes, kind in (
+                ("dx", needs_dx, None if dx is None else [dx], [(n, cols)], dx_dtype),
+                ("dw", needs_dw, None if dws is None else list(dws), self.shapes, dw_dtype)):
+            if given is not None:
+                if not needed or len(given) != len(shapes) or not given:
+                    raise ValueError(f"{name}: a tensor for each gradient that is needed")
+                kind = kind or given[0].dtype
+                for t, shape in zip(given, shapes):
+                    _output(t, name, shape, kind, self.device)
+            kind = kind or torch.bfloat16
+            if kind not in (torch.bfloat16, torch.float32):
+                raise TypeError(f"{name} must be bfloat16 or float32")
+            kinds[name] = kind if needed else None
+        if accumulate and (dws is None or not needs_dw):
+            raise ValueError("accumulate adds to dws")
+        made = [t for t in (([] if dx is None else [dx]) + ([] if dws is None else list(dws)))]
+        guard, st = _on(self.device, stream)
+        with guard:
+            given, targets = targets, targets.contiguous()
+            p.targets = targets.data_ptr()
+            if needs_dx:
+                if dx is None:
+                    dx = torch.empty(n, cols, dtype=kinds["dx"], device=self.device)
+                g.dx, g.dx_stride, g.dx_type = dx.data_ptr(), dx.stride(0) if n > 1 else cols, _type(dx.dtype)
+            if needs_dw:
+                if dws is None:
+                    dws = [torch.empty(shape, dtype=kinds["dw"], device=self.device) for shape in self.shapes]
+                g.dw_type = _type(kinds["dw"])
+            sizes = df11_vocab_sizes(n, cols, self._rows, needs_dx, torch.float32 in kinds.values())
+            need = int(LIB.df11_vocab_loss_gradient_scratch_bytes(sizes))
+            scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
+            for k in self._each(p, status, st):
+                if needs_dw:
+                    dw = dws[k]
+                    g.dw, g.dw_stride = dw.data_ptr(), dw.stride(0) if p.rows > 1 else cols
+                _check("df11_vocab_loss_gradient",
+                       LIB.df11_vocab_loss_gradient(p, g, sizes, scratch.data_ptr(), need, st))
+        if made:
+            torch._C._increment_version(made)
+        dx, dws = dx if needs_dx else None, list(dws) if needs_dw else None
+        self._used(stream, st, [x, given, *factors, *([dx] if needs_dx else []), *(dws or []),
+                                *([] if status is None else [status])])
+        return dx, dws
 
 
 def table_bytes(cb: df11_codebook) -> int:

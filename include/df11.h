@@ -837,6 +837,106 @@ uint64_t df11_embedding_gradient_scratch_bytes(uint64_t n, uint32_t cols);
 int df11_embedding_gradient(const df11_embedding_grad *g, void *scratch, uint64_t scratch_bytes,
                             df11_hip_stream st);
 
+/*
+ * Softmax cross entropy under a large output head, without keeping the logits.
+ * For the hidden states x[t] (n tokens of cols BF16) and a head w of vocab rows
+ * (BF16), in pieces of consecutive rows:
+ *   l[t][v] = x[t] . w[v]    lse[t] = log(sum over v of exp(l[t][v]))
+ *   loss[t] = lse[t] - l[t][targets[t]]
+ * Products are exact, sums, exponentials and logarithms float32.  A token whose
+ * target is `ignored` has loss 0 (and its lse); any other target outside
+ * 0 .. vocab - 1 gives a loss of NaN.  A token with a logit of +infinity or NaN
+ * has lse and loss NaN; logits of -infinity count nothing.
+ *
+ * A call takes one piece: rows `first` .. first + rows - 1 of the head, at w.  A
+ * head in one piece is one call with begin = end = 1; a head in several (decoded
+ * one after another into the same memory, say) is a call for each, in any order,
+ * the first with begin, the last with end, between which scratch holds the
+ * sums: losses and lse are written by the last.  Two launches a call.
+ * x and w 16-byte aligned, cols and the strides multiples of 8.
+ */
+#define DF11_VOCAB_MAX_TOKENS (1u << 20)
+#define DF11_VOCAB_MAX_ROWS (1u << 24)
+#define DF11_VOCAB_MAX_COLS (1u << 20)
+#define DF11_VOCAB_MAX_STRIDE (1u << 21)
+typedef struct df11_vocab_piece {
+    const void *x;           /* n x cols, BF16 */
+    const void *targets;     /* n integers of target_bits, signed */
+    const void *w;           /* rows x cols, BF16 */
+    uint64_t x_stride;       /* elements, up to DF11_VOCAB_MAX_STRIDE, like w_stride */
+    uint64_t w_stride;
+    int64_t ignored;         /* usually -100 */
+    uint32_t n;              /* 0 .. DF11_VOCAB_MAX_TOKENS */
+    uint32_t cols;           /* 0 .. DF11_VOCAB_MAX_COLS */
+    uint32_t vocab;          /* rows of the whole head, 1 .. DF11_VOCAB_MAX_ROWS */
+    uint32_t first;
+    uint32_t rows;
+    uint32_t target_bits;    /* 32 or 64 */
+    uint32_t begin;          /* 0 or 1 */
+    uint32_t end;            /* 0 or 1 */
+} df11_vocab_piece;
+
+/* What a scratch is sized for. */
+typedef struct df11_vocab_sizes {
+    uint32_t n, cols;
+    uint32_t rows;           /* of the largest piece */
+    uint32_t dx;             /* 1: the gradient of x is asked for */
+    uint32_t two_terms;      /* 1: a gradient in float32 is */
+} df11_vocab_sizes;
+
+/*
+ * losses and lse: device, n floats.  scratch: device, 256-byte aligned, at
+ * least df11_vocab_loss_scratch_bytes bytes for the largest piece, not shared
+ * by calls that may overlap; no initialisation needed.  Asynchronous.  Outputs
+ * must not overlap anything.  Errors: DF11_E_INVALID (null or misaligned
+ * pointers, sizes, strides, a piece outside the head, the scratch), DF11_E_HIP.
+ */
+uint64_t df11_vocab_loss_scratch_bytes(const df11_vocab_sizes *z);
+int df11_vocab_loss(const df11_vocab_piece *p, float *losses, float *lse, void *scratch,
+                    uint64_t scratch_bytes, df11_hip_stream st);
+
+/*
+ * The gradients of x and of the head for given gradients a of the losses and c
+ * of lse (each one number, or one for every token):
+ *   g[t][v] = (a[t] + c[t]) exp(l[t][v] - lse[t]) - a[t] [v = targets[t]]
+ *   dx = g w       dw = g^T x       (dw + that, with accumulate)
+ * The logits are computed again.  g is rounded to BF16 for gradients in BF16;
+ * for those in float32 it is held as two BF16 terms (16 bits and more), which
+ * doubles their products.  Sums are float32, rounded once.  Ignored tokens have
+ * no gradient at all: their dx is zero, and nothing of their x (which may be
+ * NaN) enters dw.  A target outside the head makes its token's dx and all of dw
+ * NaN.  Pieces as above: begin, then dw of each piece is written by its own
+ * call, dx by the one with end.  g exists for 2^27 elements at a time.
+ * 2 launches for begin, 1 for end, and 3 for every 2^27 elements of g.
+ */
+typedef struct df11_vocab_grad {
+    const float *lse;        /* n, from df11_vocab_loss */
+    const float *loss_grad;  /* loss_grads (1 or n) values; null: loss_grad_all */
+    const float *lse_grad;   /* lse_grads (1 or n) values; null: none */
+    void *dx;                /* n x cols of dx_type (with sizes->dx) */
+    void *dw;                /* rows x cols of dw_type, or null */
+    uint64_t dx_stride;
+    uint64_t dw_stride;
+    uint32_t loss_grads;
+    uint32_t lse_grads;
+    uint32_t dx_type;        /* DF11_TYPE_F32 or DF11_TYPE_BF16 */
+    uint32_t dw_type;
+    uint32_t accumulate;     /* 0 or 1 */
+    float loss_grad_all;
+} df11_vocab_grad;
+
+/*
+ * sizes: those that the scratch was sized for, the same in all calls of a
+ * gradient, as n, cols, x, targets and lse are.  scratch as above, of
+ * df11_vocab_loss_gradient_scratch_bytes bytes.  dx and dw need their element's
+ * alignment only, and must not overlap anything.  Deterministic.  Asynchronous.
+ * Errors as df11_vocab_loss's.
+ */
+uint64_t df11_vocab_loss_gradient_scratch_bytes(const df11_vocab_sizes *z);
+int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g,
+                             const df11_vocab_sizes *sizes, void *scratch, uint64_t scratch_bytes,
+                             df11_hip_stream st);
+
 #ifdef __cplusplus
 }
 #endif
