@@ -1495,7 +1495,7 @@ class AdamW(_Lender):
 def _rows_apart(t, what, device=None):
     """Checks a 2-D device tensor whose rows are contiguous; returns its row stride."""
     if t.dim() != 2 or not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{what} must be a 2-D tensor on {'a device' if device is None else device}")
+        raise ValueError(f"{what} must be a 2-D device tensor" + ("" if device is None else f" on {device}"))
     if (t.size(1) > 1 and t.stride(1) != 1) or t.stride(0) < 0:
         raise ValueError(f"{what} must have contiguous rows")
     return t.stride(0) if t.size(0) > 1 else t.size(1)

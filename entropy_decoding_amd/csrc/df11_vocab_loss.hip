@@ -10,7 +10,7 @@
 // value and sum of exponentials, or its part of g.  g exists in BF16 for a
 // piece of the vocabulary at a time.
 //
-//   loss_tiles      logits of a tile; largest value, sum, target's logit
+//   stats tiles     logits of a tile; the target's, and the others' largest value and sum
 //   loss_join       joins tiles and pieces: lse and loss
 //   pick, gather    the tokens that have a gradient, one behind the other
 //   grad tiles      logits again; g
@@ -59,7 +59,7 @@ struct TileArgs {
     // STATS and GRAD
     const void *targets;
     uint32_t target_bits, first;
-    float2 *part;         // [token / 16][tile][token % 16]: largest, sum
+    float2 *part;         // [token / 16][tile][token % 16]: largest, sum of the others
     uint32_t part_tiles;
     float *told;          // the targets' logits
     const float *lse;
@@ -72,6 +72,7 @@ struct TileArgs {
     void *y;
     uint64_t y_stride, y_split;
     uint32_t add;
+    uint32_t past;  // store past the caches
 };
 
 // A tile's operand whose rows are consecutive in k: 128 bytes of each of ROWS
@@ -391,8 +392,9 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     const uint32_t r = 16 * h + 4 * q + e;
-                    told = target == r ? acc[f][h][e] : told;
-                    if (r0 + wr + r >= a.r_size) acc[f][h][e] = -__builtin_inff();
+                    const bool is = target == r;
+                    told = is ? acc[f][h][e] : told;
+                    if (is || r0 + wr + r >= a.r_size) acc[f][h][e] = -__builtin_inff();
                     top = fmaxf(top, acc[f][h][e]);
                 }
             if (target < 16 * FR && (target >> 2 & 3) == q) a.told[t] = told;
@@ -459,7 +461,8 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
 #pragma unroll
                         for (uint32_t e = 0; e < kEach; e++) sum[e] = Y(v[e]);
                     }
-                    *reinterpret_cast<YE_any *>(to) = sum;
+                    if (KIND == DW && a.past) __builtin_nontemporal_store(YE_any(sum), reinterpret_cast<YE_any *>(to));
+                    else *reinterpret_cast<YE_any *>(to) = sum;
                 } else {
 #pragma unroll
                     for (uint32_t e = 0; e < kEach - 1; e++)
@@ -580,11 +583,26 @@ __global__ __launch_bounds__(1024) void loss_join(TokenArgs a) {
     if (!a.begin) r = joined(a.state[t], r);
     a.state[t] = r;
     if (!a.end) return;
-    const float lse = r.x == -__builtin_inff() ? r.x + 0.0f * r.y : r.x + logf(r.y);
+    // o: the logarithm of the others' sum; with d = o - l[target] the loss is
+    // log(1 + exp d), which keeps its digits where the target is nearly certain
+    const float inf = __builtin_inff(), nan = __builtin_nanf("");
+    const float of_sum = r.x == -inf ? 0.0f * r.y : logf(r.y);
+    const float o = r.x + of_sum;
     const int64_t target = target_at(a, t);
+    if (target < 0 || target >= a.vocab) {
+        a.lse[t] = o;
+        a.losses[t] = target == a.ignored ? 0.0f : nan;
+        return;
+    }
+    const float told = a.told[t], d = r.x - told + of_sum;
+    const float more = log1pf(expf(-fabsf(d)));
+    float loss = fmaxf(d, 0.0f) + more, lse = d > 0.0f ? o + more : told + loss;
+    if (d != d || told == inf) {  // NaN, an infinite logit, or none above -infinity
+        loss = nan;
+        lse = o == -inf && told == -inf ? -inf : nan;
+    }
     a.lse[t] = lse;
-    a.losses[t] = target == a.ignored ? 0.0f
-                  : target >= 0 && target < a.vocab ? lse - a.told[t] : __builtin_nanf("");
+    a.losses[t] = target == a.ignored ? 0.0f : loss;
 }
 
 // The tokens that have a gradient, in order, with what their part of g needs.
@@ -650,32 +668,83 @@ __global__ __launch_bounds__(256) void spread(TokenArgs a) {
 
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
+// The tiles, how many workgroups a compute unit holds, and the microseconds of a
+// stage with the chip full of them and with one of them alone, fitted to the
+// logits of 16 to 8192 tokens x 128256 rows x 4096 columns and of 1001 x 32003 x
+// 1000.
 struct Tile {
-    uint32_t t, r;
+    uint32_t t, r, held;
+    float full, alone;
 };
-constexpr Tile kTiles[] = {{32, 64}, {64, 64}, {128, 128}, {256, 256}};
+constexpr Tile kTiles[] = {{32, 64, 2, 0.30f, 0.20f},   {64, 64, 2, 0.42f, 0.23f},  {64, 128, 2, 0.73f, 0.35f},
+                           {128, 128, 1, 0.57f, 0.42f}, {256, 128, 1, 0.95f, 0.8f}, {256, 256, 1, 1.49f, 1.3f}};
+constexpr int kTileKinds = sizeof(kTiles) / sizeof(kTiles[0]);
+constexpr uint32_t kUnits = 256;  // compute units
+
+uint64_t tiles_of(const Tile &tile, uint64_t t, uint64_t r) {
+    return (t + tile.t - 1) / tile.t * ((r + tile.r - 1) / tile.r);
+}
+
+// How long a product of t x r results takes, its sums of `stages` stages: rounds
+// of the workgroups that the chip holds at once, 3 us for a tile's start and end.
+float time_of(const Tile &tile, uint64_t t, uint64_t r, uint64_t stages) {
+    const uint64_t tiles = tiles_of(tile, t, r), round = kUnits * tile.held;
+    const float rounds = float((tiles + round - 1) / round);
+    return tiles <= kUnits ? float(stages) * tile.alone + 3.0f : rounds * (float(stages) * tile.full + 3.0f);
+}
+
+// The tile with the least time for a product of t x r results, sums of k.  What it
+// decides (logits of 128256 rows, us, tiles of 64 x 128 / 128 x 128 / 256 x 256):
+// 64 tokens 193 / 200 / -, 128 tokens - / 233 / 280, 256 tokens - / 354 / 266, 512
+// tokens 793 / 666 / 504.
+int tile_for(uint64_t t, uint64_t r, uint64_t k) {
+    const uint64_t stages = (k + kDepth - 1) / kDepth;
+    int best = 0;
+    for (int i = 1; i < kTileKinds; i++)
+        if (time_of(kTiles[i], t, r, stages) < time_of(kTiles[best], t, r, stages)) best = i;
+    return best;
+}
+
+// dx's long sums in parts, so that its few tiles fill the chip: the tile, and
+// how many parts.  A part writes and reads n x cols floats more (5 TB/s).  512
+// tokens x 128256 x 4096: 8 parts of 256 x 256 tiles 483 us, 4 parts of 128 x 128
+// 618, one part 1147.
+struct Split {
+    int tile;
+    uint32_t parts;
+};
+Split dx_split(uint64_t n, uint64_t cols, uint64_t rows) {
+    const uint64_t stages = std::max<uint64_t>((rows + kDepth - 1) / kDepth, 1);
+    Split best{0, 1};
+    float least = 0;
+    for (int i = 0; i < kTileKinds; i++) {
+        const uint64_t tiles = std::max<uint64_t>(tiles_of(kTiles[i], n, cols), 1);
+        const uint64_t most = std::min<uint64_t>({kUnits * kTiles[i].held / tiles, stages / 8, 64});
+        const uint64_t parts = std::max<uint64_t>(most, 1);
+        const float time = time_of(kTiles[i], n, cols * parts, (stages + parts - 1) / parts) +
+                           float(parts * n * cols) * (8 / 5e6f);
+        if (i && time >= least) continue;
+        least = time;
+        best = {i, uint32_t(parts)};
+    }
+    return best;
+}
 
 template <class Y, class S, int KIND>
 int run_tiles(int tile, const TileArgs &a, uint64_t t_most, hipStream_t st) {
-    const uint64_t all = up(t_most, kTiles[tile].t) / kTiles[tile].t *
-                         (up(a.r_size, kTiles[tile].r) / kTiles[tile].r) * a.splits;
+    const uint64_t all = tiles_of(kTiles[tile], t_most, a.r_size) * a.splits;
     if (!all) return DF11_OK;
     const uint64_t groups = up(all, 8);
-    if (groups >> 23) return DF11_E_INVALID;  // a grid holds less than 2^32 threads
+    if (groups >> 22) return DF11_E_INVALID;  // a grid holds less than 2^32 threads
     const dim3 grid = dim3(uint32_t(groups));
     switch (tile) {
     case 0: return status(launch(tiles<Y, S, KIND, 32, 64, 1, 2, 6>, grid, dim3(128), 0, st, a));
     case 1: return status(launch(tiles<Y, S, KIND, 64, 64, 2, 2, 4>, grid, dim3(256), 0, st, a));
-    case 2: return status(launch(tiles<Y, S, KIND, 128, 128, 4, 2, 4>, grid, dim3(512), 0, st, a));
+    case 2: return status(launch(tiles<Y, S, KIND, 64, 128, 1, 4, 3>, grid, dim3(256), 0, st, a));
+    case 3: return status(launch(tiles<Y, S, KIND, 128, 128, 4, 2, 4>, grid, dim3(512), 0, st, a));
+    case 4: return status(launch(tiles<Y, S, KIND, 256, 128, 4, 2, 3>, grid, dim3(512), 0, st, a));
     default: return status(launch(tiles<Y, S, KIND, 256, 256, 2, 4, 2>, grid, dim3(512), 0, st, a));
     }
-}
-
-// The tile for a product of t x r results.
-int tile_for(uint64_t t, uint64_t r) {
-    if (t <= 32) return 0;
-    if (t <= 64) return 1;
-    return t <= 128 || t * r < 256ull * 256 * 256 ? 2 : 3;
 }
 
 bool bad_piece(const df11_vocab_piece *p) {
@@ -705,11 +774,11 @@ struct LossScratch {
     float2 *state, *part;
     float *told;
     uint64_t bytes;
-    LossScratch(void *p, uint64_t n, uint64_t rows) {
+    LossScratch(void *p, uint64_t n, uint64_t rows, uint64_t cols) {
         Scratch s{static_cast<char *>(p)};
         state = s.take<float2>(n);
         told = s.take<float>(n);
-        const uint32_t r = kTiles[tile_for(n, rows)].r;
+        const uint32_t r = kTiles[tile_for(n, rows, cols)].r;
         part = s.take<float2>(up(n, 16) * ((rows + r - 1) / r));
         bytes = s.at;
     }
@@ -720,16 +789,9 @@ uint64_t chunk_rows(uint64_t n, uint64_t rows) {
     return std::min(up(rows, 256), std::max<uint64_t>((1ull << 27) / std::max<uint64_t>(n, 1) / 256 * 256, 256));
 }
 
-// Parts of dx's long sum: enough workgroups for the chip.
-uint32_t dx_splits(uint64_t n, uint64_t cols, uint64_t rows) {
-    const Tile t = kTiles[tile_for(n, cols)];
-    const uint64_t tiles = (n + t.t - 1) / t.t * ((cols + t.r - 1) / t.r);
-    const uint64_t stages = (rows + kDepth - 1) / kDepth;
-    return uint32_t(std::max<uint64_t>(1, std::min<uint64_t>({512 / std::max<uint64_t>(tiles, 1), stages / 8, 32})));
-}
-
 struct GradScratch {
-    uint32_t *count, *order, *place, *target_of, splits;
+    uint32_t *count, *order, *place, *target_of;
+    Split dx;
     float *lse_of, *sums;
     float2 *factor;
     __bf16 *x, *g;
@@ -744,8 +806,8 @@ struct GradScratch {
         x_stride = up(z.cols, 64);
         x = s.take<__bf16>(n * x_stride);
         chunk = chunk_rows(n, z.rows);
-        splits = dx_splits(n, z.cols, chunk);
-        sums = s.take<float>(z.dx ? splits * n * z.cols : 0);
+        dx = dx_split(n, z.cols, chunk);
+        sums = s.take<float>(z.dx ? dx.parts * n * z.cols : 0);
         g = s.take<__bf16>(n * chunk * (z.two_terms ? 2 : 1));
         bytes = s.at;
     }
@@ -768,19 +830,19 @@ TileArgs tile_args() {
 extern "C" {
 
 uint64_t df11_vocab_loss_scratch_bytes(const df11_vocab_sizes *z) {
-    return bad_sizes(z) ? 0 : LossScratch(nullptr, z->n, z->rows).bytes;
+    return bad_sizes(z) ? 0 : LossScratch(nullptr, z->n, z->rows, z->cols).bytes;
 }
 
 int df11_vocab_loss(const df11_vocab_piece *p, float *losses, float *lse, void *scratch,
                     uint64_t scratch_bytes, df11_hip_stream stream) {
     if (bad_piece(p) || !p->vocab) return DF11_E_INVALID;
     if (!p->n) return DF11_OK;
-    const LossScratch s(scratch, p->n, p->rows);
+    const LossScratch s(scratch, p->n, p->rows, p->cols);
     if (!scratch || !aligned(scratch, 256) || scratch_bytes < s.bytes ||
         (p->end && (!losses || !lse || !aligned(losses, 4) || !aligned(lse, 4))))
         return DF11_E_INVALID;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const int tile = tile_for(p->n, p->rows);
+    const int tile = tile_for(p->n, p->rows, p->cols);
     TileArgs a = tile_args();
     a.a = static_cast<const __bf16 *>(p->x), a.b = static_cast<const __bf16 *>(p->w);
     a.a_stride = p->x_stride, a.b_stride = p->w_stride;
@@ -857,7 +919,7 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
         a.lse = s.lse_of, a.factor = s.factor, a.target_of = s.target_of;
         a.g = s.g, a.g_stride = g_stride, a.g_half = p->n * g_stride, a.r_padded = uint32_t(g_stride);
         a.halves = terms;
-        rc = run_tiles<__bf16, __bf16, GRAD>(tile_for(p->n, here), a, p->n, st);
+        rc = run_tiles<__bf16, __bf16, GRAD>(tile_for(p->n, here, p->cols), a, p->n, st);
         if (rc != DF11_OK) return rc;
         if (has_dx && p->n) {
             a = tile_args();
@@ -865,11 +927,11 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
             a.b = w, a.b_stride = p->w_stride;
             a.count = s.count;
             a.r_size = p->cols, a.k_size = here;
-            a.splits = s.splits;
-            a.split_stages = uint32_t((g_stride / kDepth + s.splits - 1) / s.splits);
+            a.splits = s.dx.parts;
+            a.split_stages = uint32_t((g_stride / kDepth + s.dx.parts - 1) / s.dx.parts);
             a.y = s.sums, a.y_stride = p->cols, a.y_split = uint64_t(p->n) * p->cols;
             a.add = !(p->begin && c == 0);
-            rc = run_tiles<float, float, DX>(tile_for(p->n, p->cols), a, p->n, st);
+            rc = run_tiles<float, float, DX>(s.dx.tile, a, p->n, st);
             if (rc != DF11_OK) return rc;
         }
         if (has_dw && here) {
@@ -879,7 +941,10 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
             a.count = s.count;
             a.t_size = here, a.r_size = p->cols;
             a.y_stride = g->dw_stride, a.add = g->accumulate;
-            const int tile = tile_for(here, p->cols);
+            // a gradient that the caches do not hold passes them by, which leaves x and g
+            // there (512 tokens, 128256 x 4096: 580 us, 629 through them)
+            a.past = uint64_t(p->rows) * p->cols * type_bytes(g->dw_type) >= 1ull << 27;
+            const int tile = tile_for(here, p->cols, uint64_t(p->n) * dw_terms);
             if (g->dw_type == DF11_TYPE_F32) {
                 a.y = static_cast<float *>(g->dw) + c * g->dw_stride;
                 rc = run_tiles<float, float, DW>(tile, a, here, st);
@@ -892,7 +957,7 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
         }
     }
     if (!has_dx || !p->end || !p->n) return DF11_OK;
-    t.sums = s.sums, t.sums_split = uint64_t(p->n) * p->cols, t.splits = s.splits;
+    t.sums = s.sums, t.sums_split = uint64_t(p->n) * p->cols, t.splits = s.dx.parts;
     t.dx = g->dx, t.dx_stride = g->dx_stride;
     return status(g->dx_type == DF11_TYPE_F32 ? launch(spread<float>, rows, dim3(256), 0, st, t)
                                               : launch(spread<__bf16>, rows, dim3(256), 0, st, t));

@@ -6,7 +6,9 @@ Bounds, with u = 2^-24 and K columns (everything to first order):
 * an exponential exp(d) has an argument off by 2 |d| u and its own rounding of
   2 u, and the sum of all of them, in parts of at most 300 terms one behind
   another, rounds 600 times at most; the mean of |d| under the probabilities is
-  at most log V, so lse is off by e = K u S + (4 log V + 700) u + 4 u |lse|;
+  at most log V, so lse is off by e = K u S + (4 log V + 700) u + 4 u |lse|, and
+  the others' lse less the target's logit, d, by twice K u S and the same
+  otherwise; the loss log(1 + exp d) by (1 - p) of that and its own roundings;
 * a probability is off by the factor 2 e + 4 u (|l - lse| + 2), an entry of g by
   that times it, and by 2 u |g|, and by its rounding: 2^-8 of it, or with two
   terms (that of 2^-8 of what the first left) 2^-16;
@@ -73,7 +75,15 @@ class Exact:
         size = (self.x.abs() @ self.w.abs().t()).amax(1)
         self.off_logit = cols * U * size
         self.off_lse = self.off_logit + (4 * math.log(rows + 1) + 700) * U + 4 * U * self.lse.abs()
-        self.off_loss = self.off_lse + self.off_logit + 2 * U * (self.lse.abs() + self.loss.abs())
+        # the loss is log(1 + exp d), d what the others' lse is above the target's
+        # logit; it changes with d by 1 - p
+        told = self.logits.gather(1, self.at[:, None])
+        rest = self.logits.scatter(1, self.at[:, None], -math.inf)
+        d = torch.logsumexp(rest, 1) - told[:, 0]
+        off_d = 2 * self.off_logit + (4 * math.log(rows + 1) + 700) * U + 4 * U * (rest.amax(1) - told[:, 0]).abs()
+        off_d = torch.where(d == -math.inf, 0.0, off_d)
+        self.loss = torch.where(self.counted, torch.logaddexp(d, torch.zeros_like(d)), 0.0)
+        self.off_loss = torch.sigmoid(d) * off_d * (1 + off_d) + 8 * U * self.loss
 
     def gradient(self, loss_grad, lse_grad, terms):
         """g and how far it may be off."""
@@ -227,12 +237,16 @@ def test_targets_outside():
     want, same_lse = head(x, good)
     bad = torch.zeros(40, dtype=torch.bool, device="cuda")
     bad[[0, 7, 39]] = True
-    assert losses[bad].isnan().all() and torch.equal(losses[~bad], want[~bad]) and torch.equal(lse, same_lse)
+    assert losses[bad].isnan().all() and torch.equal(losses[~bad], want[~bad])
+    e = Exact(x, w, good)
+    assert torch.equal(lse[~bad], same_lse[~bad])
+    check(lse, e.lse, e.off_lse, "lse")
     dx, dws = head.gradient(x, targets, lse)
     dx_want, _ = head.gradient(x, good, lse)
     assert dx[bad].isnan().all() and torch.equal(dx[~bad], dx_want[~bad])
     assert all(t.isnan().all() for t in dws)
-    losses, _ = head(x, good, ignore_index=int(good[5]))
+    losses, lse = head(x, good, ignore_index=int(good[5]))
+    assert torch.equal(lse, same_lse)
     assert (losses[good == good[5]] == 0).all() and torch.equal(losses[good != good[5]], want[good != good[5]])
     far = torch.full((40,), -2 ** 62, device="cuda")
     assert not head(x, far, ignore_index=-2 ** 62)[0].any()
@@ -297,6 +311,30 @@ def test_infinite_and_extreme_logits():
     ones = torch.ones(1, cols, dtype=BF16, device="cuda")
     losses, lse = ed.VocabLoss([all_low])(ones, targets[:1] * 0)
     assert lse.item() == -float("inf") and losses.isnan().all()
+    all_low[1:] = 1.0  # the target alone at -infinity, then the target at +infinity
+    losses, lse = ed.VocabLoss([all_low])(ones, targets[:1] * 0)
+    assert losses.item() == float("inf") and abs(lse.item() - 64 - math.log(2)) < 1e-4
+    losses, lse = ed.VocabLoss([-all_low])(ones, targets[:1] * 0)
+    assert losses.isnan().all() and lse.isnan().all()
+    only = torch.ones(1, cols, dtype=BF16, device="cuda")
+    losses, lse = ed.VocabLoss([only])(ones, targets[:1] * 0)
+    assert losses.item() == 0 and lse.item() == 64
+
+
+def test_certain_targets():
+    """Losses down to 1e-24 keep their digits: differences of logarithms would not."""
+    say("[gpu] nearly certain targets")
+    rows, cols = 500, 64
+    w = (randn(rows, cols) / 8).to(BF16)
+    targets = torch.arange(60, device="cuda")
+    x = (w[:60].float() * torch.linspace(1, 80, 60, device="cuda")[:, None]).to(BF16)
+    losses, lse = ed.VocabLoss([w])(x, targets)
+    e = Exact(x, w, targets)
+    # of the inputs, in float64; the bound's largest part is 2 K u S, where S is up
+    # to 80 |w|^2 = 80: 6e-4
+    assert e.loss.min() < 1e-24 and (e.off_loss < 1e-3 * e.loss).all()
+    check(losses, e.loss, e.off_loss, "loss")
+    check(lse, e.lse, e.off_lse, "lse")
 
 
 def test_shapes_and_strides():
