@@ -382,7 +382,7 @@ def _load():
                                    ctypes.POINTER(df11_int8_tensor), ctypes.c_uint32,
                                    ctypes.c_uint32, vp, ctypes.c_uint64, vp]
     L.df11_embedding.argtypes = [ctypes.POINTER(df11_embedding_lookup), vp]
-    L.df11_embedding_gradient_scratch_bytes.argtypes = [ctypes.c_uint64, ctypes.c_uint32]
+    L.df11_embedding_gradient_scratch_bytes.argtypes = [ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint32]
     L.df11_embedding_gradient_scratch_bytes.restype = ctypes.c_uint64
     L.df11_embedding_gradient.argtypes = [ctypes.POINTER(df11_embedding_grad), vp, ctypes.c_uint64, vp]
     vs = ctypes.POINTER(df11_vocab_sizes)
@@ -1512,15 +1512,18 @@ def _output(t, what, shape, dtype, device):
 
 
 def _token_bits(tokens, device) -> int:
-    bits = _TOKEN_BITS.get(str(tokens.dtype))
+    bits = _TOKEN_BITS.get(tokens.dtype)
     if bits is None:
-        raise TypeError("tokens must be int32 or int64")
+        bits = {"torch.int32": 32, "torch.int64": 64}.get(str(tokens.dtype))
+        if bits is None:
+            raise TypeError("tokens must be int32 or int64")
+        _TOKEN_BITS[tokens.dtype] = bits
     if tokens.device != device:
         raise ValueError(f"tokens must be on {device}")
     return bits
 
 
-_TOKEN_BITS = {"torch.int32": 32, "torch.int64": 64}
+_TOKEN_BITS = {}  # by torch's types, filled when first seen
 
 
 class Embedding(_Lender):
@@ -1559,7 +1562,7 @@ class Embedding(_Lender):
             if out is None:
                 out, a.out_stride = torch.empty(*tokens.shape, a.cols, dtype=out_dtype, device=self.device), a.cols
             a.tokens, a.out = tokens.data_ptr(), out.data_ptr()
-            _check("df11_embedding", LIB.df11_embedding(ctypes.byref(a), st))
+            _check("df11_embedding", LIB.df11_embedding(a, st))
         if st not in self._lent:
             self._lend(stream, st)
         if stream is not None:
@@ -1607,11 +1610,11 @@ def embedding_gradient(tokens, dy, rows: int, dtype=None, out=None, accumulate: 
         if made:
             out, g.dw_stride = torch.empty(rows, g.cols, dtype=dtype or dy.dtype, device=device), g.cols
         g.dw_type = _type(out.dtype)
-        need = int(LIB.df11_embedding_gradient_scratch_bytes(g.n, g.cols))
-        scratch = torch.empty(need, dtype=torch.uint8, device=device)
+        need = LIB.df11_embedding_gradient_scratch_bytes(g.n, rows, g.cols)
+        scratch = torch.empty(need, dtype=torch.uint8, device=device) if need else None
         g.tokens, g.dy, g.dw = tokens.data_ptr(), dy.data_ptr(), out.data_ptr()
         _check("df11_embedding_gradient",
-               LIB.df11_embedding_gradient(ctypes.byref(g), scratch.data_ptr(), need, st))
+               LIB.df11_embedding_gradient(g, scratch.data_ptr() if need else None, need, st))
     if not made:
         torch._C._increment_version([out])
     if stream is not None:
@@ -1665,11 +1668,17 @@ class VocabLoss(_Lender):
             raise ValueError("pieces must have equal columns")
         self._first = np.cumsum([0] + [r for r, _ in shapes]).tolist()
         self._rows = max(r for r, _ in shapes)
+        self._p = df11_vocab_piece(cols=self.cols, vocab=self.vocab, rows=self._rows, begin=1, end=1)
+        self._bytes = {}  # scratch for a number of tokens
 
     def _each(self, p, status, st):
         """Sets p to each piece in turn, decompressed where it has to be."""
         import torch
 
+        if len(self.shapes) == 1 and self.pieces is not None:  # p is this one already
+            p.w, p.w_stride = self._held[0]
+            yield 0
+            return
         slot = None
         if self.pieces is None:
             slot = torch.empty(self._rows * self.cols, dtype=torch.bfloat16, device=self.device)
@@ -1696,9 +1705,10 @@ class VocabLoss(_Lender):
         stride = _rows_apart(x, "hidden states", self.device)
         if x.shape != (targets.numel(), self.cols):
             raise ValueError("hidden states must be [number of targets, cols]")
-        return x, df11_vocab_piece(x=x.data_ptr(), x_stride=stride, n=x.size(0), cols=self.cols,
-                                   vocab=self.vocab, ignored=ignore_index,
-                                   target_bits=_token_bits(targets, self.device))
+        p = df11_vocab_piece.from_buffer_copy(self._p)
+        p.x, p.x_stride, p.n, p.ignored = x.data_ptr(), stride, x.size(0), ignore_index
+        p.target_bits = _token_bits(targets, self.device)
+        return x, p
 
     def __call__(self, x, targets, ignore_index: int = -100, status=None, stream=None):
         """(losses, lse), float32 like ``targets`` (int32 or int64): the cross entropy
@@ -1719,12 +1729,16 @@ class VocabLoss(_Lender):
             p.targets = targets.data_ptr()
             losses = torch.empty(targets.shape, dtype=torch.float32, device=self.device)
             lse = torch.empty_like(losses)
-            need = int(LIB.df11_vocab_loss_scratch_bytes(df11_vocab_sizes(p.n, p.cols, self._rows, 0, 0)))
+            need = self._bytes.get(p.n)
+            if need is None:
+                need = self._bytes[p.n] = LIB.df11_vocab_loss_scratch_bytes(
+                    df11_vocab_sizes(p.n, p.cols, self._rows, 0, 0))
             scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
             for _ in self._each(p, status, st):
                 _check("df11_vocab_loss",
                        LIB.df11_vocab_loss(p, losses.data_ptr(), lse.data_ptr(), scratch.data_ptr(), need, st))
-        self._used(stream, st, [x, given, losses, lse] + ([] if status is None else [status]))
+        if stream is not None or st not in self._lent:
+            self._used(stream, st, [x, given, losses, lse] + ([] if status is None else [status]))
         return losses, lse
 
     def _used(self, stream, st, tensors):
@@ -1792,7 +1806,7 @@ class VocabLoss(_Lender):
                     dws = [torch.empty(shape, dtype=kinds["dw"], device=self.device) for shape in self.shapes]
                 g.dw_type = _type(kinds["dw"])
             sizes = df11_vocab_sizes(n, cols, self._rows, needs_dx, torch.float32 in kinds.values())
-            need = int(LIB.df11_vocab_loss_gradient_scratch_bytes(sizes))
+            need = LIB.df11_vocab_loss_gradient_scratch_bytes(sizes)
             scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
             for k in self._each(p, status, st):
                 if needs_dw:

@@ -802,18 +802,18 @@ int df11_embedding(const df11_embedding_lookup *e, df11_hip_stream st);
  * df11_embedding_gradient: what the table of such a lookup receives,
  *   dw[v][c] = scale * sum over the i with tokens[i] = v of dy[i][c]
  * or, with accumulate, dw[v][c] + that (as where microbatches add up, or an
- * output head shares the table's memory).  Sums are float32: chunks of 16 to
- * 128 tokens of a row (a number that depends on n alone), each in the order of
- * their positions, then the chunks in order; scaled, added and rounded once to
- * dw_type.  No atomics on floats: the same inputs give the same bits.  Rows
+ * output head shares the table's memory).  Sums are float32, of a row's tokens
+ * in the order of their positions, or of up to 8 or chunks of 32 or 128 of them
+ * and then of those sums in order (as n, rows and cols have it, and the tokens'
+ * places among the sorted); scaled, added and rounded once to dw_type.  No atomics on floats: the same inputs give the same bits.  Rows
  * without a token are set to zeros; with accumulate they are neither read nor
  * written.  Tokens equal to padding (-1: none) and tokens outside
  * 0 .. rows - 1 add nothing.  Alignment and strides as df11_embedding's; dw
  * must not overlap anything; dy's rows may be one and the same (stride 0).
  * scratch: device, 128-byte aligned, at least
- * df11_embedding_gradient_scratch_bytes(n, cols) bytes, not shared by calls
- * that may overlap; no initialisation needed.  Three launches on st (two for
- * up to 16 tokens), asynchronous.  Errors as df11_embedding's, and
+ * df11_embedding_gradient_scratch_bytes(n, rows, cols) bytes, not shared by calls
+ * that may overlap; no initialisation needed.  Three launches on st; up to 2048
+ * tokens take one, and no scratch (0 bytes; it may be null then).  Asynchronous.  Errors as df11_embedding's, and
  * DF11_E_INVALID for accumulate and the scratch.
  */
 typedef struct df11_embedding_grad {
@@ -833,7 +833,7 @@ typedef struct df11_embedding_grad {
     float scale;
 } df11_embedding_grad;
 
-uint64_t df11_embedding_gradient_scratch_bytes(uint64_t n, uint32_t cols);
+uint64_t df11_embedding_gradient_scratch_bytes(uint64_t n, uint64_t rows, uint32_t cols);
 int df11_embedding_gradient(const df11_embedding_grad *g, void *scratch, uint64_t scratch_bytes,
                             df11_hip_stream st);
 

@@ -27,7 +27,7 @@ def gradient(scratch=1 << 20, nbytes=None, **change):
              dy_type=1, dw_type=0, token_bits=64, accumulate=0, scale=1.0)
     a.update(change)
     if nbytes is None:
-        nbytes = L.df11_embedding_gradient_scratch_bytes(a["n"], a["cols"])
+        nbytes = L.df11_embedding_gradient_scratch_bytes(a["n"], a["rows"], a["cols"])
     return L.df11_embedding_gradient(ctypes.byref(ed.df11_embedding_grad(**a)), scratch, nbytes, None)
 
 
@@ -52,7 +52,7 @@ def test_lookup_of_nothing():
     {"dw_stride": BIG}, {"dy_stride": BIG}, {"dy_type": 3}, {"dw_type": 3}, {"token_bits": 8},
     {"accumulate": 2}, {"rows": (1 << 24) + 1}, {"n": (1 << 24) + 1, "nbytes": 1 << 40},
     {"cols": (1 << 20) + 1, "dw_stride": 1 << 21, "nbytes": 1 << 40},
-    {"scratch": 0}, {"scratch": (1 << 20) + 64}, {"nbytes": 100}])
+    {"n": 3000, "scratch": 0}, {"n": 3000, "scratch": (1 << 20) + 64}, {"n": 3000, "nbytes": 100}])
 def test_gradient_refuses(change):
     assert gradient(**change) == ed.DF11_E_INVALID
 
@@ -66,8 +66,10 @@ def test_gradient_of_nothing():
 
 def test_scratch_bytes():
     f = L.df11_embedding_gradient_scratch_bytes
-    assert f((1 << 24) + 1, 8) == 0 and f(8, (1 << 20) + 1) == 0
-    assert 0 < f(0, 8) <= f(1, 8) < f(100_000, 8) < f(100_000, 80)
+    assert f((1 << 24) + 1, 8, 8) == f(3000, (1 << 24) + 1, 8) == f(3000, 8, (1 << 20) + 1) == 0
+    assert f(2048, 128_256, 4096) == 0 < f(2049, 128_256, 4096)
+    assert f(3000, 8, 8) < f(100_000, 8, 8) < f(100_000, 1 << 20, 8) < f(100_000, 1 << 20, 80)
+    assert f(8, 1 << 24, 1 << 20) > 0  # more workgroups than a grid holds: three launches
 
 
 def test_struct_layouts(tmp_path):

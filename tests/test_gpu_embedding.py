@@ -139,7 +139,8 @@ def check_gradient(got, tokens, dy, rows, scale=1.0, padding=None, before=None):
 @pytest.mark.parametrize("kind", [F32, BF16, F16])
 @pytest.mark.parametrize("out", [F32, BF16, F16])
 @pytest.mark.parametrize("n,rows,cols", [(1, 1, 1), (2, 3, 8), (16, 5, 40), (17, 5, 520), (300, 999, 513),
-                                         (1000, 7, 24), (4100, 2500, 40)])
+                                         (1000, 7, 24), (2048, 1, 8), (2048, 700, 1030), (2049, 700, 1030),
+                                         (4100, 2500, 40)])
 def test_gradient(kind, out, n, rows, cols):
     say(f"[gpu] gradient {n} of {rows} x {cols}, {kind} to {out}")
     tokens = some_tokens(n, rows, n, torch.int64 if n % 2 else torch.int32)
@@ -150,7 +151,7 @@ def test_gradient(kind, out, n, rows, cols):
     assert torch.equal(got, ed.embedding_gradient(tokens, dy, rows, out, scale=0.37))
 
 
-@pytest.mark.parametrize("n", [1, 15, 16, 31, 32, 33, 48, 1024, 5000, 70_000])
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 48, 1024, 2047, 2048, 2049, 5000, 70_000])
 @pytest.mark.parametrize("rows", [1, 5, 600_000])
 def test_gradient_of_one_row(n, rows):
     """All tokens the same: a run over all chunks."""
@@ -161,10 +162,11 @@ def test_gradient_of_one_row(n, rows):
 
 
 def test_gradient_of_runs_that_end_with_chunks():
-    """Runs of 1 to 64 tokens, each length at every offset of a chunk of 16."""
+    """Runs of 1 to 128 tokens, each length at every offset of a chunk of 32."""
     say("[gpu] gradient of runs at chunk borders")
-    for first in range(1, 17):
-        lengths = [first] + [k for k in (16, 32, 1, 15, 17, 31, 33, 48, 64, 16, 16, 2) for _ in "ab"]
+    for first in range(1, 33):
+        lengths = [first] + [k for k in (16, 32, 1, 31, 33, 63, 64, 65, 128, 32, 32, 2) for _ in "abcde"]
+        assert sum(lengths) > 2048
         tokens = torch.repeat_interleave(torch.arange(len(lengths), device="cuda"),
                                          torch.tensor(lengths, device="cuda"))
         tokens = tokens[torch.randperm(len(tokens), generator=gen(first), device="cuda")]
@@ -173,10 +175,11 @@ def test_gradient_of_runs_that_end_with_chunks():
 
 
 @pytest.mark.parametrize("out", [F32, BF16])
-def test_gradient_added(out):
+@pytest.mark.parametrize("n", [200, 2000, 3000])
+def test_gradient_added(n, out):
     """Added to what is there; rows without a token are not touched, not even NaN."""
-    say(f"[gpu] gradient added, {out}")
-    n, rows, cols, padding = 2000, 700, 136, 35
+    say(f"[gpu] gradient added, {n} tokens, {out}")
+    rows, cols, padding = 700, 136, 35
     tokens, dy = some_tokens(n, rows, 9), randn(n, cols, seed=2)
     tokens[::7] = padding
     tokens[3::50], tokens[4::50] = -100, rows
