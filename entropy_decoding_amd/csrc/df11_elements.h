@@ -29,24 +29,31 @@ __device__ __forceinline__ f32x8 widen(typename Group<T>::type v) {
     return r;
 }
 
-// Columns c .. c + 7 of a row of `cols`; columns past the end are 0.
-template <class T>
+// Columns c .. c + 7 of a row of `cols`; columns past the end are 0.  ONCE: what is
+// read once passes the caches by.
+template <class T, bool ONCE = false>
 __device__ __forceinline__ typename Group<T>::type load_group(const T *row, uint32_t c, uint32_t cols) {
-    if (c + 8 <= cols) return *reinterpret_cast<const typename Group<T>::any *>(row + c);
+    typedef typename Group<T>::any any;
+    if (c + 8 <= cols)
+        return ONCE ? __builtin_nontemporal_load(reinterpret_cast<const any *>(row + c))
+                    : *reinterpret_cast<const any *>(row + c);
     typename Group<T>::type v;
 #pragma unroll
     for (uint32_t e = 0; e < 8; e++) v[e] = c + e < cols ? row[c + e] : T(0.0f);
     return v;
 }
 
-// The group rounded to T (to nearest, ties to even) into columns c .. c + 7.
-template <class T>
+// The group rounded to T (to nearest, ties to even) into columns c .. c + 7; PAST the
+// caches, or not.
+template <class T, bool PAST = false>
 __device__ __forceinline__ void store_group(T *row, uint32_t c, uint32_t cols, f32x8 x) {
-    typename Group<T>::type v;
+    typedef typename Group<T>::any any;
+    any v;
 #pragma unroll
     for (int e = 0; e < 8; e++) v[e] = T(x[e]);
     if (c + 8 <= cols) {
-        *reinterpret_cast<typename Group<T>::any *>(row + c) = v;
+        if (PAST) __builtin_nontemporal_store(v, reinterpret_cast<any *>(row + c));
+        else *reinterpret_cast<any *>(row + c) = v;
     } else {
 #pragma unroll
         for (uint32_t e = 0; e < 7; e++)

@@ -79,13 +79,14 @@ __global__ __launch_bounds__(256) void lookup(LookupArgs a) {
 
 // ---------------------------------------------------------------- gradient
 
-// What the launches hand on: positions of the kept tokens sorted by row, the
-// sorted rows, where each one's run ends (by sorted token, and by row of the
-// table: 0 where there is none), and sums of runs that cross chunks.
+// What the launches hand on: the kept tokens sorted by row (each one's position,
+// row, and where the run of its row begins and ends), the ends by row of the
+// table (0 where there is no token), and sums of runs in chunks.
 struct GradArgs {
     const void *tokens, *dy;
     void *dw;
-    uint32_t *kept, *order, *row, *end, *total;
+    uint32_t *kept, *total;
+    uint4 *sorted;
     float *part;
     uint64_t dy_stride, dw_stride, part_stride;
     int64_t padding;
@@ -94,6 +95,21 @@ struct GradArgs {
     float scale;
 };
 
+// Calls f(r, which lanes have it, the first of them) for every r of the lanes that
+// are `in`.  For counting, LDS atomics are the faster way as long as few lanes can
+// have the same r (32768 tokens: 35 against 41 us for the sort), but those on one
+// address take their turns (32768 equal tokens: 48 against 31 us).
+template <class F>
+__device__ __forceinline__ void match(uint32_t r, bool in, F f) {
+    for (uint64_t left = __ballot(in); left;) {
+        const uint32_t first = __builtin_ctzll(left);
+        const uint32_t r0 = __builtin_amdgcn_readlane(r, first);
+        const uint64_t same = __ballot(in && r == r0);
+        f(r0, same, first);
+        left &= ~same;
+    }
+}
+
 constexpr uint32_t kSortWaves = 16;
 
 // Sorts the tokens by row, stably, in one launch without a word between its
@@ -101,13 +117,12 @@ constexpr uint32_t kSortWaves = 16;
 // keeps those of its rows.  The first reading counts them by wave and row, and
 // all tokens of earlier rows, which says where its rows begin; the second puts
 // each at its place.  A wave reads `span` consecutive tokens, in order, so
-// places within a row ascend with the position.  What bounds it is the reading
-// of all tokens by all workgroups, and its latency; up to 32768 tokens are held in
-// registers in between (TIME_SORT us of them, 34 us reading twice).
+// places within a row ascend with the position.  TIME_SORT us
+// for 8192 and TIME_SORT2 us for 32768 tokens of 128256 rows.
 template <class I>
 __global__ __launch_bounds__(64 * kSortWaves) void sort_tokens(GradArgs a) {
     extern __shared__ uint32_t shared[];
-    uint32_t *count = shared, *total = shared + kSortWaves * a.run;  // [wave][row], [row]
+    uint32_t *count = shared, *before = shared + kSortWaves * a.run;  // [wave][row], [row]
     __shared__ uint32_t sums[kSortWaves];
     const uint32_t lane = threadIdx.x & 63u, wave = uniform(threadIdx.x >> 6);
     const uint32_t base = blockIdx.x * a.run;
@@ -116,31 +131,48 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_tokens(GradArgs a) {
 
     const uint32_t from = min(a.n, wave * a.span), to = min(a.n, from + a.span);
     const I *tokens = static_cast<const I *>(a.tokens);
-    constexpr uint32_t kLoads = 32;
-    // the row of each of a wave's next tokens, 2^32 - 1 for those that are not kept
-    const auto read = [&](uint32_t p, uint32_t (&row)[kLoads]) {
-        I t[kLoads];
+    // Calls f(position, row less base, whether the row is the workgroup's, whether it
+    // is an earlier one) for a wave's tokens, 64 at a time, in order.  The next
+    // tokens are on their way meanwhile.  All workgroups visit all tokens, so the
+    // instructions of a visit are what the sort takes (64-bit comparisons and a row
+    // for every token: 32 us for 32768 tokens).
+    constexpr uint32_t kLoads = 8;
+    const uint32_t mine_rows = min(a.run, a.rows - base);
+    const bool padded = uint64_t(a.padding) <= 0xFFFFFFFFu;
+    const auto each = [&](auto f) {
+        I now[kLoads], next[kLoads];
+        const auto fetch = [&](uint32_t p, I (&t)[kLoads]) {
 #pragma unroll
-        for (uint32_t u = 0; u < kLoads; u++) {
-            const uint32_t i = p + 64 * u + lane;
-            t[u] = i < to ? tokens[i] : I(-1);
+            for (uint32_t u = 0; u < kLoads; u++) t[u] = tokens[min(p + 64 * u + lane, a.n - 1)];
+        };
+        if (from < to) fetch(from, now);
+#pragma unroll 1
+        for (uint32_t p = from; p < to; p += 64 * kLoads) {
+            if (p + 64 * kLoads < to) fetch(p + 64 * kLoads, next);
+#pragma unroll
+            for (uint32_t u = 0; u < kLoads; u++) {
+                const uint32_t i = p + 64 * u + lane, low = uint32_t(now[u]);
+                bool valid = p + 64 * kLoads <= to || i < to;
+                if constexpr (sizeof(I) == 8) valid = valid && uint64_t(now[u]) >> 32 == 0;
+                if (padded) valid = valid && low != uint32_t(a.padding);
+                f(i, low - base, valid && low - base < mine_rows, valid && low < base);
+                now[u] = next[u];
+            }
         }
-#pragma unroll
-        for (uint32_t u = 0; u < kLoads; u++)
-            row[u] = int64_t(t[u]) == a.padding ? 0xFFFFFFFFu : row_of(t[u], a.rows);
     };
-    uint32_t below = 0, row[kLoads];
-    for (uint32_t p = from; p < to; p += 64 * kLoads) {
-        read(p, row);
-#pragma unroll
-        for (uint32_t u = 0; u < kLoads; u++) {
-            below += uint32_t(row[u] < base);
-            const uint32_t r = row[u] - base;
-            if (row[u] >= base && r < a.run) atomicAdd(&count[wave * a.run + r], 1u);
+    // A wave's counts and places are its own: its LDS operations take effect in order.
+    volatile uint32_t *place = count + wave * a.run;
+    uint32_t below = 0;
+    each([&](uint32_t, uint32_t r, bool in, bool earlier) {
+        below += __popcll(__ballot(earlier));
+        if (__popcll(__ballot(in)) <= 8) {
+            if (in) atomicAdd(&count[wave * a.run + r], 1u);
+        } else {
+            match(r, in, [&](uint32_t r0, uint64_t same, uint32_t first) {
+                if (lane == first) place[r0] = place[r0] + __popcll(same);
+            });
         }
-    }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) below += __shfl_xor(below, d);
+    });
     if (lane == 0) sums[wave] = below;
     __syncthreads();
     uint32_t start = 0;  // of the workgroup's rows
@@ -163,7 +195,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_tokens(GradArgs a) {
     for (uint32_t w = 0; w < wave; w++) upto += sums[w];
     upto += start;
     if (threadIdx.x < a.run) {
-        total[threadIdx.x] = mine ? upto : 0;
+        before[threadIdx.x] = upto;
         if (base + threadIdx.x < a.rows) a.total[base + threadIdx.x] = mine ? upto : 0;
         uint32_t at = upto - mine;
         for (uint32_t w = 0; w < kSortWaves; w++) {
@@ -175,119 +207,134 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_tokens(GradArgs a) {
     }
     __syncthreads();
 
-    // A wave's places are its own: its LDS operations take effect in order.
-    volatile uint32_t *place = count + wave * a.run;
-    for (uint32_t p = from; p < to; p += 64 * kLoads) {
-        if (a.span > 64 * kLoads) read(p, row);  // or they are held from the first reading
-#pragma unroll
-        for (uint32_t u = 0; u < kLoads; u++) {
-            const uint32_t r = row[u] - base;
-            const bool in = row[u] >= base && r < a.run && row[u] != 0xFFFFFFFFu;
-            for (uint64_t left = __ballot(in); left;) {
-                const uint32_t first = __builtin_ctzll(left);
-                const uint32_t r0 = __builtin_amdgcn_readlane(r, first);
-                const uint64_t same = __ballot(in && r == r0);
-                const uint32_t at = place[r0];
-                if (in && r == r0) {
-                    const uint32_t to_place = at + __popcll(same & ((1ull << lane) - 1));
-                    a.order[to_place] = p + 64 * u + lane;
-                    a.row[to_place] = row[u];
-                    a.end[to_place] = total[r0];
-                }
-                if (lane == first) place[r0] = at + __popcll(same);
-                left &= ~same;
-            }
-        }
-    }
+    each([&](uint32_t i, uint32_t r, bool in, bool) {
+        match(r, in, [&](uint32_t r0, uint64_t same, uint32_t first) {
+            const uint32_t at = place[r0];
+            if (in && r == r0)
+                a.sorted[at + __popcll(same & ((1ull << lane) - 1))] =
+                    make_uint4(i, base + r, r0 ? before[r0 - 1] : start, before[r0]);
+            if (lane == first) place[r0] = at + __popcll(same);
+        });
+    });
 }
 
 template <class Y>
-__device__ __forceinline__ void finish(const GradArgs &a, uint32_t row, uint32_t c, f32x8 sum, bool add) {
-    Y *dw = static_cast<Y *>(a.dw) + row * a.dw_stride;
+__device__ __forceinline__ Y *row_of_dw(const GradArgs &a, uint32_t row) {
+    return static_cast<Y *>(a.dw) + row * a.dw_stride;
+}
+
+// Stores a row's sum, added to `old` where ADD.
+template <class Y, bool ADD, bool PAST = false>
+__device__ __forceinline__ void finish(const GradArgs &a, uint32_t row, uint32_t c, f32x8 sum,
+                                       typename Group<Y>::type old) {
     sum = scaled(sum, a.scale);
-    if (add) sum += widen<Y>(load_group<Y>(dw, c, a.cols));
-    store_group<Y>(dw, c, a.cols, sum);
+    if (ADD) sum += widen<Y>(old);
+    store_group<Y, PAST>(row_of_dw<Y>(a, row), c, a.cols, sum);
+}
+
+template <class Y, bool ADD>
+__device__ __forceinline__ void finish(const GradArgs &a, uint32_t row, uint32_t c, f32x8 sum) {
+    typename Group<Y>::type old{};
+    if (ADD) old = load_group<Y>(row_of_dw<Y>(a, row), c, a.cols);
+    finish<Y, ADD>(a, row, c, sum, old);
 }
 
 // Clears the rows without a token among 64 rows, 512 columns of them.
-template <class Y>
+template <class Y, bool PAST>
 __device__ __forceinline__ void clear_rows(const GradArgs &a, uint32_t wave, uint32_t lane) {
     const uint32_t first = wave / a.parts * 64, c = wave % a.parts * 512 + lane * 8;
     const uint32_t row = first + lane;
     for (uint64_t none = __ballot(row < a.rows && a.total[min(row, a.rows - 1)] == 0); none; none &= none - 1)
-        store_group<Y>(static_cast<Y *>(a.dw) + (first + __builtin_ctzll(none)) * a.dw_stride, c, a.cols, f32x8(0.0f));
+        store_group<Y, PAST>(row_of_dw<Y>(a, first + __builtin_ctzll(none)), c, a.cols, f32x8(0.0f));
 }
 
-// Sums the runs of equal rows within chunks of sorted tokens, a wave for a
-// chunk's 512 columns.  A run that crosses into another chunk leaves its sum of
-// this one in the chunk's first (it began before) or second slot.  Without ADD
-// further workgroups clear the rows without a token meanwhile.  Bound by HBM.
-template <class X, class Y, bool ADD>
+// Sums the runs of equal rows, a wave for 512 columns of a chunk of sorted tokens:
+// the runs that begin in it, also where they go on behind it.  A run longer than
+// a chunk is summed by all chunks that it touches; each leaves its sum in the
+// chunk's first (the run began before) or second slot.  Without ADD further
+// workgroups clear the rows without a token meanwhile.  Bound by HBM.
+//
+// BIG: what would fill the caches passes them by.  With ADD that is dy (32768
+// tokens of 8192 columns, added to float32: 285 -> 262 us for the three launches),
+// otherwise dw, which leaves dy there (8192 tokens, 128256 x 4096 in BF16: 241 ->
+// 212 us; with dy read past the caches as well 240).
+template <class X, class Y, bool ADD, bool BIG>
 __global__ __launch_bounds__(256) void sum_runs(GradArgs a) {
+    constexpr bool PAST = BIG && !ADD, ONCE = BIG && ADD;
     const uint32_t lane = threadIdx.x & 63u;
     if (!ADD && blockIdx.x >= a.summing)
-        return clear_rows<Y>(a, uniform((blockIdx.x - a.summing) * 4 + (threadIdx.x >> 6)), lane);
+        return clear_rows<Y, PAST>(a, uniform((blockIdx.x - a.summing) * 4 + (threadIdx.x >> 6)), lane);
     const uint32_t wave = uniform(blockIdx.x * 4 + (threadIdx.x >> 6));
     const uint32_t chunk = wave / a.parts, c = wave % a.parts * 512 + lane * 8;
-    const uint32_t kept = *a.kept, from = chunk * a.chunk;
-    if (from >= kept) return;
-    const uint32_t to = min(kept, from + a.chunk);
+    const uint32_t kept = *a.kept, begin = chunk * a.chunk;
+    if (begin >= kept) return;
+    const uint32_t end = min(kept, begin + a.chunk);
+    const uint4 first = a.sorted[begin], last = a.sorted[end - 1];
+    const uint32_t from = first.z < begin && first.w - first.z <= a.chunk ? first.w : begin;
+    const uint32_t to = last.z >= begin && last.w - last.z <= a.chunk ? last.w : end;
     const X *dy = static_cast<const X *>(a.dy);
-    const bool began_before = from && a.row[from - 1] == a.row[from];
     constexpr uint32_t kLoads = 8;
     f32x8 sum = 0.0f;
-    uint32_t first = from;  // of the run
     for (uint32_t j = from; j < to; j += kLoads) {
         typename Group<X>::type v[kLoads];
+        typename Group<Y>::type old[kLoads];
+        uint4 of[kLoads];
 #pragma unroll
-        for (uint32_t u = 0; u < kLoads; u++)
-            v[u] = load_group<X>(dy + a.order[min(j + u, to - 1)] * a.dy_stride, c, a.cols);
+        for (uint32_t u = 0; u < kLoads; u++) {
+            of[u] = a.sorted[min(j + u, to - 1)];
+            v[u] = load_group<X, ONCE>(dy + of[u].x * a.dy_stride, c, a.cols);
+            // what the sums are added to comes with them
+            if (ADD && j + u + 1 == of[u].w) old[u] = load_group<Y>(row_of_dw<Y>(a, of[u].y), c, a.cols);
+        }
 #pragma unroll
         for (uint32_t u = 0; u < kLoads; u++) {
             if (j + u >= to) break;
             sum += widen<X>(v[u]);
-            const uint32_t end = a.end[j + u];
-            if (j + u + 1 < to && j + u + 1 != end) continue;
+            if (j + u + 1 < to && j + u + 1 != of[u].w) continue;
             // the run's last token here
-            const bool before = first == from && began_before;
-            if (before || end > to) {
-                float *part = a.part + (2 * uint64_t(chunk) + (before ? 0 : 1)) * a.part_stride + c;
+            if (of[u].w - of[u].z > a.chunk) {
+                float *part = a.part + (2 * uint64_t(chunk) + (of[u].z < begin ? 0 : 1)) * a.part_stride + c;
                 if (c < a.cols) *reinterpret_cast<f32x8 *>(part) = sum;
             } else {
-                finish<Y>(a, a.row[j + u], c, sum, ADD);
+                finish<Y, ADD, PAST>(a, of[u].y, c, sum, old[u]);
             }
             sum = 0.0f;
-            first = j + u + 1;
         }
     }
 }
 
-// Joins the sums of a run that begins in this chunk and goes on in others.
+// Joins the sums of a run longer than a chunk, where it begins: a workgroup for 512
+// columns, each of its waves a part of the chunks.
 template <class Y, bool ADD>
 __global__ __launch_bounds__(256) void join_runs(GradArgs a) {
-    const uint32_t wave = uniform(blockIdx.x * 4 + (threadIdx.x >> 6)), lane = threadIdx.x & 63u;
-    const uint32_t chunk = wave / a.parts, c = wave % a.parts * 512 + lane * 8;
-    const uint32_t kept = *a.kept, from = chunk * a.chunk;
-    if (from >= kept || kept - from <= a.chunk) return;
-    const uint32_t last = from + a.chunk - 1, row = a.row[last], end = a.end[last];
-    if (end <= from + a.chunk) return;                                       // ends here
-    if (from && a.row[from] == row && a.row[from - 1] == row) return;  // began before
-    if (c >= a.cols) return;
-    const uint32_t chunks = (end - 1) / a.chunk - chunk;  // behind this one
-    const float *part = a.part + (2 * uint64_t(chunk) + 1) * a.part_stride + c;
-    f32x8 sum = *reinterpret_cast<const f32x8 *>(part);
-    part += a.part_stride;
-    constexpr uint32_t kLoads = 4;
-    for (uint32_t k = 0; k < chunks; k += kLoads) {
+    __shared__ float part_s[3][512];
+    const uint32_t wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63u;
+    const uint32_t chunk = blockIdx.x / a.parts, c = blockIdx.x % a.parts * 512 + lane * 8;
+    const uint32_t kept = *a.kept, begin = chunk * a.chunk;
+    if (begin >= kept) return;
+    const uint4 of = a.sorted[min(kept, begin + a.chunk) - 1];
+    if (of.z < begin || of.w - of.z <= a.chunk) return;
+    // the run's chunks behind this one; slot 1 of this one and slot 0 of those
+    const uint32_t chunks = (of.w - 1) / a.chunk - chunk, from = chunks * wave / 4, to = chunks * (wave + 1) / 4;
+    const float *part = a.part + 2 * uint64_t(chunk + 1) * a.part_stride + min(c, uint32_t(a.part_stride) - 8);
+    constexpr uint32_t kLoads = 8;
+    f32x8 sum = 0.0f;
+    if (wave == 0) sum = *reinterpret_cast<const f32x8 *>(part - a.part_stride);
+    for (uint32_t k = from; k < to; k += kLoads) {
         f32x8 v[kLoads];
 #pragma unroll
         for (uint32_t u = 0; u < kLoads; u++)
-            v[u] = *reinterpret_cast<const f32x8 *>(part + 2 * uint64_t(min(k + u, chunks - 1)) * a.part_stride);
+            v[u] = *reinterpret_cast<const f32x8 *>(part + 2 * uint64_t(min(k + u, to - 1)) * a.part_stride);
 #pragma unroll
         for (uint32_t u = 0; u < kLoads; u++)
-            if (k + u < chunks) sum += v[u];
+            if (k + u < to) sum += v[u];
     }
-    finish<Y>(a, row, c, sum, ADD);
+    if (wave) *reinterpret_cast<f32x8 *>(&part_s[wave - 1][lane * 8]) = sum;
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (uint32_t w = 0; w < 3; w++) sum += *reinterpret_cast<const f32x8 *>(&part_s[w][lane * 8]);
+    finish<Y, ADD>(a, of.y, c, sum);
 }
 
 // Few tokens: all of it in one launch.  A workgroup owns `run` neighbouring rows
@@ -335,9 +382,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void sum_few(GradArgs a) {
         row[u] = row[u] - base < a.run && row[u] >= base ? row[u] - base : 0xFFFFFFFFu;
     }
     __syncthreads();
+    volatile uint32_t *place = count[wave];
 #pragma unroll
     for (uint32_t u = 0; u < kFewEach; u++)
-        if (row[u] != 0xFFFFFFFFu) atomicAdd(&count[wave][row[u]], 1u);
+        match(row[u], row[u] != 0xFFFFFFFFu, [&](uint32_t r0, uint64_t same, uint32_t first) {
+            if (lane == first) place[r0] = place[r0] + __popcll(same);
+        });
     __syncthreads();
     uint32_t mine = 0;
     if (threadIdx.x < a.run)
@@ -361,28 +411,23 @@ __global__ __launch_bounds__(64 * kFewWaves) void sum_few(GradArgs a) {
         }
     }
     __syncthreads();
-    volatile uint32_t *place = count[wave];
 #pragma unroll
-    for (uint32_t u = 0; u < kFewEach; u++) {
-        for (uint64_t left = __ballot(row[u] != 0xFFFFFFFFu); left;) {
-            const uint32_t first = __builtin_ctzll(left);
-            const uint32_t r0 = __builtin_amdgcn_readlane(row[u], first);
-            const uint64_t same = __ballot(row[u] == r0);
+    for (uint32_t u = 0; u < kFewEach; u++)
+        match(row[u], row[u] != 0xFFFFFFFFu, [&](uint32_t r0, uint64_t same, uint32_t first) {
             const uint32_t at = place[r0];
             if (row[u] == r0) list[at + __popcll(same & ((1ull << lane) - 1))] = uint16_t(wave * a.span + 64 * u + lane);
             if (lane == first) place[r0] = at + __popcll(same);
-            left &= ~same;
-        }
-    }
+        });
     __syncthreads();
 
     uint64_t many = 0;  // whether a row of many tokens is among the workgroup's
     for (uint32_t r = wave; r < a.run && base + r < a.rows; r += kFewWaves) {
         const uint32_t from = uniform(r ? end[r - 1] : 0), n = uniform(end[r]) - from;
         if (n == 0) {
-            if (!ADD) store_group<Y>(static_cast<Y *>(a.dw) + (base + r) * a.dw_stride, c, a.cols, f32x8(0.0f));
+            if (!ADD)
+                store_group<Y>(row_of_dw<Y>(a, base + r), c, a.cols, f32x8(0.0f));
         } else if (n <= kMany) {
-            finish<Y>(a, base + r, c, sum_listed<X>(a, list + from, n, c), ADD);
+            finish<Y, ADD>(a, base + r, c, sum_listed<X>(a, list + from, n, c));
         } else {
             many = 1;
         }
@@ -398,7 +443,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void sum_few(GradArgs a) {
             f32x8 sum = *reinterpret_cast<const f32x8 *>(&part[0][lane * 8]);
 #pragma unroll
             for (uint32_t w = 1; w < kFewWaves; w++) sum += *reinterpret_cast<const f32x8 *>(&part[w][lane * 8]);
-            finish<Y>(a, base + r, c, sum, ADD);
+            finish<Y, ADD>(a, base + r, c, sum);
         }
         __syncthreads();
     }
@@ -425,7 +470,7 @@ bool too_many(uint64_t waves) { return (waves + 3) >> 26; }
 
 // Tokens of a chunk: enough chunks to fill the chip, and no more than their
 // borders' sums are worth.
-uint32_t chunk_of(uint32_t n) { return n <= 4096 ? 16 : n <= 65536 ? 32 : 128; }
+uint32_t chunk_of(uint32_t n) { return n <= 65536 ? 32 : 128; }
 
 // Rows of a sorting workgroup: about 128 workgroups where the table has the rows
 // for it, as each reads all tokens; up to 1024, a thread each.
@@ -484,7 +529,7 @@ uint64_t df11_embedding_gradient_scratch_bytes(uint64_t n, uint64_t rows, uint32
     if (n > DF11_EMBEDDING_MAX_TOKENS || rows > DF11_EMBEDDING_MAX_ROWS || cols > DF11_EMBEDDING_MAX_COLS) return 0;
     if (is_few(n, rows, cols)) return 0;
     const uint32_t chunk = chunk_of(uint32_t(n));
-    return 128 + 4 * (3 * padded(n) + padded(rows)) + (n + chunk - 1) / chunk * 2 * 4 * padded(cols);
+    return 128 + 16 * padded(n) + 4 * padded(rows) + (n + chunk - 1) / chunk * 2 * 4 * padded(cols);
 }
 
 int df11_embedding_gradient(const df11_embedding_grad *g, void *scratch, uint64_t scratch_bytes,
@@ -527,31 +572,37 @@ int df11_embedding_gradient(const df11_embedding_grad *g, void *scratch, uint64_
     a.chunk = chunk_of(a.n), a.run = run_of(a.rows);
     a.span = uint32_t((g->n + 64 * kSortWaves - 1) / (64 * kSortWaves) * 64);
     a.kept = static_cast<uint32_t *>(scratch);
-    a.order = a.kept + 32, a.row = a.order + padded(a.n), a.end = a.row + padded(a.n);
-    a.total = a.end + padded(a.n);
+    a.sorted = reinterpret_cast<uint4 *>(a.kept + 32);
+    a.total = reinterpret_cast<uint32_t *>(a.sorted + padded(a.n));
     a.part = reinterpret_cast<float *>(a.total + padded(a.rows));
     a.part_stride = padded(a.cols);
     const uint32_t chunks = (a.n + a.chunk - 1) / a.chunk;
-    const uint64_t summing = (uint64_t(chunks) * a.parts + 3) / 4;
+    const uint64_t joining = uint64_t(chunks) * a.parts, summing = (joining + 3) / 4;
     const uint64_t clearing = g->accumulate ? 0 : ((a.rows + 63) / 64 * uint64_t(a.parts) + 3) / 4;
-    if (too_many(4 * (summing + clearing))) return DF11_E_INVALID;
+    if (too_many(4 * std::max(joining, summing + clearing))) return DF11_E_INVALID;
     a.summing = uint32_t(summing);
     const dim3 sorting((a.rows + a.run - 1) / a.run), both(uint32_t(summing + clearing));
     const size_t lds = (kSortWaves + 1) * a.run * 4;
+    // half of the last cache
+    const bool big = (g->accumulate ? uint64_t(a.n) * a.cols * type_bytes(g->dy_type)
+                                    : uint64_t(a.rows) * a.cols * type_bytes(g->dw_type)) >= 1ull << 27;
     int rc = status(g->token_bits == 64 ? launch(sort_tokens<int64_t>, sorting, dim3(64 * kSortWaves), lds, st, a)
                                         : launch(sort_tokens<int32_t>, sorting, dim3(64 * kSortWaves), lds, st, a));
     if (rc != DF11_OK) return rc;
     rc = with_types([&](auto y, auto x, auto) {
         using Y = decltype(y);
         using X = decltype(x);
-        return g->accumulate ? launch(sum_runs<X, Y, true>, both, dim3(256), 0, st, a)
-                             : launch(sum_runs<X, Y, false>, both, dim3(256), 0, st, a);
+        if (g->accumulate)
+            return big ? launch(sum_runs<X, Y, true, true>, both, dim3(256), 0, st, a)
+                       : launch(sum_runs<X, Y, true, false>, both, dim3(256), 0, st, a);
+        return big ? launch(sum_runs<X, Y, false, true>, both, dim3(256), 0, st, a)
+                   : launch(sum_runs<X, Y, false, false>, both, dim3(256), 0, st, a);
     });
     if (rc != DF11_OK) return rc;
     return with_type(g->dw_type, [&](auto y) {
         using Y = decltype(y);
-        return status(g->accumulate ? launch(join_runs<Y, true>, dim3(a.summing), dim3(256), 0, st, a)
-                                    : launch(join_runs<Y, false>, dim3(a.summing), dim3(256), 0, st, a));
+        return status(g->accumulate ? launch(join_runs<Y, true>, dim3(uint32_t(joining)), dim3(256), 0, st, a)
+                                    : launch(join_runs<Y, false>, dim3(uint32_t(joining)), dim3(256), 0, st, a));
     });
 }
 

@@ -39,7 +39,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // What the tiles of a launch compute.
-enum Kind { STATS, GRAD, DX, DW };
+enum Kind { STATS, GRAD, DX, DW, DW_PAST };  // DW_PAST: DW stored past the caches
 
 constexpr uint32_t kDepth = 64;  // of a stage: columns (or rows) that are summed over
 constexpr uint32_t kNever = 0x7FFFFF00u;  // an offset behind every buffer: the load gives zeros
@@ -72,7 +72,6 @@ struct TileArgs {
     void *y;
     uint64_t y_stride, y_split;
     uint32_t add;
-    uint32_t past;  // store past the caches
 };
 
 // A tile's operand whose rows are consecutive in k: 128 bytes of each of ROWS
@@ -199,8 +198,8 @@ __device__ __forceinline__ float2 joined(float2 r, float2 o) {
 template <class Y, class S, int KIND, int BT, int BR, int WT, int WR, int NB>
 __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
     constexpr int kWaves = WT * WR, FT = BT / WT / 16, FR = BR / WR / 16;
-    constexpr bool kLogits = KIND == STATS || KIND == GRAD;
-    using A = std::conditional_t<KIND == DW, Turned<BT, kWaves>, Straight<BT, kWaves>>;
+    constexpr bool kLogits = KIND == STATS || KIND == GRAD, kDw = KIND >= DW;
+    using A = std::conditional_t<kDw, Turned<BT, kWaves>, Straight<BT, kWaves>>;
     using B = std::conditional_t<kLogits, Straight<BR, kWaves>, Turned<BR, kWaves>>;
     constexpr int kA = BT * kDepth * 2, kB = BR * kDepth * 2;  // bytes of a stage
     // a buffer is an object of its own, so that the compiler sees that reads
@@ -214,8 +213,8 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
     const uint32_t wave = uniform(threadIdx.x >> 6);
     // tokens that there are, where only the device knows
     const uint32_t n = a.count ? uniform(*a.count) : 0;
-    const uint32_t t_size = KIND != DW && a.count ? n : a.t_size;
-    const uint32_t k_size = KIND == DW ? n : a.k_size;
+    const uint32_t t_size = !kDw && a.count ? n : a.t_size;
+    const uint32_t k_size = kDw ? n : a.k_size;
 
     // Workgroups go to the 8 XCDs in turn: every XCD takes one run of the
     // tiles and walks them 4 wide in t, so that the tiles at work on an XCD
@@ -232,7 +231,7 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
 
     A xa;
     B wb;
-    if constexpr (KIND == DW) xa.init(a.a + t0, a.a_stride, uint32_t(a.a_stride) - t0, 0, wave, lane);
+    if constexpr (kDw) xa.init(a.a + t0, a.a_stride, uint32_t(a.a_stride) - t0, 0, wave, lane);
     else xa.init(a.a + t0 * a.a_stride, a.a_stride, t_size - t0, KIND == DX ? uint32_t(a.a_stride) : k_size, wave, lane);
     if constexpr (kLogits) wb.init(a.b + r0 * a.b_stride, a.b_stride, a.r_size - r0, k_size, wave, lane);
     else wb.init(a.b + r0, a.b_stride, a.r_size - r0, 0, wave, lane);
@@ -461,7 +460,7 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
 #pragma unroll
                         for (uint32_t e = 0; e < kEach; e++) sum[e] = Y(v[e]);
                     }
-                    if (KIND == DW && a.past) __builtin_nontemporal_store(YE_any(sum), reinterpret_cast<YE_any *>(to));
+                    if (KIND == DW_PAST) __builtin_nontemporal_store(YE_any(sum), reinterpret_cast<YE_any *>(to));
                     else *reinterpret_cast<YE_any *>(to) = sum;
                 } else {
 #pragma unroll
@@ -941,17 +940,19 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
             a.count = s.count;
             a.t_size = here, a.r_size = p->cols;
             a.y_stride = g->dw_stride, a.add = g->accumulate;
+            const int tile = tile_for(here, p->cols, uint64_t(p->n) * dw_terms);
             // a gradient that the caches do not hold passes them by, which leaves x and g
             // there (512 tokens, 128256 x 4096: 580 us, 629 through them)
-            a.past = uint64_t(p->rows) * p->cols * type_bytes(g->dw_type) >= 1ull << 27;
-            const int tile = tile_for(here, p->cols, uint64_t(p->n) * dw_terms);
+            const bool past = uint64_t(p->rows) * p->cols * type_bytes(g->dw_type) >= 1ull << 27;
             if (g->dw_type == DF11_TYPE_F32) {
                 a.y = static_cast<float *>(g->dw) + c * g->dw_stride;
-                rc = run_tiles<float, float, DW>(tile, a, here, st);
+                rc = past ? run_tiles<float, float, DW_PAST>(tile, a, here, st)
+                          : run_tiles<float, float, DW>(tile, a, here, st);
             } else {
                 a.y = static_cast<__bf16 *>(g->dw) + c * g->dw_stride;
-                rc = g->accumulate ? run_tiles<__bf16, float, DW>(tile, a, here, st)
-                                   : run_tiles<__bf16, __bf16, DW>(tile, a, here, st);
+                if (g->accumulate) rc = run_tiles<__bf16, float, DW>(tile, a, here, st);
+                else rc = past ? run_tiles<__bf16, __bf16, DW_PAST>(tile, a, here, st)
+                               : run_tiles<__bf16, __bf16, DW>(tile, a, here, st);
             }
             if (rc != DF11_OK) return rc;
         }

@@ -803,7 +803,7 @@ int df11_embedding(const df11_embedding_lookup *e, df11_hip_stream st);
  *   dw[v][c] = scale * sum over the i with tokens[i] = v of dy[i][c]
  * or, with accumulate, dw[v][c] + that (as where microbatches add up, or an
  * output head shares the table's memory).  Sums are float32, of a row's tokens
- * in the order of their positions, or of up to 8 or chunks of 32 or 128 of them
+ * in the order of their positions, or of up to 8 or chunks of 32 to 128 of them
  * and then of those sums in order (as n, rows and cols have it, and the tokens'
  * places among the sorted); scaled, added and rounded once to dw_type.  No atomics on floats: the same inputs give the same bits.  Rows
  * without a token are set to zeros; with accumulate they are neither read nor

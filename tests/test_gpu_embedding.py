@@ -162,7 +162,7 @@ def test_gradient_of_one_row(n, rows):
 
 
 def test_gradient_of_runs_that_end_with_chunks():
-    """Runs of 1 to 128 tokens, each length at every offset of a chunk of 32."""
+    """Runs of 1 to 128 tokens, each length at many offsets of a chunk of 32."""
     say("[gpu] gradient of runs at chunk borders")
     for first in range(1, 33):
         lengths = [first] + [k for k in (16, 32, 1, 31, 33, 63, 64, 65, 128, 32, 32, 2) for _ in "abcde"]
