@@ -1571,9 +1571,12 @@ class Embedding(_Lender):
 
     def gradient(self, tokens, dy, out=None, dtype=None, accumulate: bool = False, stream=None):
         """The table's gradient of a call with these tokens whose output's gradient
-        is ``dy``: embedding_gradient with the table's rows, scale and padding."""
-        return embedding_gradient(tokens, dy, self.table.size(0), dtype or self.table.dtype, out, accumulate,
-                                  self.scale, self.padding_idx, stream)
+        is ``dy``: embedding_gradient with the table's rows, scale and padding, of the
+        table's type by default."""
+        if dtype is None and out is None:
+            dtype = self.table.dtype
+        return embedding_gradient(tokens, dy, self.table.size(0), dtype, out, accumulate, self.scale,
+                                  self.padding_idx, stream)
 
 
 def embedding_gradient(tokens, dy, rows: int, dtype=None, out=None, accumulate: bool = False,
