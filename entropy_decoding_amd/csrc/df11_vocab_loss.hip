@@ -318,6 +318,26 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
             products(odd, f);
         }
     };
+    // what the results of a token need: its lse, p, q and target's row (of the
+    // piece), read first and put into LDS when they have come
+    __shared__ float4 tokens[kLogits ? BT : 1];
+    float4 token = make_float4(0.0f, 0.0f, 0.0f, __uint_as_float(kNever));
+    if (kLogits && threadIdx.x < BT && t0 + threadIdx.x < t_size) {
+        const uint32_t t = t0 + threadIdx.x;
+        if constexpr (KIND == STATS) {
+            const int64_t target = a.target_bits == 64 ? static_cast<const int64_t *>(a.targets)[t]
+                                                       : int64_t(static_cast<const int32_t *>(a.targets)[t]);
+            if (target >= a.first && target < int64_t(a.first) + a.r_size)
+                token.w = __uint_as_float(uint32_t(target) - a.first);
+        } else {
+            token.x = a.lse[t], token.y = a.factor[t].x, token.z = a.factor[t].y;
+            token.w = __uint_as_float(a.target_of[t] - a.first);
+        }
+    }
+    const auto put_token = [&] {
+        if (kLogits && threadIdx.x < BT) tokens[threadIdx.x] = token;
+    };
+    if (!stages) put_token();
     if (stages) {
         if constexpr (kLogits) {
             const uint32_t tail = (stages - 1) * kDepth;
@@ -337,6 +357,7 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
         if constexpr (NB > 2) begin(x2, w2, 2);
         if constexpr (NB > 3) begin(x3, w3, 3);
         if constexpr (NB > 4) begin(x4, w4, 4), begin(x5, w5, 5);
+        put_token();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt((kStart & 15) | (kStart >> 4 << 14) | 0x0070);
         __builtin_amdgcn_s_barrier();
@@ -371,32 +392,38 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
 
     // Lane l holds t l % 16 and r 4 (l / 16) .. + 3 of each product.
     const uint32_t q = lane >> 4, i = lane & 15u;
+    const bool edge = r0 + BR > a.r_size || t0 + BT > t_size;
     if constexpr (KIND == STATS) {
         float2 *both = reinterpret_cast<float2 *>(x0);  // [wave of r][t]
         static_assert(WR * BT * 8 <= kA, "room for the waves' sums");
 #pragma unroll
         for (int f = 0; f < FT; f++) {
-            const uint32_t t = t0 + wt + 16 * f + i;
-            // the target's row within this wave's, if it is there
-            uint32_t target = kNever;
-            if (t < t_size) {
-                const int64_t of = (a.target_bits == 64 ? static_cast<const int64_t *>(a.targets)[t]
-                                                        : int64_t(static_cast<const int32_t *>(a.targets)[t])) -
-                                   a.first;
-                if (of >= r0 + wr && of < a.r_size) target = uint32_t(of) - r0 - wr;
+            // the target's logit, where it is this wave's, leaves the others
+            const uint32_t target = __float_as_uint(tokens[wt + 16 * f + i].w) - r0 - wr;
+            if (__any(target < 16 * FR)) {
+                float told = 0.0f;
+#pragma unroll
+                for (int h = 0; h < FR; h++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const bool is = target == 16 * h + 4 * q + e;
+                        told = is ? acc[f][h][e] : told;
+                        acc[f][h][e] = is ? -__builtin_inff() : acc[f][h][e];
+                    }
+                if (target < 16 * FR && (target >> 2 & 3) == q) a.told[t0 + wt + 16 * f + i] = told;
             }
-            float top = -__builtin_inff(), told = 0.0f;
+            if (edge) {
+#pragma unroll
+                for (int h = 0; h < FR; h++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if (r0 + wr + 16 * h + 4 * q + e >= a.r_size) acc[f][h][e] = -__builtin_inff();
+            }
+            float top = -__builtin_inff();
 #pragma unroll
             for (int h = 0; h < FR; h++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const uint32_t r = 16 * h + 4 * q + e;
-                    const bool is = target == r;
-                    told = is ? acc[f][h][e] : told;
-                    if (is || r0 + wr + r >= a.r_size) acc[f][h][e] = -__builtin_inff();
-                    top = fmaxf(top, acc[f][h][e]);
-                }
-            if (target < 16 * FR && (target >> 2 & 3) == q) a.told[t] = told;
+                for (int e = 0; e < 4; e++) top = fmaxf(top, acc[f][h][e]);
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
             const float from = top == -__builtin_inff() ? 0.0f : top;
@@ -471,33 +498,33 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
         };
 #pragma unroll
         for (int f = 0; f < FT / 2; f++) {
-            float lse[2], p[2], minus[2];
-            uint32_t target[2];
-            if constexpr (KIND == GRAD) {
-#pragma unroll
-                for (int g = 0; g < 2; g++) {
-                    const uint32_t t = min(t0 + wt + 32 * f + 16 * g + i, t_size - 1);
-                    lse[g] = a.lse[t];
-                    p[g] = a.factor[t].x, minus[g] = a.factor[t].y;
-                    target[g] = a.target_of[t] - a.first;
-                }
-            }
 #pragma unroll
             for (int h0 = 0; h0 < FR; h0 += kParts) {
                 if constexpr (KIND == GRAD) {
                     // the part of g, rounded to BF16; the second term is what that leaves
 #pragma unroll
                     for (int g = 0; g < 2; g++) {
-                        const bool token = t0 + wt + 32 * f + 16 * g + i < t_size;
+                        const float4 of = tokens[wt + 32 * f + 16 * g + i];
+                        const uint32_t target = __float_as_uint(of.w) - r0 - wr;
+                        const bool on = t0 + wt + 32 * f + 16 * g + i < t_size;
+                        f32x4 (&row)[FR] = acc[2 * f + g];
 #pragma unroll
-                        for (int h = h0; h < h0 + kParts; h++) {
+                        for (int h = h0; h < h0 + kParts; h++)
 #pragma unroll
-                            for (int e = 0; e < 4; e++) {
-                                const uint32_t r = r0 + wr + 16 * h + 4 * q + e;
-                                float v = p[g] * exp_of(acc[2 * f + g][h][e] - lse[g]);
-                                if (r == target[g]) v -= minus[g];
-                                acc[2 * f + g][h][e] = token && r < a.r_size ? v : 0.0f;
-                            }
+                            for (int e = 0; e < 4; e++) row[h][e] = of.y * exp_of(row[h][e] - of.x);
+                        if (__any(target < 16 * FR)) {
+#pragma unroll
+                            for (int h = h0; h < h0 + kParts; h++)
+#pragma unroll
+                                for (int e = 0; e < 4; e++)
+                                    row[h][e] -= target == 16 * h + 4 * q + e ? of.z : 0.0f;
+                        }
+                        if (edge) {
+#pragma unroll
+                            for (int h = h0; h < h0 + kParts; h++)
+#pragma unroll
+                                for (int e = 0; e < 4; e++)
+                                    if (!on || r0 + wr + 16 * h + 4 * q + e >= a.r_size) row[h][e] = 0.0f;
                         }
                     }
                 }
@@ -783,9 +810,13 @@ struct LossScratch {
     }
 };
 
-// g of a piece of so many rows at a time: 2^27 elements of it.
+// g of so many rows at a time: up to 2^29 elements of it, in chunks of about the
+// same size.  Every chunk but the first reads and writes dx's sums again: in chunks
+// of 2^27 elements 8192 tokens x 128256 x 4096 took CHUNK_27 ms, of 2^29 CHUNK_29.
 uint64_t chunk_rows(uint64_t n, uint64_t rows) {
-    return std::min(up(rows, 256), std::max<uint64_t>((1ull << 27) / std::max<uint64_t>(n, 1) / 256 * 256, 256));
+    const uint64_t most = std::max<uint64_t>((1ull << 29) / std::max<uint64_t>(n, 1) / 256 * 256, 256);
+    const uint64_t chunks = (rows + most - 1) / most;
+    return up((rows + chunks - 1) / std::max<uint64_t>(chunks, 1), 256);
 }
 
 struct GradScratch {

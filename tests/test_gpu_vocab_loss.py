@@ -174,8 +174,8 @@ def test_pieces(n, rows, cols, pieces):
 def test_long_vocabulary_in_chunks():
     """g in several chunks of the vocabulary, with one and with two terms."""
     say("[gpu] g in several chunks")
-    check_all(9000, 40_000, 16, seed=1)
-    check_all(9000, 30_100, 16, seed=2, dx=F32, dw=F32, add=True)
+    check_all(20_000, 60_000, 16, seed=1)
+    check_all(20_000, 30_100, 16, seed=2, dx=F32, dw=F32, add=True)
 
 
 def test_one_number_for_all():

@@ -85,8 +85,9 @@ def test_scratch_bytes():
         assert f(bad) == g(bad) == 0
     assert 0 < f(z(1, 64, 100, 0, 0)) <= f(z(100, 64, 100, 0, 0)) <= f(z(100, 64, 9000, 0, 0))
     assert 0 < g(z(100, 64, 9000, 0, 0)) < g(z(100, 64, 9000, 1, 0)) < g(z(100, 64, 9000, 1, 1))
-    # g takes 2^27 elements at most, or 256 rows: not the logits' memory
-    assert g(z(8192, 4096, 1 << 24, 1, 0)) < 2 ** 28 + 8192 * 4096 * 4 * 2 + 2 ** 20
+    # g takes 2^29 elements at most, or 256 rows: not the logits' memory
+    assert g(z(8192, 4096, 1 << 24, 1, 0)) < 2 ** 30 + 8192 * 4096 * 4 * 2 + 2 ** 20
+    assert g(z(1 << 20, 8, 1 << 24, 0, 0)) < 2 ** 30 + 2 ** 20 * 200
 
 
 def test_struct_layouts(tmp_path):
