@@ -1765,51 +1765,54 @@ class VocabLoss(_Lender):
 
         x, p = self._piece(x, targets, ignore_index)
         n, cols = p.n, p.cols
-        g = df11_vocab_grad(accumulate=bool(accumulate))
-        factors = []
-        for name, value in (("lse", lse), ("loss_grad", loss_grad), ("lse_grad", lse_grad)):
-            if value is None or (name == "loss_grad" and not hasattr(value, "data_ptr")):
-                continue
-            if (value.dtype != torch.float32 or value.device != self.device or not value.is_contiguous()
-                    or value.numel() not in ((n,) if name == "lse" else (1, n))):
-                raise ValueError(f"{name} must be contiguous float32 on {self.device}, one for each token")
-            factors.append(value)
-            setattr(g, name, value.data_ptr())
-            if name != "lse":
-                setattr(g, name + "s", value.numel())
-        if not hasattr(loss_grad, "data_ptr"):
+        g, used = df11_vocab_grad(), [x, targets, lse]
+        g.accumulate = bool(accumulate)
+        g.lse = self._per_token("lse", lse, (n,))
+        if hasattr(loss_grad, "data_ptr"):
+            g.loss_grad, g.loss_grads = self._per_token("loss_grad", loss_grad, (1, n)), loss_grad.numel()
+            used.append(loss_grad)
+        else:
             g.loss_grad_all = loss_grad
-        kinds = {}
-        for name, needed, given, shapes, kind in (
-                ("dx", needs_dx, None if dx is None else [dx], [(n, cols)], dx_dtype),
-                ("dw", needs_dw, None if dws is None else list(dws), self.shapes, dw_dtype)):
-            if given is not None:
-                if not needed or len(given) != len(shapes) or not given:
-                    raise ValueError(f"{name}: a tensor for each gradient that is needed")
-                kind = kind or given[0].dtype
-                for t, shape in zip(given, shapes):
-                    _output(t, name, shape, kind, self.device)
-            kind = kind or torch.bfloat16
-            if kind not in (torch.bfloat16, torch.float32):
-                raise TypeError(f"{name} must be bfloat16 or float32")
-            kinds[name] = kind if needed else None
-        if accumulate and (dws is None or not needs_dw):
-            raise ValueError("accumulate adds to dws")
-        made = [t for t in (([] if dx is None else [dx]) + ([] if dws is None else list(dws)))]
+        if lse_grad is not None:
+            g.lse_grad, g.lse_grads = self._per_token("lse_grad", lse_grad, (1, n)), lse_grad.numel()
+            used.append(lse_grad)
+        given = []  # outputs
+        if dx is not None:
+            _output(dx, "dx", (n, cols), dx_dtype, self.device)
+            dx_dtype = dx.dtype
+            given.append(dx)
+        if dws is not None:
+            dws = list(dws)
+            if len(dws) != len(self.shapes):
+                raise ValueError("dws must be a tensor for each piece")
+            dw_dtype = dw_dtype or dws[0].dtype
+            for t, shape in zip(dws, self.shapes):
+                _output(t, "dws", shape, dw_dtype, self.device)
+            given += dws
+        if (accumulate and dws is None) or (dx is not None and not needs_dx) or (dws is not None and not needs_dw):
+            raise ValueError("accumulate adds to dws; outputs are given for gradients that are needed")
+        dx_dtype, dw_dtype = dx_dtype or torch.bfloat16, dw_dtype or torch.bfloat16
+        for kind in (dx_dtype, dw_dtype):
+            if kind is not torch.bfloat16 and kind is not torch.float32:
+                raise TypeError("gradients are bfloat16 or float32")
+        two = (needs_dx and dx_dtype is torch.float32) or (needs_dw and dw_dtype is torch.float32)
         guard, st = _on(self.device, stream)
         with guard:
-            given, targets = targets, targets.contiguous()
-            p.targets = targets.data_ptr()
+            at = targets.contiguous()
+            p.targets = at.data_ptr()
             if needs_dx:
                 if dx is None:
-                    dx = torch.empty(n, cols, dtype=kinds["dx"], device=self.device)
-                g.dx, g.dx_stride, g.dx_type = dx.data_ptr(), dx.stride(0) if n > 1 else cols, _type(dx.dtype)
+                    dx = torch.empty(n, cols, dtype=dx_dtype, device=self.device)
+                g.dx, g.dx_stride, g.dx_type = dx.data_ptr(), dx.stride(0) if n > 1 else cols, _type(dx_dtype)
             if needs_dw:
                 if dws is None:
-                    dws = [torch.empty(shape, dtype=kinds["dw"], device=self.device) for shape in self.shapes]
-                g.dw_type = _type(kinds["dw"])
-            sizes = df11_vocab_sizes(n, cols, self._rows, needs_dx, torch.float32 in kinds.values())
-            need = LIB.df11_vocab_loss_gradient_scratch_bytes(sizes)
+                    dws = [torch.empty(shape, dtype=dw_dtype, device=self.device) for shape in self.shapes]
+                g.dw_type = _type(dw_dtype)
+            held = self._bytes.get((n, needs_dx, two))
+            if held is None:
+                sizes = df11_vocab_sizes(n, cols, self._rows, bool(needs_dx), two)
+                held = self._bytes[n, needs_dx, two] = sizes, LIB.df11_vocab_loss_gradient_scratch_bytes(sizes)
+            sizes, need = held
             scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
             for k in self._each(p, status, st):
                 if needs_dw:
@@ -1817,12 +1820,21 @@ class VocabLoss(_Lender):
                     g.dw, g.dw_stride = dw.data_ptr(), dw.stride(0) if p.rows > 1 else cols
                 _check("df11_vocab_loss_gradient",
                        LIB.df11_vocab_loss_gradient(p, g, sizes, scratch.data_ptr(), need, st))
-        if made:
-            torch._C._increment_version(made)
-        dx, dws = dx if needs_dx else None, list(dws) if needs_dw else None
-        self._used(stream, st, [x, given, *factors, *([dx] if needs_dx else []), *(dws or []),
-                                *([] if status is None else [status])])
-        return dx, dws
+        if given:
+            torch._C._increment_version(given)
+        if stream is not None or st not in self._lent:
+            self._used(stream, st, used + ([dx] if needs_dx else []) + (dws if needs_dw else []) +
+                       ([] if status is None else [status]))
+        return dx if needs_dx else None, dws if needs_dw else None
+
+    def _per_token(self, name, value, counts):
+        """The address of a float32 tensor of one of these numbers of elements."""
+        import torch
+
+        if (value.dtype is not torch.float32 or value.device != self.device or not value.is_contiguous()
+                or value.numel() not in counts):
+            raise ValueError(f"{name} must be contiguous float32 on {self.device}, one for each token")
+        return value.data_ptr()
 
 
 def table_bytes(cb: df11_codebook) -> int:

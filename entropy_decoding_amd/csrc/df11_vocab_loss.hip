@@ -12,7 +12,8 @@
 //
 //   stats tiles     logits of a tile; the target's, and the others' largest value and sum
 //   loss_join       joins tiles and pieces: lse and loss
-//   pick, gather    the tokens that have a gradient, one behind the other
+//   pick, gather    the tokens that have a gradient, one behind the other (up to 1024
+//                   tokens in one launch)
 //   grad tiles      logits again; g
 //   dx tiles        g w, added up over pieces in float32
 //   dw tiles        g^T x
@@ -632,7 +633,19 @@ __global__ __launch_bounds__(1024) void loss_join(TokenArgs a) {
     a.losses[t] = target == a.ignored ? 0.0f : loss;
 }
 
-// The tokens that have a gradient, in order, with what their part of g needs.
+// What a token's part of g needs, at its place among those that have a gradient.
+__device__ __forceinline__ void put_token(const TokenArgs &a, uint32_t t, uint32_t at, int64_t target) {
+    const bool inside = target >= 0 && target < a.vocab;
+    const float of_loss = a.loss_grad ? a.loss_grad[t * uint64_t(a.loss_grad_step)] : a.loss_grad_all;
+    const float of_lse = a.lse_grad ? a.lse_grad[t * uint64_t(a.lse_grad_step)] : 0.0f;
+    const float nan = __builtin_nanf("");
+    a.order[at] = t;
+    a.target_of[at] = inside ? uint32_t(target) : 0xFFFFFFFFu;
+    a.lse_of[at] = a.lse_in[t];
+    a.factor[at] = inside ? make_float2(of_loss + of_lse, of_loss) : make_float2(nan, nan);
+}
+
+// The tokens that have a gradient, in order.
 __global__ __launch_bounds__(1024) void pick(TokenArgs a) {
     __shared__ uint32_t sums[16];
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
@@ -652,15 +665,7 @@ __global__ __launch_bounds__(1024) void pick(TokenArgs a) {
         before += total;
         __syncthreads();
         if (t < a.n) a.place[t] = on ? at : 0xFFFFFFFFu;
-        if (!on) continue;
-        const bool inside = target >= 0 && target < a.vocab;
-        const float of_loss = a.loss_grad ? a.loss_grad[t * uint64_t(a.loss_grad_step)] : a.loss_grad_all;
-        const float of_lse = a.lse_grad ? a.lse_grad[t * uint64_t(a.lse_grad_step)] : 0.0f;
-        const float nan = __builtin_nanf("");
-        a.order[at] = t;
-        a.target_of[at] = inside ? uint32_t(target) : 0xFFFFFFFFu;
-        a.lse_of[at] = a.lse_in[t];
-        a.factor[at] = inside ? make_float2(of_loss + of_lse, of_loss) : make_float2(nan, nan);
+        if (on) put_token(a, t, at, target);
     }
     if (threadIdx.x == 0) *a.count = before;
 }
@@ -673,6 +678,31 @@ __global__ __launch_bounds__(256) void gather(TokenArgs a) {
     if (i >= *a.count || c >= a.cols) return;
     *reinterpret_cast<bf16x8 *>(a.to + i * a.to_stride + c) =
         *reinterpret_cast<const bf16x8 *>(a.x + a.order[i] * a.x_stride + c);
+}
+
+// Both in one launch for few tokens: every wave counts those before its own.
+constexpr uint32_t kFewTokens = 1024;
+
+__global__ __launch_bounds__(256) void pick_and_gather(TokenArgs a) {
+    const uint32_t parts = (a.cols + 511) / 512;
+    const uint32_t wave = uniform(blockIdx.x * 4 + (threadIdx.x >> 6)), lane = threadIdx.x & 63u;
+    const uint32_t t = wave / parts, c = wave % parts * 512 + lane * 8;
+    if (t >= a.n) return;
+    const int64_t target = target_at(a, t);
+    bf16x8 x;
+    if (c < a.cols) x = *reinterpret_cast<const bf16x8 *>(a.x + t * a.x_stride + c);
+    uint32_t at = 0;
+#pragma unroll 4
+    for (uint32_t i = lane; i < kFewTokens; i += 64) {
+        if (i - lane >= t) break;
+        at += __popcll(__ballot(i < t && target_at(a, min(i, t)) != a.ignored));
+    }
+    const bool on = target != a.ignored;
+    if (on && c < a.cols) *reinterpret_cast<bf16x8 *>(a.to + at * a.to_stride + c) = x;
+    if (wave % parts || lane) return;
+    a.place[t] = on ? at : 0xFFFFFFFFu;
+    if (on) put_token(a, t, at, target);
+    if (t == a.n - 1) *a.count = at + on;
 }
 
 // dx of every token: the splits' sums in order, zeros for those without a gradient.
@@ -935,8 +965,12 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
     t.to = s.x, t.to_stride = s.x_stride, t.cols = p->cols;
     int rc = DF11_OK;
     if (p->begin) {
-        rc = status(launch(pick, dim3(1), dim3(1024), 0, st, t));
-        if (rc == DF11_OK && p->n) rc = status(launch(gather, rows, dim3(256), 0, st, t));
+        if (p->n && p->n <= kFewTokens) {
+            rc = status(launch(pick_and_gather, rows, dim3(256), 0, st, t));
+        } else {
+            rc = status(launch(pick, dim3(1), dim3(1024), 0, st, t));
+            if (rc == DF11_OK && p->n) rc = status(launch(gather, rows, dim3(256), 0, st, t));
+        }
         if (rc != DF11_OK) return rc;
     }
     for (uint64_t c = 0; c < p->rows || (!p->rows && !c); c += s.chunk) {

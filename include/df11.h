@@ -908,7 +908,7 @@ int df11_vocab_loss(const df11_vocab_piece *p, float *losses, float *lse, void *
  * NaN.  Pieces as above: begin, then dw of each piece is written by its own
  * call, dx by the one with end.  g exists for up to 2^29 elements at a time (n times
  * the rows of a piece, or of equal parts of it; at least 256 rows).  2 launches for
- * begin, 1 for end, and 3 for every such part.
+ * begin (1 for up to 1024 tokens), 1 for end, and 3 for every such part.
  */
 typedef struct df11_vocab_grad {
     const float *lse;        /* n, from df11_vocab_loss */

@@ -270,7 +270,7 @@ def test_nan_in_ignored_tokens_goes_nowhere():
     """A padded batch whose padding holds NaN and infinities: the counted tokens'
     results are those of a batch without it."""
     say("[gpu] NaN in ignored tokens")
-    for n in (20, 150, 400):
+    for n in (20, 150, 400, 1023, 1024, 1025, 3000):
         x, w, targets = inputs(n, 500, 72, n)
         head, on = ed.VocabLoss([w]), targets != -100
         x[~on] = float("nan")
