@@ -258,6 +258,7 @@ class df11_vocab_sizes(ctypes.Structure):
 class df11_vocab_grad(ctypes.Structure):
     _fields_ = [
         ("lse", ctypes.c_void_p),
+        ("losses", ctypes.c_void_p),
         ("loss_grad", ctypes.c_void_p),
         ("lse_grad", ctypes.c_void_p),
         ("dx", ctypes.c_void_p),
@@ -1752,15 +1753,17 @@ class VocabLoss(_Lender):
 
     def gradient(self, x, targets, lse, loss_grad=1.0, lse_grad=None, ignore_index: int = -100,
                  dx_dtype=None, dw_dtype=None, dx=None, dws=None, accumulate: bool = False,
-                 needs_dx: bool = True, needs_dw: bool = True, status=None, stream=None):
+                 needs_dx: bool = True, needs_dw: bool = True, losses=None, status=None, stream=None):
         """(dx, dws) of a call with these arguments that returned ``lse``: the hidden
         states' gradient [n, cols] and a list of the pieces' gradients, BF16 or
         float32 (``dx_dtype``, ``dw_dtype``: BF16 by default; float32 doubles that
         product's work), as new tensors or written into ``dx`` and ``dws``, with
         ``accumulate`` added to dws.  ``loss_grad``: the gradient that the losses
         have, a number or a float32 device tensor of one or of n elements;
-        ``lse_grad``: that of lse, such a tensor or None.  Ignored tokens have no
-        gradient and add none.  Without ``needs_dx`` or ``needs_dw`` that one is None."""
+        ``lse_grad``: that of lse, such a tensor or None.  ``losses``: the call's; with
+        them the gradient keeps its digits where a target is nearly certain.  Ignored
+        tokens have no gradient and add none.  Without ``needs_dx`` or ``needs_dw`` that
+        one is None."""
         import torch
 
         x, p = self._piece(x, targets, ignore_index)
@@ -1768,6 +1771,9 @@ class VocabLoss(_Lender):
         g, used = df11_vocab_grad(), [x, targets, lse]
         g.accumulate = bool(accumulate)
         g.lse = self._per_token("lse", lse, (n,))
+        if losses is not None:
+            g.losses = self._per_token("losses", losses, (n,))
+            used.append(losses)
         if hasattr(loss_grad, "data_ptr"):
             g.loss_grad, g.loss_grads = self._per_token("loss_grad", loss_grad, (1, n)), loss_grad.numel()
             used.append(loss_grad)

@@ -64,7 +64,8 @@ struct TileArgs {
     uint32_t part_tiles;
     float *told;          // the targets' logits
     const float *lse;
-    const float2 *factor; // p, q
+    const float2 *factor; // p, and q or (exact_target) what g is at the target
+    uint32_t exact_target;
     const uint32_t *target_of;
     __bf16 *g;
     uint64_t g_stride, g_half;
@@ -519,7 +520,8 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
                             for (int h = h0; h < h0 + kParts; h++)
 #pragma unroll
                                 for (int e = 0; e < 4; e++)
-                                    row[h][e] -= target == 16 * h + 4 * q + e ? of.z : 0.0f;
+                                    if (target == 16 * h + 4 * q + e)
+                                        row[h][e] = a.exact_target ? of.z : row[h][e] - of.z;
                         }
                         if (edge) {
 #pragma unroll
@@ -568,7 +570,7 @@ struct TokenArgs {
     float *losses, *lse;
     uint32_t begin, end;
     // pick, gather, spread
-    const float *lse_in, *loss_grad, *lse_grad;
+    const float *lse_in, *loss_in, *loss_grad, *lse_grad;
     uint32_t loss_grad_step, lse_grad_step;
     float loss_grad_all;
     uint32_t *count, *order, *place, *target_of;
@@ -639,10 +641,13 @@ __device__ __forceinline__ void put_token(const TokenArgs &a, uint32_t t, uint32
     const float of_loss = a.loss_grad ? a.loss_grad[t * uint64_t(a.loss_grad_step)] : a.loss_grad_all;
     const float of_lse = a.lse_grad ? a.lse_grad[t * uint64_t(a.lse_grad_step)] : 0.0f;
     const float nan = __builtin_nanf("");
+    // at the target p (l - lse) - q = of_loss (exp(-loss) - 1) + of_lse exp(-loss)
+    float q = of_loss;
+    if (a.loss_in) q = of_loss * expm1f(-a.loss_in[t]) + (of_lse == 0.0f ? 0.0f : of_lse * expf(-a.loss_in[t]));
     a.order[at] = t;
     a.target_of[at] = inside ? uint32_t(target) : 0xFFFFFFFFu;
     a.lse_of[at] = a.lse_in[t];
-    a.factor[at] = inside ? make_float2(of_loss + of_lse, of_loss) : make_float2(nan, nan);
+    a.factor[at] = inside ? make_float2(of_loss + of_lse, q) : make_float2(nan, nan);
 }
 
 // The tokens that have a gradient, in order.
@@ -938,7 +943,7 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
     if (has_dw && (!aligned(g->dw, type_bytes(g->dw_type)) || (p->rows > 1 && g->dw_stride < p->cols) ||
                    g->dw_stride >> 40))
         return DF11_E_INVALID;
-    if (p->n && (!g->lse || !aligned(g->lse, 4) || !aligned(g->loss_grad, 4) || !aligned(g->lse_grad, 4) ||
+    if (p->n && (!g->lse || !aligned(g->lse, 4) || !aligned(g->losses, 4) || !aligned(g->loss_grad, 4) || !aligned(g->lse_grad, 4) ||
                  (g->loss_grad && g->loss_grads != 1 && g->loss_grads != p->n) ||
                  (g->lse_grad && g->lse_grads != 1 && g->lse_grads != p->n)))
         return DF11_E_INVALID;
@@ -957,7 +962,7 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
     TokenArgs t{};
     t.targets = p->targets, t.target_bits = p->target_bits, t.n = p->n, t.vocab = p->vocab;
     t.ignored = p->ignored;
-    t.lse_in = g->lse, t.loss_grad = g->loss_grad, t.lse_grad = g->lse_grad, t.loss_grad_all = g->loss_grad_all;
+    t.lse_in = g->lse, t.loss_in = g->losses, t.loss_grad = g->loss_grad, t.lse_grad = g->lse_grad, t.loss_grad_all = g->loss_grad_all;
     t.loss_grad_step = g->loss_grads > 1, t.lse_grad_step = g->lse_grads > 1;
     t.count = s.count, t.order = s.order, t.place = s.place, t.target_of = s.target_of;
     t.lse_of = s.lse_of, t.factor = s.factor;
@@ -983,7 +988,7 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
         a.r_size = here, a.k_size = p->cols, a.first = uint32_t(p->first + c);
         a.lse = s.lse_of, a.factor = s.factor, a.target_of = s.target_of;
         a.g = s.g, a.g_stride = g_stride, a.g_half = p->n * g_stride, a.r_padded = uint32_t(g_stride);
-        a.halves = terms;
+        a.halves = terms, a.exact_target = g->losses != nullptr;
         rc = run_tiles<__bf16, __bf16, GRAD>(tile_for(p->n, here, p->cols), a, p->n, st);
         if (rc != DF11_OK) return rc;
         if (has_dx && p->n) {

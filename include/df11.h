@@ -900,7 +900,10 @@ int df11_vocab_loss(const df11_vocab_piece *p, float *losses, float *lse, void *
  * of lse (each one number, or one for every token):
  *   g[t][v] = (a[t] + c[t]) exp(l[t][v] - lse[t]) - a[t] [v = targets[t]]
  *   dx = g w       dw = g^T x       (dw + that, with accumulate)
- * The logits are computed again.  g is rounded to BF16 for gradients in BF16;
+ * The logits are computed again.  With the losses, g at the target is formed from
+ * them, a (exp(-loss) - 1) + c exp(-loss), which keeps its digits where the target
+ * is nearly certain; the difference of logit and lse has those that lse holds.
+ * g is rounded to BF16 for gradients in BF16;
  * for those in float32 it is held as two BF16 terms (16 bits and more), which
  * doubles their products.  Sums are float32, rounded once.  Ignored tokens have
  * no gradient at all: their dx is zero, and nothing of their x (which may be
@@ -912,6 +915,7 @@ int df11_vocab_loss(const df11_vocab_piece *p, float *losses, float *lse, void *
  */
 typedef struct df11_vocab_grad {
     const float *lse;        /* n, from df11_vocab_loss */
+    const float *losses;     /* n, from df11_vocab_loss, or null */
     const float *loss_grad;  /* loss_grads (1 or n) values; null: loss_grad_all */
     const float *lse_grad;   /* lse_grads (1 or n) values; null: none */
     void *dx;                /* n x cols of dx_type (with sizes->dx) */

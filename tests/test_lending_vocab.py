@@ -53,8 +53,8 @@ def test_loss(gpu):  # noqa: F811
     assert lent(gpu, [*pieces, x, targets, *out], 7)
     a, c = torch.zeros(1), torch.zeros(5)
     dws = [torch.zeros(6, 16), torch.zeros(3, 16)]
-    dx, got = head.gradient(x, targets, lse, a, c, dws=dws, accumulate=True, stream=8)
-    assert lent(gpu, [*pieces, x, targets, lse, a, c, dx, *dws], 8) and got == dws
+    dx, got = head.gradient(x, targets, lse, a, c, dws=dws, accumulate=True, losses=out[0], stream=8)
+    assert lent(gpu, [*pieces, x, targets, lse, out[0], a, c, dx, *dws], 8) and got is not None and all(p is q for p, q in zip(got, dws))
 
 
 @pytest.mark.parametrize("stream", [None, 7])
@@ -114,7 +114,7 @@ def test_refusals(gpu):  # noqa: F811
         with pytest.raises(ValueError):
             ed.VocabLoss(pieces)
     good = torch.zeros(6, 16)
-    for kw in ({"lse": lse[:4]}, {"lse": lse.double()}, {"loss_grad": torch.zeros(2)}, {"lse_grad": torch.zeros(4)},
+    for kw in ({"lse": lse[:4]}, {"losses": lse[:4]}, {"lse": lse.double()}, {"loss_grad": torch.zeros(2)}, {"lse_grad": torch.zeros(4)},
                {"loss_grad": torch.zeros(1).double()}, {"accumulate": True}, {"dws": [good, good]}, {"dws": []},
                {"dws": [good[:5]]}, {"dws": [good], "dw_dtype": BF16}, {"dx": torch.zeros(4, 16)},
                {"dws": [good], "needs_dw": False}, {"dws": [good], "accumulate": True, "needs_dw": False}):

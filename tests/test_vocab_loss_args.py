@@ -53,7 +53,7 @@ def test_loss_refuses(change):
     {"scratch": 0}, {"scratch": (1 << 20) + 128}, {"nbytes": 100},
     {"sizes": {"n": 4}}, {"sizes": {"cols": 72}}, {"sizes": {"rows": 59}}, {"sizes": {"rows": (1 << 24) + 1}}] + [
     {"grad": g} for g in (
-        {"lse": 0}, {"lse": 65538}, {"dx": 0}, {"dx": (1 << 17) + 1}, {"dx_stride": 63}, {"dx_stride": 1 << 40},
+        {"lse": 0}, {"lse": 65538}, {"losses": 4098}, {"dx": 0}, {"dx": (1 << 17) + 1}, {"dx_stride": 63}, {"dx_stride": 1 << 40},
         {"dw": (1 << 18) + 1}, {"dw_stride": 63}, {"dw_stride": 1 << 40}, {"dx_type": 2}, {"dw_type": 2},
         {"dx_type": 0}, {"dw_type": 0},  # float32 without sizes for two terms
         {"accumulate": 2}, {"loss_grad": 4098, "loss_grads": 1}, {"loss_grad": 4096, "loss_grads": 2},
