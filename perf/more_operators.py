@@ -176,7 +176,7 @@ def _loss(s):
             return {"loss": losses, "lse": lse}
         dx, (dw,) = s["head"].gradient(s["x"], s["targets"], lse, s["each"], dx_dtype=TYPES[case["dx"]],
                                        dw_dtype=TYPES[case["dw"]], accumulate=case["add"],
-                                       dws=[s["dw"]] if case["add"] else None)
+                                       dws=[s["dw"]] if case["add"] else None, losses=losses)
         return {"loss": losses, "lse": lse, "dx": dx, "dw": dw}
     x, w = s["x"].float(), s["w"].float()
     logits = x @ w.T
