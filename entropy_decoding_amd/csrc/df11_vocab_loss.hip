@@ -52,7 +52,7 @@ struct TileArgs {
     uint64_t a_stride, b_stride;
     const uint32_t *count;  // where not null, the number of tokens (t, or k of DW)
     uint32_t t_size, r_size, k_size;
-    // g in two terms: the second lies `a_half` elements behind the first, and
+    // g in one or two terms: the second lies `a_half` elements behind the first, and
     // the stages go over k once for each
     uint32_t halves;
     uint64_t a_half;
@@ -246,18 +246,20 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
 
     // Logits: stage 0 is the last 8 .. 64 columns, stage s > 0 starts at column
     // 64 (s - 1).  The others' stages go over whole groups of 64 (loads give zeros
-    // behind the end of k), a split's own, once for each term of g.
+    // behind the end of k), a split's own, each once for every term of g, so that
+    // the other operand comes from the cache the second time (16 tokens, 128256 x
+    // 4096, two terms: 1029 us where the second term followed the first, 911 so).
     const uint32_t whole = (k_size + kDepth - 1) / kDepth;
     const uint32_t s_first = kLogits ? 0 : min(whole, split * a.split_stages);
     const uint32_t s_here = kLogits ? whole : min(whole - s_first, a.split_stages);
-    const uint32_t stages = s_here * (kLogits ? 1 : a.halves);
+    const uint32_t two = kLogits ? 0 : a.halves - 1;
+    const uint32_t stages = s_here << two;
     const auto load_a = [&](char *lds, uint32_t s, int from, int to) {
         if constexpr (kLogits) {
             xa.load(lds, (s - 1) * kDepth, 0, s < stages, wave, lane, from, to);
         } else {
-            const bool half = s >= s_here;
-            const uint32_t k0 = (s_first + s - (half ? s_here : 0)) * kDepth;
-            const uint64_t behind = half ? a.a_half : 0;
+            const uint32_t k0 = (s_first + (s >> two)) * kDepth;
+            const uint64_t behind = s & two ? a.a_half : 0;
             if constexpr (KIND == DX) xa.load(lds, k0, behind, s < stages, wave, lane, from, to);
             else xa.load(lds, k0, s < stages ? k_size : 0, behind, wave, from, to);
         }
@@ -266,7 +268,7 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
         if constexpr (kLogits) {
             wb.load(lds, (s - 1) * kDepth, 0, s < stages, wave, lane, from, to);
         } else {
-            const uint32_t k0 = (s_first + s - (s >= s_here ? s_here : 0)) * kDepth;
+            const uint32_t k0 = (s_first + (s >> two)) * kDepth;
             wb.load(lds, k0, s < stages ? k_size : 0, 0, wave, from, to);
         }
     };
@@ -697,10 +699,13 @@ __global__ __launch_bounds__(256) void pick_and_gather(TokenArgs a) {
     bf16x8 x;
     if (c < a.cols) x = *reinterpret_cast<const bf16x8 *>(a.x + t * a.x_stride + c);
     uint32_t at = 0;
-#pragma unroll 4
-    for (uint32_t i = lane; i < kFewTokens; i += 64) {
-        if (i - lane >= t) break;
-        at += __popcll(__ballot(i < t && target_at(a, min(i, t)) != a.ignored));
+    for (uint32_t i0 = 0; i0 < t; i0 += 4 * 64) {
+        int64_t other[4];
+#pragma unroll
+        for (uint32_t u = 0; u < 4; u++) other[u] = target_at(a, min(i0 + 64 * u + lane, t));
+#pragma unroll
+        for (uint32_t u = 0; u < 4; u++)
+            at += __popcll(__ballot(i0 + 64 * u + lane < t && other[u] != a.ignored));
     }
     const bool on = target != a.ignored;
     if (on && c < a.cols) *reinterpret_cast<bf16x8 *>(a.to + at * a.to_stride + c) = x;
@@ -855,6 +860,12 @@ uint64_t chunk_rows(uint64_t n, uint64_t rows) {
     return up((rows + chunks - 1) / std::max<uint64_t>(chunks, 1), 256);
 }
 
+// Few tokens have g in two terms also for gradients in BF16: their products wait
+// for the head's rows (loss and gradient of 128256 x 4096: 16 tokens 911 us, with
+// one term 835; 64 tokens 918 and 848; 128 tokens 1134 and 921), and a sum of few
+// products shows a rounding of one of them where they cancel.
+constexpr uint32_t kTwoTermTokens = 64;
+
 struct GradScratch {
     uint32_t *count, *order, *place, *target_of;
     Split dx;
@@ -874,7 +885,7 @@ struct GradScratch {
         chunk = chunk_rows(n, z.rows);
         dx = dx_split(n, z.cols, chunk);
         sums = s.take<float>(z.dx ? dx.parts * n * z.cols : 0);
-        g = s.take<__bf16>(n * chunk * (z.two_terms ? 2 : 1));
+        g = s.take<__bf16>(n * chunk * (z.two_terms || n <= kTwoTermTokens ? 2 : 1));
         bytes = s.at;
     }
 };
@@ -937,9 +948,13 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
         p->rows > sizes->rows || g->dx_type > DF11_TYPE_BF16 || g->dw_type > DF11_TYPE_BF16 || g->accumulate > 1)
         return DF11_E_INVALID;
     const bool has_dx = sizes->dx, has_dw = g->dw;
-    const uint32_t dx_terms = g->dx_type == DF11_TYPE_F32 ? 2 : 1, dw_terms = g->dw_type == DF11_TYPE_F32 ? 2 : 1;
+    const bool few = p->n <= kTwoTermTokens;
+    const uint32_t dx_terms = few || g->dx_type == DF11_TYPE_F32 ? 2 : 1;
+    const uint32_t dw_terms = few || g->dw_type == DF11_TYPE_F32 ? 2 : 1;
     const uint32_t terms = std::max(has_dx ? dx_terms : 1, has_dw ? dw_terms : 1);
-    if (terms > 1 && !sizes->two_terms) return DF11_E_INVALID;
+    if (!sizes->two_terms &&
+        ((has_dx && g->dx_type == DF11_TYPE_F32) || (has_dw && g->dw_type == DF11_TYPE_F32)))
+        return DF11_E_INVALID;
     if (has_dw && (!aligned(g->dw, type_bytes(g->dw_type)) || (p->rows > 1 && g->dw_stride < p->cols) ||
                    g->dw_stride >> 40))
         return DF11_E_INVALID;

@@ -903,9 +903,9 @@ int df11_vocab_loss(const df11_vocab_piece *p, float *losses, float *lse, void *
  * The logits are computed again.  With the losses, g at the target is formed from
  * them, a (exp(-loss) - 1) + c exp(-loss), which keeps its digits where the target
  * is nearly certain; the difference of logit and lse has those that lse holds.
- * g is rounded to BF16 for gradients in BF16;
- * for those in float32 it is held as two BF16 terms (16 bits and more), which
- * doubles their products.  Sums are float32, rounded once.  Ignored tokens have
+ * g is rounded to BF16 for gradients in BF16; for those in float32, and for up to
+ * 64 tokens, it is held as two BF16 terms (16 bits and more), which doubles their
+ * products.  Sums are float32, rounded once.  Ignored tokens have
  * no gradient at all: their dx is zero, and nothing of their x (which may be
  * NaN) enters dw.  A target outside the head makes its token's dx and all of dw
  * NaN.  Pieces as above: begin, then dw of each piece is written by its own
