@@ -389,7 +389,7 @@ def _load():
     vs = ctypes.POINTER(df11_vocab_sizes)
     for f in (L.df11_vocab_loss_scratch_bytes, L.df11_vocab_loss_gradient_scratch_bytes):
         f.argtypes, f.restype = [vs], ctypes.c_uint64
-    L.df11_vocab_loss.argtypes = [ctypes.POINTER(df11_vocab_piece), vp, vp, vp, ctypes.c_uint64, vp]
+    L.df11_vocab_loss.argtypes = [ctypes.POINTER(df11_vocab_piece), vp, vp, vs, vp, ctypes.c_uint64, vp]
     L.df11_vocab_loss_gradient.argtypes = [ctypes.POINTER(df11_vocab_piece),
                                            ctypes.POINTER(df11_vocab_grad), vs, vp, ctypes.c_uint64, vp]
     for f in (L.df11_build_codebook, L.df11_encode_size, L.df11_encode,
@@ -1733,14 +1733,16 @@ class VocabLoss(_Lender):
             p.targets = targets.data_ptr()
             losses = torch.empty(targets.shape, dtype=torch.float32, device=self.device)
             lse = torch.empty_like(losses)
-            need = self._bytes.get(p.n)
-            if need is None:
-                need = self._bytes[p.n] = LIB.df11_vocab_loss_scratch_bytes(
-                    df11_vocab_sizes(p.n, p.cols, self._rows, 0, 0))
+            held = self._bytes.get(p.n)
+            if held is None:
+                sizes = df11_vocab_sizes(p.n, p.cols, self._rows, 0, 0)
+                held = self._bytes[p.n] = sizes, LIB.df11_vocab_loss_scratch_bytes(sizes)
+            sizes, need = held
             scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
             for _ in self._each(p, status, st):
                 _check("df11_vocab_loss",
-                       LIB.df11_vocab_loss(p, losses.data_ptr(), lse.data_ptr(), scratch.data_ptr(), need, st))
+                       LIB.df11_vocab_loss(p, losses.data_ptr(), lse.data_ptr(), sizes, scratch.data_ptr(),
+                                           need, st))
         if stream is not None or st not in self._lent:
             self._used(stream, st, [x, given, losses, lse] + ([] if status is None else [status]))
         return losses, lse

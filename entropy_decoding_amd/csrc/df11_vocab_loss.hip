@@ -844,16 +844,17 @@ struct Scratch {
     }
 };
 
+// All pieces of a head have the tile of the largest one, whose results have room.
 struct LossScratch {
     float2 *state, *part;
     float *told;
+    int tile;
     uint64_t bytes;
-    LossScratch(void *p, uint64_t n, uint64_t rows, uint64_t cols) {
+    LossScratch(void *p, const df11_vocab_sizes &z) : tile(tile_for(z.n, z.rows, z.cols)) {
         Scratch s{static_cast<char *>(p)};
-        state = s.take<float2>(n);
-        told = s.take<float>(n);
-        const uint32_t r = kTiles[tile_for(n, rows, cols)].r;
-        part = s.take<float2>(up(n, 16) * ((rows + r - 1) / r));
+        state = s.take<float2>(z.n);
+        told = s.take<float>(z.n);
+        part = s.take<float2>(up(z.n, 16) * ((uint64_t(z.rows) + kTiles[tile].r - 1) / kTiles[tile].r));
         bytes = s.at;
     }
 };
@@ -863,8 +864,8 @@ struct LossScratch {
 // of 2^27 elements 8192 tokens x 128256 x 4096 took 25.32 ms, of 2^29 25.03.
 uint64_t chunk_rows(uint64_t n, uint64_t rows) {
     const uint64_t most = std::max<uint64_t>((1ull << 29) / std::max<uint64_t>(n, 1) / 256 * 256, 256);
-    const uint64_t chunks = (rows + most - 1) / most;
-    return up((rows + chunks - 1) / std::max<uint64_t>(chunks, 1), 256);
+    const uint64_t chunks = std::max<uint64_t>((rows + most - 1) / most, 1);
+    return std::max<uint64_t>(up((rows + chunks - 1) / chunks, 256), 256);
 }
 
 // Few tokens have g in two terms also for gradients in BF16: their products wait
@@ -902,6 +903,11 @@ bool bad_sizes(const df11_vocab_sizes *z) {
            z->rows > DF11_VOCAB_MAX_ROWS;
 }
 
+// Whether a piece is not one that the sizes are for.
+bool other_sizes(const df11_vocab_piece *p, const df11_vocab_sizes *z) {
+    return bad_sizes(z) || z->n != p->n || z->cols != p->cols || p->rows > z->rows;
+}
+
 TileArgs tile_args() {
     TileArgs a{};
     a.halves = a.splits = 1;
@@ -914,19 +920,19 @@ TileArgs tile_args() {
 extern "C" {
 
 uint64_t df11_vocab_loss_scratch_bytes(const df11_vocab_sizes *z) {
-    return bad_sizes(z) ? 0 : LossScratch(nullptr, z->n, z->rows, z->cols).bytes;
+    return bad_sizes(z) ? 0 : LossScratch(nullptr, *z).bytes;
 }
 
-int df11_vocab_loss(const df11_vocab_piece *p, float *losses, float *lse, void *scratch,
-                    uint64_t scratch_bytes, df11_hip_stream stream) {
-    if (bad_piece(p) || !p->vocab) return DF11_E_INVALID;
+int df11_vocab_loss(const df11_vocab_piece *p, float *losses, float *lse, const df11_vocab_sizes *sizes,
+                    void *scratch, uint64_t scratch_bytes, df11_hip_stream stream) {
+    if (bad_piece(p) || !p->vocab || other_sizes(p, sizes)) return DF11_E_INVALID;
     if (!p->n) return DF11_OK;
-    const LossScratch s(scratch, p->n, p->rows, p->cols);
+    const LossScratch s(scratch, *sizes);
     if (!scratch || !aligned(scratch, 256) || scratch_bytes < s.bytes ||
         (p->end && (!losses || !lse || !aligned(losses, 4) || !aligned(lse, 4))))
         return DF11_E_INVALID;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const int tile = tile_for(p->n, p->rows, p->cols);
+    const int tile = s.tile;
     TileArgs a = tile_args();
     a.a = static_cast<const __bf16 *>(p->x), a.b = static_cast<const __bf16 *>(p->w);
     a.a_stride = p->x_stride, a.b_stride = p->w_stride;
@@ -951,8 +957,7 @@ uint64_t df11_vocab_loss_gradient_scratch_bytes(const df11_vocab_sizes *z) {
 int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g,
                              const df11_vocab_sizes *sizes, void *scratch, uint64_t scratch_bytes,
                              df11_hip_stream stream) {
-    if (bad_piece(p) || !p->vocab || !g || bad_sizes(sizes) || sizes->n != p->n || sizes->cols != p->cols ||
-        p->rows > sizes->rows || g->dx_type > DF11_TYPE_BF16 || g->dw_type > DF11_TYPE_BF16 || g->accumulate > 1)
+    if (bad_piece(p) || !p->vocab || !g || other_sizes(p, sizes) || g->dx_type > DF11_TYPE_BF16 || g->dw_type > DF11_TYPE_BF16 || g->accumulate > 1)
         return DF11_E_INVALID;
     const bool has_dx = sizes->dx, has_dw = g->dw;
     const bool few = p->n <= kTwoTermTokens;

@@ -876,7 +876,7 @@ typedef struct df11_vocab_piece {
     uint32_t end;            /* 0 or 1 */
 } df11_vocab_piece;
 
-/* What a scratch is sized for. */
+/* What a scratch is sized for, the same in all calls of a loss or of a gradient. */
 typedef struct df11_vocab_sizes {
     uint32_t n, cols;
     uint32_t rows;           /* of the largest piece */
@@ -885,15 +885,17 @@ typedef struct df11_vocab_sizes {
 } df11_vocab_sizes;
 
 /*
- * losses and lse: device, n floats.  scratch: device, 256-byte aligned, at
- * least df11_vocab_loss_scratch_bytes bytes for the largest piece, not shared
- * by calls that may overlap; no initialisation needed.  Asynchronous.  Outputs
+ * losses and lse: device, n floats.  sizes: n, cols and the rows of the largest
+ * piece.  scratch: device, 256-byte aligned, at least
+ * df11_vocab_loss_scratch_bytes(sizes) bytes, not shared by calls that may
+ * overlap; no initialisation needed.  Asynchronous.  Outputs
  * must not overlap anything.  Errors: DF11_E_INVALID (null or misaligned
  * pointers, sizes, strides, a piece outside the head, the scratch), DF11_E_HIP.
  */
 uint64_t df11_vocab_loss_scratch_bytes(const df11_vocab_sizes *z);
-int df11_vocab_loss(const df11_vocab_piece *p, float *losses, float *lse, void *scratch,
-                    uint64_t scratch_bytes, df11_hip_stream st);
+int df11_vocab_loss(const df11_vocab_piece *p, float *losses, float *lse,
+                    const df11_vocab_sizes *sizes, void *scratch, uint64_t scratch_bytes,
+                    df11_hip_stream st);
 
 /*
  * The gradients of x and of the head for given gradients a of the losses and c
@@ -931,9 +933,9 @@ typedef struct df11_vocab_grad {
 } df11_vocab_grad;
 
 /*
- * sizes: those that the scratch was sized for, the same in all calls of a
- * gradient, as n, cols, x, targets and lse are.  scratch as above, of
- * df11_vocab_loss_gradient_scratch_bytes bytes.  dx and dw need their element's
+ * sizes as above, with dx and two_terms.  x, targets, lse and the factors are the
+ * same in all calls of a gradient.  scratch as above, of
+ * df11_vocab_loss_gradient_scratch_bytes(sizes) bytes.  dx and dw need their element's
  * alignment only, and must not overlap anything.  Deterministic.  Asynchronous.
  * Errors as df11_vocab_loss's.
  */

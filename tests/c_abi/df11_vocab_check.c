@@ -122,7 +122,7 @@ static int on_the_gpu(void) {
             p.w = (const uint16_t *)d_w + (size_t)p.first * COLS;
             v.dw = d_dw + (size_t)p.first * COLS;
             CHECK((pass ? df11_vocab_loss_gradient(&p, &v, &z, scratch, more, NULL)
-                        : df11_vocab_loss(&p, d_losses, d_lse, scratch, bytes, NULL)) == DF11_OK);
+                        : df11_vocab_loss(&p, d_losses, d_lse, &z, scratch, bytes, NULL)) == DF11_OK);
         }
     download(losses, d_losses, sizeof losses);
     download(lse, d_lse, sizeof lse);
@@ -167,14 +167,14 @@ int main(void) {
     /* nothing to do */
     CHECK(df11_embedding(&e, NULL) == DF11_OK);
     CHECK(df11_embedding_gradient(&g, NULL, 0, NULL) == DF11_OK);
-    CHECK(df11_vocab_loss(&p, NULL, NULL, NULL, 0, NULL) == DF11_OK);
+    CHECK(df11_vocab_loss(&p, NULL, NULL, &z, NULL, 0, NULL) == DF11_OK);
     /* refused */
     e.n = e.rows = TOKENS, e.cols = COLS;
     CHECK(df11_embedding(&e, NULL) == DF11_E_INVALID);
     g.rows = ROWS, g.cols = COLS;
     CHECK(df11_embedding_gradient(&g, NULL, 0, NULL) == DF11_E_INVALID);
     p.n = TOKENS;
-    CHECK(df11_vocab_loss(&p, NULL, NULL, NULL, 0, NULL) == DF11_E_INVALID);
+    CHECK(df11_vocab_loss(&p, NULL, NULL, NULL, NULL, 0, NULL) == DF11_E_INVALID);
     CHECK(df11_vocab_loss_gradient(&p, &v, &z, NULL, 0, NULL) == DF11_E_INVALID);
     z.n = DF11_VOCAB_MAX_TOKENS + 1;
     CHECK(df11_vocab_loss_scratch_bytes(&z) == 0 && df11_vocab_loss_gradient_scratch_bytes(&z) == 0);

@@ -179,6 +179,23 @@ def test_pieces(n, rows, cols, pieces):
     check_all(n, rows, cols, seed=n, pieces=pieces, dx=F32)
 
 
+@pytest.mark.parametrize("sizes", [[70_000, 40_000], [33_000, 1, 32_000], [5, 0, 300]])
+@pytest.mark.parametrize("n", [1, 30])
+def test_pieces_of_unlike_sizes(n, sizes):
+    """Smaller pieces, for which another tile would be the faster one, fit where the
+    largest does."""
+    say(f"[gpu] pieces of {sizes} rows, {n} tokens")
+    x, w, targets = inputs(n, sum(sizes), 8, n)
+    head, e = ed.VocabLoss(list(w.split(sizes))), Exact(x, w, targets)
+    losses, lse = head(x, targets)
+    check(lse, e.lse, e.off_lse, "lse")
+    check(losses, e.loss, e.off_loss, "loss")
+    dx, dws = head.gradient(x, targets, lse, 0.5, dx_dtype=F32, losses=losses)
+    g, off = e.gradient(0.5, 0.0, 2, True)
+    check(dx, *e.dx(g, off, F32), "dx")
+    check(torch.cat(dws), *e.dw(g, off, BF16), "dw")
+
+
 def test_long_vocabulary_in_chunks():
     """g in several chunks of the vocabulary, with one and with two terms."""
     say("[gpu] g in several chunks")

@@ -23,11 +23,14 @@ BAD_PIECES = [
     {"n": (1 << 20) + 1}, {"begin": 2}, {"end": 2}]
 
 
-def loss(losses=32768, lse=65536, scratch=1 << 20, nbytes=None, **change):
+def loss(losses=32768, lse=65536, scratch=1 << 20, nbytes=None, sizes=None, **change):
     p = ed.df11_vocab_piece(**{**PIECE, **change})
+    z = ed.df11_vocab_sizes(p.n, p.cols, p.rows, 0, 0)
+    for k, v in (sizes or {}).items():
+        setattr(z, k, v)
     if nbytes is None:
-        nbytes = L.df11_vocab_loss_scratch_bytes(ed.df11_vocab_sizes(p.n, p.cols, p.rows, 0, 0))
-    return L.df11_vocab_loss(p, losses, lse, scratch, nbytes, None)
+        nbytes = L.df11_vocab_loss_scratch_bytes(z)
+    return L.df11_vocab_loss(p, losses, lse, z, scratch, nbytes, None)
 
 
 def gradient(scratch=1 << 20, nbytes=None, sizes=None, grad=None, **change):
@@ -44,7 +47,7 @@ def gradient(scratch=1 << 20, nbytes=None, sizes=None, grad=None, **change):
 
 @pytest.mark.parametrize("change", BAD_PIECES + [
     {"losses": 0}, {"losses": 32770}, {"lse": 0}, {"lse": 65537}, {"scratch": 0}, {"scratch": (1 << 20) + 128},
-    {"nbytes": 100}])
+    {"nbytes": 100}, {"sizes": {"n": 4}}, {"sizes": {"cols": 72}}, {"sizes": {"rows": 59}}])
 def test_loss_refuses(change):
     assert loss(**change) == ed.DF11_E_INVALID
 
@@ -63,7 +66,7 @@ def test_gradient_refuses(change):
 
 
 def test_nothing_to_do():
-    assert L.df11_vocab_loss(None, 4096, 4096, 1 << 20, 1 << 20, None) == ed.DF11_E_INVALID
+    assert L.df11_vocab_loss(None, 4096, 4096, None, 1 << 20, 1 << 20, None) == ed.DF11_E_INVALID
     assert loss(n=0, x=0, targets=0) == ed.DF11_OK
     assert L.df11_vocab_loss_gradient(None, None, None, 1 << 20, 1 << 20, None) == ed.DF11_E_INVALID
     assert gradient(cols=0, x=0, w=0) == ed.DF11_OK
@@ -85,6 +88,7 @@ def test_scratch_bytes():
         assert f(bad) == g(bad) == 0
     assert 0 < f(z(1, 64, 100, 0, 0)) <= f(z(100, 64, 100, 0, 0)) <= f(z(100, 64, 9000, 0, 0))
     assert 0 < g(z(100, 64, 9000, 0, 0)) < g(z(100, 64, 9000, 1, 0)) < g(z(100, 64, 9000, 1, 1))
+    assert g(z(100, 64, 0, 1, 1)) < 2 ** 18  # no rows: room for one chunk of 256
     # g takes 2^29 elements at most, or 256 rows: not the logits' memory
     assert g(z(8192, 4096, 1 << 24, 1, 0)) < 2 ** 30 + 8192 * 4096 * 4 * 2 + 2 ** 20
     assert g(z(1 << 20, 8, 1 << 24, 0, 0)) < 2 ** 30 + 2 ** 20 * 200
