@@ -123,3 +123,63 @@ def test_two_calls_of_one_head_at_once():
         torch.cuda.synchronize()
         for (lse, (dx, (dw,))), (lse2, (dx2, (dw2,))) in zip(got, wants):
             assert torch.equal(lse, lse2) and torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+def test_captured_on_a_stream_that_the_calls_name():
+    say("[gpu] lookup, loss and gradients captured on a named stream")
+    table = (randn(900, 136) / 10).to(BF16)
+    emb, head = ed.Embedding(table), ed.VocabLoss([table])
+    stream = torch.cuda.Stream()
+    tokens = torch.randint(0, 900, (3001,), device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    grad = torch.zeros(900, 136, device="cuda")
+
+    def step(at):
+        x = emb(tokens[:-1], stream=at)
+        losses, lse = head(x, tokens[1:], stream=at)
+        dx, _ = head.gradient(x, tokens[1:], lse, 0.01, losses=losses, dws=[grad], accumulate=True, stream=at)
+        emb.gradient(tokens[:-1], dx, out=grad, accumulate=True, stream=at)
+        return losses, dx
+
+    stream.wait_stream(torch.cuda.current_stream())
+    step(stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        losses, dx = step(stream)
+    for turn in range(3):
+        tokens.copy_(torch.randint(0, 900, (3001,), device="cuda"))
+        grad.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = losses.clone(), dx.clone(), grad.clone()
+        grad.zero_()
+        want = *step(None), grad
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_freed_while_another_stream_uses_them():
+    """The head, the table and what the calls are given are dropped at once, with the
+    stream still busy: new tensors must not lie there."""
+    say("[gpu] table and head dropped while a busy stream uses them")
+    from test_gpu_lifetimes import busy, refill
+
+    table = (randn(3000, 264) / 10).to(BF16)
+    tokens = torch.randint(0, 3000, (601,), device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    want = ed.VocabLoss([table])(ed.Embedding(table)(tokens[:-1]), tokens[1:])[0]
+    used = [table.clone(), tokens.clone(), torch.zeros(600, 264, dtype=BF16, device="cuda")]
+    emb, head = ed.Embedding(used[0]), ed.VocabLoss([used[0]])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    held = busy(side)
+    emb(used[1][:-1], out=used[2], stream=side)
+    losses, _ = head(used[2], used[1][1:], stream=side)
+    at = {t.data_ptr() for t in used}
+    sizes = [t.numel() * t.element_size() for t in used]
+    del emb, head, used
+    others, places = refill(sizes, torch.uint8)
+    assert not at & places
+    torch.cuda.synchronize()
+    assert torch.equal(losses, want)
+    del held, others
