@@ -1677,12 +1677,14 @@ class VocabLoss(_Lender):
 
     def _each(self, p, status, st):
         """Sets p to each piece in turn, decompressed where it has to be."""
+        if self.pieces is not None and len(self.shapes) == 1:  # p is this one already
+            p.w, p.w_stride = self._held[0]
+            return 0,
+        return self._in_turn(p, status, st)
+
+    def _in_turn(self, p, status, st):
         import torch
 
-        if len(self.shapes) == 1 and self.pieces is not None:  # p is this one already
-            p.w, p.w_stride = self._held[0]
-            yield 0
-            return
         slot = None
         if self.pieces is None:
             slot = torch.empty(self._rows * self.cols, dtype=torch.bfloat16, device=self.device)
@@ -1739,10 +1741,9 @@ class VocabLoss(_Lender):
                 held = self._bytes[p.n] = sizes, LIB.df11_vocab_loss_scratch_bytes(sizes)
             sizes, need = held
             scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
+            given_to = losses.data_ptr(), lse.data_ptr(), sizes, scratch.data_ptr(), need, st
             for _ in self._each(p, status, st):
-                _check("df11_vocab_loss",
-                       LIB.df11_vocab_loss(p, losses.data_ptr(), lse.data_ptr(), sizes, scratch.data_ptr(),
-                                           need, st))
+                _check("df11_vocab_loss", LIB.df11_vocab_loss(p, *given_to))
         if stream is not None or st not in self._lent:
             self._used(stream, st, [x, given, losses, lse] + ([] if status is None else [status]))
         return losses, lse

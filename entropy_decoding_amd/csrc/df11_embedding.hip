@@ -257,10 +257,12 @@ __device__ __forceinline__ void clear_rows(const GradArgs &a, uint32_t wave, uin
 // BIG: what would fill the caches passes them by.  With ADD that is dy (32768
 // tokens of 8192 columns, added to float32: 285 -> 262 us for the three launches),
 // otherwise dw, which leaves dy there (8192 tokens, 128256 x 4096 in BF16: 241 ->
-// 212 us; with dy read past the caches as well 240).
+// 212 us; with dy read past the caches as well 240), if of 2 bytes an element: a
+// lane stores 8 float32 in two halves, which the caches have to bring together (the
+// same in float32: 448 us, past the caches 1000).
 template <class X, class Y, bool ADD, bool BIG>
 __global__ __launch_bounds__(256) void sum_runs(GradArgs a) {
-    constexpr bool PAST = BIG && !ADD, ONCE = BIG && ADD;
+    constexpr bool PAST = BIG && !ADD && sizeof(Y) == 2, ONCE = BIG && ADD;
     const uint32_t lane = threadIdx.x & 63u;
     if (!ADD && blockIdx.x >= a.summing)
         return clear_rows<Y, PAST>(a, uniform((blockIdx.x - a.summing) * 4 + (threadIdx.x >> 6)), lane);
