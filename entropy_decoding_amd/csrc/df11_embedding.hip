@@ -239,13 +239,35 @@ __device__ __forceinline__ void finish(const GradArgs &a, uint32_t row, uint32_t
     finish<Y, ADD>(a, row, c, sum, old);
 }
 
+// Clears a wave's 512 columns of a row, `first` and on.
+template <class Y, bool PAST>
+__device__ __forceinline__ void clear_row(Y *dw, uint32_t first, uint32_t lane, uint32_t cols) {
+    if constexpr (sizeof(Y) == 2) {
+        store_group<Y, PAST>(dw, first + lane * 8, cols, f32x8(0.0f));
+    } else {
+        // two halves, each in whole lines, so that these can pass the caches
+        typedef f32x4 any __attribute__((aligned(4)));
+#pragma unroll
+        for (uint32_t half = 0; half < 2; half++) {
+            const uint32_t c = first + half * 256 + lane * 4;
+            if (c + 4 <= cols) {
+                if (PAST) __builtin_nontemporal_store(any(0.0f), reinterpret_cast<any *>(dw + c));
+                else *reinterpret_cast<any *>(dw + c) = any(0.0f);
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < 3; e++)
+                    if (c + e < cols) dw[c + e] = Y(0.0f);
+            }
+        }
+    }
+}
+
 // Clears the rows without a token among 64 rows, 512 columns of them.
 template <class Y, bool PAST>
 __device__ __forceinline__ void clear_rows(const GradArgs &a, uint32_t wave, uint32_t lane) {
-    const uint32_t first = wave / a.parts * 64, c = wave % a.parts * 512 + lane * 8;
-    const uint32_t row = first + lane;
+    const uint32_t first = wave / a.parts * 64, row = first + lane;
     for (uint64_t none = __ballot(row < a.rows && a.total[min(row, a.rows - 1)] == 0); none; none &= none - 1)
-        store_group<Y, PAST>(row_of_dw<Y>(a, first + __builtin_ctzll(none)), c, a.cols, f32x8(0.0f));
+        clear_row<Y, PAST>(row_of_dw<Y>(a, first + __builtin_ctzll(none)), wave % a.parts * 512, lane, a.cols);
 }
 
 // Sums the runs of equal rows, a wave for 512 columns of a chunk of sorted tokens:
@@ -259,13 +281,14 @@ __device__ __forceinline__ void clear_rows(const GradArgs &a, uint32_t wave, uin
 // otherwise dw, which leaves dy there (8192 tokens, 128256 x 4096 in BF16: 241 ->
 // 212 us; with dy read past the caches as well 240), if of 2 bytes an element: a
 // lane stores 8 float32 in two halves, which the caches have to bring together (the
-// same in float32: 448 us, past the caches 1000).
+// same in float32: 448 us, past the caches 1000); cleared rows are stored otherwise
+// (402 us).
 template <class X, class Y, bool ADD, bool BIG>
 __global__ __launch_bounds__(256) void sum_runs(GradArgs a) {
     constexpr bool PAST = BIG && !ADD && sizeof(Y) == 2, ONCE = BIG && ADD;
     const uint32_t lane = threadIdx.x & 63u;
     if (!ADD && blockIdx.x >= a.summing)
-        return clear_rows<Y, PAST>(a, uniform((blockIdx.x - a.summing) * 4 + (threadIdx.x >> 6)), lane);
+        return clear_rows<Y, BIG>(a, uniform((blockIdx.x - a.summing) * 4 + (threadIdx.x >> 6)), lane);
     const uint32_t wave = uniform(blockIdx.x * 4 + (threadIdx.x >> 6));
     const uint32_t chunk = wave / a.parts, c = wave % a.parts * 512 + lane * 8;
     const uint32_t kept = *a.kept, begin = chunk * a.chunk;
@@ -427,7 +450,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void sum_few(GradArgs a) {
         const uint32_t from = uniform(r ? end[r - 1] : 0), n = uniform(end[r]) - from;
         if (n == 0) {
             if (!ADD)
-                store_group<Y>(row_of_dw<Y>(a, base + r), c, a.cols, f32x8(0.0f));
+                clear_row<Y, false>(row_of_dw<Y>(a, base + r), c - lane * 8, lane, a.cols);
         } else if (n <= kMany) {
             finish<Y, ADD>(a, base + r, c, sum_listed<X>(a, list + from, n, c));
         } else {
@@ -491,10 +514,13 @@ uint32_t few_run_of(uint32_t rows, uint32_t parts) {
 
 uint64_t padded(uint64_t n) { return (n + 31) / 32 * 32; }
 
-// sum_few's calls (a grid of its workgroups holds less than 2^32 threads)
-bool is_few(uint64_t n, uint64_t rows, uint32_t cols) {
+// sum_few's calls: a grid of its workgroups holds less than 2^32 threads, and a table
+// of 2^26 elements and more is cleared faster beside sum_runs (1000 tokens, 128256 x
+// 4096 in float32: 521 us against 400).
+bool is_few(uint64_t n, uint64_t rows, uint32_t cols, bool add) {
     const uint32_t parts = (cols + 511) / 512;
-    return n <= kFew && (rows + kFewRows - 1) / kFewRows * parts < (1u << 23) - 1;
+    return n <= kFew && (add || rows * cols < 1ull << 26) &&
+           (rows + kFewRows - 1) / kFewRows * parts < (1u << 23) - 1;
 }
 
 }  // namespace
@@ -529,7 +555,7 @@ int df11_embedding(const df11_embedding_lookup *e, df11_hip_stream stream) {
 
 uint64_t df11_embedding_gradient_scratch_bytes(uint64_t n, uint64_t rows, uint32_t cols) {
     if (n > DF11_EMBEDDING_MAX_TOKENS || rows > DF11_EMBEDDING_MAX_ROWS || cols > DF11_EMBEDDING_MAX_COLS) return 0;
-    if (is_few(n, rows, cols)) return 0;
+    if (is_few(n, rows, cols, false)) return 0;  // those that add need it less often
     const uint32_t chunk = chunk_of(uint32_t(n));
     return 128 + 16 * padded(n) + 4 * padded(rows) + (n + chunk - 1) / chunk * 2 * 4 * padded(cols);
 }
@@ -541,7 +567,8 @@ int df11_embedding_gradient(const df11_embedding_grad *g, void *scratch, uint64_
         bad_matrix(g->dy, g->dy_type, g->dy_stride, g->n, g->cols) ||
         bad_output(g->dw, g->dw_type, g->dw_stride, g->rows, g->cols))
         return DF11_E_INVALID;
-    const uint64_t need = df11_embedding_gradient_scratch_bytes(g->n, g->rows, g->cols);
+    const bool few = is_few(g->n, g->rows, g->cols, g->accumulate);
+    const uint64_t need = few ? 0 : df11_embedding_gradient_scratch_bytes(g->n, g->rows, g->cols);
     if (need && (!scratch || !aligned(scratch, 128) || scratch_bytes < need)) return DF11_E_INVALID;
     if (!g->rows || !g->cols || (!g->n && g->accumulate)) return DF11_OK;
     GradArgs a{};
@@ -559,7 +586,7 @@ int df11_embedding_gradient(const df11_embedding_grad *g, void *scratch, uint64_
             });
         });
     };
-    if (is_few(g->n, g->rows, g->cols)) {
+    if (few) {
         a.run = few_run_of(a.rows, a.parts);
         a.span = uint32_t((g->n + 64 * kFewWaves - 1) / (64 * kFewWaves) * 64);
         const dim3 grid((a.rows + a.run - 1) / a.run * a.parts);
@@ -600,7 +627,7 @@ int df11_embedding_gradient(const df11_embedding_grad *g, void *scratch, uint64_
         return big ? launch(sum_runs<X, Y, false, true>, both, dim3(256), 0, st, a)
                    : launch(sum_runs<X, Y, false, false>, both, dim3(256), 0, st, a);
     });
-    if (rc != DF11_OK) return rc;
+    if (rc != DF11_OK || !joining) return rc;
     return with_type(g->dw_type, [&](auto y) {
         using Y = decltype(y);
         return status(g->accumulate ? launch(join_runs<Y, true>, dim3(uint32_t(joining)), dim3(256), 0, st, a)

@@ -813,7 +813,8 @@ int df11_embedding(const df11_embedding_lookup *e, df11_hip_stream st);
  * scratch: device, 128-byte aligned, at least
  * df11_embedding_gradient_scratch_bytes(n, rows, cols) bytes, not shared by calls
  * that may overlap; no initialisation needed.  Three launches on st; up to 2048
- * tokens take one, and no scratch (0 bytes; it may be null then).  Asynchronous.  Errors as df11_embedding's, and
+ * tokens that are added, or of a table of less than 2^26 elements, take one, and no
+ * scratch (it may be null then).  Asynchronous.  Errors as df11_embedding's, and
  * DF11_E_INVALID for accumulate and the scratch.
  */
 typedef struct df11_embedding_grad {

@@ -67,7 +67,9 @@ def test_gradient_of_nothing():
 def test_scratch_bytes():
     f = L.df11_embedding_gradient_scratch_bytes
     assert f((1 << 24) + 1, 8, 8) == f(3000, (1 << 24) + 1, 8) == f(3000, 8, (1 << 20) + 1) == 0
-    assert f(2048, 128_256, 4096) == 0 < f(2049, 128_256, 4096)
+    assert f(2048, 16_383, 4096) == 0 < f(2049, 16_383, 4096)
+    assert f(1, 16_384, 4096) > 0  # 2^26 elements
+    assert gradient(n=0, tokens=0, dy=0, rows=1 << 24, accumulate=1, scratch=0, nbytes=0) == ed.DF11_OK
     assert f(3000, 8, 8) < f(100_000, 8, 8) < f(100_000, 1 << 20, 8) < f(100_000, 1 << 20, 80)
     assert f(8, 1 << 24, 1 << 20) > 0  # more workgroups than a grid holds: three launches
 

@@ -161,6 +161,22 @@ def test_gradient_of_one_row(n, rows):
     check_gradient(ed.embedding_gradient(tokens, dy, rows), tokens, dy, rows)
 
 
+@pytest.mark.parametrize("kind", [F32, BF16])
+@pytest.mark.parametrize("n", [1, 40, 3000])
+def test_gradient_of_a_large_table(kind, n):
+    """2^26 elements and more: rows that no token meets are cleared past the caches."""
+    say(f"[gpu] gradient of a large table, {n} tokens, {kind}")
+    rows, cols = 66_000, 1033
+    tokens, dy = some_tokens(n, rows, n), randn(n, cols, seed=n)
+    got = torch.full((rows, cols + 5), 7.0, dtype=kind, device="cuda")
+    ed.embedding_gradient(tokens, dy, rows, out=got[:, 2:cols + 2])
+    check_gradient(got[:, 2:cols + 2], tokens, dy, rows)
+    assert (got[:, :2] == 7).all() and (got[:, cols + 2:] == 7).all()
+    added = torch.zeros(rows, cols, device="cuda")
+    ed.embedding_gradient(tokens, dy, rows, out=added, accumulate=True)
+    check_gradient(added, tokens, dy, rows)
+
+
 def test_gradient_of_runs_that_end_with_chunks():
     """Runs of 1 to 128 tokens, each length at many offsets of a chunk of 32."""
     say("[gpu] gradient of runs at chunk borders")
@@ -219,6 +235,8 @@ def test_gradient_of_no_tokens():
     say("[gpu] gradient of no tokens")
     none = torch.zeros(0, dtype=torch.int64, device="cuda")
     assert not ed.embedding_gradient(none, torch.zeros(0, 40, device="cuda"), 30).any()
+    large = torch.ones(66_000, 1033, device="cuda")  # three launches otherwise
+    assert not ed.embedding_gradient(none, torch.zeros(0, 1033, device="cuda"), 66_000, out=large).any()
     dw = torch.ones(30, 40, device="cuda")
     ed.embedding_gradient(none, torch.zeros(0, 40, device="cuda"), 30, out=dw, accumulate=True)
     assert (dw == 1).all()
