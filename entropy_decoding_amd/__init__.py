@@ -1559,11 +1559,13 @@ class Embedding(_Lender):
         a.out_type = _type(out_dtype)
         guard, st = _on(self.device, stream)
         with guard:
-            given, tokens = tokens, tokens.contiguous()
-            if out is None:
+            given, tokens, made = tokens, tokens.contiguous(), out is None
+            if made:
                 out, a.out_stride = torch.empty(*tokens.shape, a.cols, dtype=out_dtype, device=self.device), a.cols
             a.tokens, a.out = tokens.data_ptr(), out.data_ptr()
             _check("df11_embedding", LIB.df11_embedding(a, st))
+        if not made:
+            torch._C._increment_version([out])
         if st not in self._lent:
             self._lend(stream, st)
         if stream is not None:

@@ -780,7 +780,16 @@ __global__ __launch_bounds__(256) void spread(TokenArgs a) {
     f32x8 sum = 0.0f;
     if (at != 0xFFFFFFFFu) {
         const float *from = a.sums + at * uint64_t(a.cols) + c;
-        for (uint32_t k = 0; k < a.splits; k++) sum += *reinterpret_cast<const f32x8 *>(from + k * a.sums_split);
+        constexpr uint32_t kLoads = 8;
+        for (uint32_t k = 0; k < a.splits; k += kLoads) {
+            f32x8 v[kLoads];
+#pragma unroll
+            for (uint32_t u = 0; u < kLoads; u++)
+                v[u] = *reinterpret_cast<const f32x8 *>(from + min(k + u, a.splits - 1) * a.sums_split);
+#pragma unroll
+            for (uint32_t u = 0; u < kLoads; u++)
+                if (k + u < a.splits) sum += v[u];
+        }
     }
     store_group<Y>(static_cast<Y *>(a.dx) + t * a.dx_stride, c, a.cols, sum);
 }
