@@ -1502,6 +1502,17 @@ def _rows_apart(t, what, device=None):
     return t.stride(0) if t.size(0) > 1 else t.size(1)
 
 
+def _flat(t, n, what, device, stream):
+    """[*, cols] as [n, cols]; where no one stride reaches all rows (a batch without
+    each sequence's last token), a copy, made on the call's stream."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{what} must be a device tensor on {device}")
+    if t.size(-1) > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    with _on(device, stream)[0]:
+        return t.reshape(n, t.size(-1))
+
+
 def _output(t, what, shape, dtype, device):
     """Checks a given output: rows that lie apart, of the shape and type; returns its row stride."""
     stride = _rows_apart(t, what, device)
@@ -1700,7 +1711,7 @@ class VocabLoss(_Lender):
                 p.w, p.w_stride = slot.data_ptr(), cols
             yield k
 
-    def _piece(self, x, targets, ignore_index):
+    def _piece(self, x, targets, ignore_index, stream):
         """x as [n, cols], and what all pieces of a call share."""
         import torch
 
@@ -1709,7 +1720,7 @@ class VocabLoss(_Lender):
         if x.dim() != 2:
             if x.dim() < 1 or x.shape[:-1] != targets.shape:
                 raise ValueError("hidden states must be [*targets.shape, cols]")
-            x = x.view(targets.numel(), x.size(-1))
+            x = _flat(x, targets.numel(), "hidden states", self.device, stream)
         stride = _rows_apart(x, "hidden states", self.device)
         if x.shape != (targets.numel(), self.cols):
             raise ValueError("hidden states must be [number of targets, cols]")
@@ -1721,7 +1732,9 @@ class VocabLoss(_Lender):
     def __call__(self, x, targets, ignore_index: int = -100, status=None, stream=None):
         """(losses, lse), float32 like ``targets`` (int32 or int64): the cross entropy
         of each token, and the logarithm of its sum of exponentials.  ``x``: BF16
-        hidden states [*targets.shape, cols] or [number of targets, cols].  A target
+        hidden states [*targets.shape, cols] or [number of targets, cols], contiguous
+        rows; those of a batch that no one stride reaches (``x[:, :-1]`` of several
+        sequences) are copied first.  A target
         of ``ignore_index`` has loss 0, another one outside the vocabulary NaN.
         ``status``: for a compressed head, as in df11_decompress_tensor.  The call
         records no graph: hidden states that require a gradient are refused (detach
@@ -1730,10 +1743,10 @@ class VocabLoss(_Lender):
 
         if x.requires_grad and torch.is_grad_enabled():
             raise RuntimeError("a loss records no gradient for its hidden states: detach them")
-        x, p = self._piece(x, targets, ignore_index)
+        used, (x, p) = [x, targets], self._piece(x, targets, ignore_index, stream)
         guard, st = _on(self.device, stream)
         with guard:
-            given, targets = targets, targets.contiguous()
+            targets = targets.contiguous()
             p.targets = targets.data_ptr()
             losses = torch.empty(targets.shape, dtype=torch.float32, device=self.device)
             lse = torch.empty_like(losses)
@@ -1747,7 +1760,7 @@ class VocabLoss(_Lender):
             for _ in self._each(p, status, st):
                 _check("df11_vocab_loss", LIB.df11_vocab_loss(p, *given_to))
         if stream is not None or st not in self._lent:
-            self._used(stream, st, [x, given, losses, lse] + ([] if status is None else [status]))
+            self._used(stream, st, used + [losses, lse] + ([] if status is None else [status]))
         return losses, lse
 
     def _used(self, stream, st, tensors):
@@ -1771,9 +1784,8 @@ class VocabLoss(_Lender):
         one is None."""
         import torch
 
-        x, p = self._piece(x, targets, ignore_index)
-        n, cols = p.n, p.cols
-        g, used = df11_vocab_grad(), [x, targets, lse]
+        used, (x, p) = [x, targets, lse], self._piece(x, targets, ignore_index, stream)
+        n, cols, g = p.n, p.cols, df11_vocab_grad()
         g.accumulate = bool(accumulate)
         g.lse = self._per_token("lse", lse, (n,))
         if losses is not None:

@@ -1,0 +1,41 @@
+"""GPU tests of calls of the embedding and the vocabulary loss as programs make
+them: batches of several sequences, each without its first or last token."""
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import entropy_decoding_amd as ed  # noqa: E402
+from test_gpu_vocab_loss import F32, inputs, say  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    torch.cuda.init()
+    yield
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_loss_of_a_batch_without_its_last_tokens(side):
+    """The same bits as of the rows laid out one behind the other; on a named stream
+    also where the batch is dropped at once."""
+    say(f"[gpu] loss of a cut batch, on a stream of its own: {side}")
+    x, w, targets = inputs(8 * 65, 700, 136, 3)
+    x, targets = x.view(8, 65, 136), targets.view(8, 65)
+    head, stream = ed.VocabLoss([w]), torch.cuda.Stream() if side else None
+    flat, at = x[:, :-1].reshape(-1, 136), targets[:, 1:].reshape(-1)
+    want, want_lse = head(flat, at)
+    want_dx, (want_dw,) = head.gradient(flat, at, want_lse, 0.1, dw_dtype=F32)
+    if side:
+        stream.wait_stream(torch.cuda.current_stream())
+    losses, lse = head(x[:, :-1], targets[:, 1:], stream=stream)
+    dx, (dw,) = head.gradient(x[:, :-1], targets[:, 1:], lse, 0.1, dw_dtype=F32, stream=stream)
+    del x, targets
+    torch.full((8, 65, 136), 9.0, dtype=torch.bfloat16, device="cuda"), torch.full((8, 65), 9, device="cuda")
+    torch.cuda.synchronize()
+    assert losses.shape == (8, 64) and torch.equal(losses.view(-1), want) and torch.equal(lse.view(-1), want_lse)
+    assert torch.equal(dx, want_dx) and torch.equal(dw, want_dw)

@@ -1,0 +1,69 @@
+"""Calls of the embedding and the vocabulary loss as programs make them, with the
+stand-ins of test_lending.py for the library, the streams and the device: what
+is passed on to the library is what the tensors hold."""
+
+import ctypes
+
+import pytest
+
+import entropy_decoding_amd as ed
+
+torch = pytest.importorskip("torch")
+
+from test_lending import gpu  # noqa: E402,F401
+
+BF16 = torch.bfloat16
+
+
+def rows_at(address, stride, rows, cols, kind):
+    """The rows that a call was given."""
+    bits = {BF16: (ctypes.c_int16, torch.int16), torch.float32: (ctypes.c_float, torch.float32)}[kind]
+    held = (bits[0] * (stride * (rows - 1) + cols)).from_address(address)
+    return torch.frombuffer(held, dtype=bits[1]).view(kind).as_strided((rows, cols), (stride, 1)).clone()
+
+
+@pytest.fixture
+def seen(gpu, monkeypatch):  # noqa: F811
+    """What the library's loss functions are given: (function, stream entered, rows of x)."""
+    got = []
+
+    def piece(name):
+        def call(p, *_):
+            got.append((name, gpu.inside, rows_at(p.x, p.x_stride, p.n, p.cols, BF16)))
+            return ed.DF11_OK
+        return call
+
+    for name in ("df11_vocab_loss", "df11_vocab_loss_gradient"):
+        monkeypatch.setattr(gpu.lib, name, piece(name), raising=False)
+    return got
+
+
+@pytest.mark.parametrize("stream", [None, 7])
+def test_loss_of_a_batch_without_its_last_tokens(gpu, seen, stream):  # noqa: F811
+    """Hidden states of several sequences, each without its last: no one stride
+    reaches their rows."""
+    head = ed.VocabLoss([torch.zeros(6, 16, dtype=BF16)])
+    x = torch.randn(3, 5, 16).to(BF16)
+    tokens = torch.zeros(3, 5, dtype=torch.int64)
+    for part in (x[:, :-1], x[:, 1:], x.transpose(0, 1)[:4].transpose(0, 1)):
+        seen.clear()
+        gpu.lent.clear()
+        losses, lse = head(part, tokens[:, 1:], stream=stream)
+        assert losses.shape == lse.shape == (3, 4)
+        dx, _ = head.gradient(part, tokens[:, 1:], lse, stream=stream)
+        assert dx.shape == (12, 16)
+        assert [s[0] for s in seen] == ["df11_vocab_loss", "df11_vocab_loss_gradient"]
+        assert all(s[1] == (stream or gpu.current) and torch.equal(s[2], part.reshape(12, 16)) for s in seen)
+        assert ((part.data_ptr(), 7) in gpu.lent) == (stream == 7)
+
+
+def test_hidden_states_that_are_refused(gpu, seen):  # noqa: F811
+    head, tokens = ed.VocabLoss([torch.zeros(6, 16, dtype=BF16)]), torch.zeros(3, 4, dtype=torch.int64)
+    x = torch.zeros(3, 16, 4, dtype=BF16)
+    for bad in (x.transpose(1, 2), torch.zeros(3, 4, 32, dtype=BF16)[:, :, ::2], torch.zeros(3, 5, 16, dtype=BF16),
+                torch.zeros(4, 3, 16, dtype=BF16), torch.zeros(3, 4, 24, dtype=BF16)):
+        with pytest.raises(ValueError):
+            head(bad, tokens)
+        with pytest.raises(ValueError):
+            head.gradient(bad, tokens, torch.zeros(3, 4))
+    assert not seen
