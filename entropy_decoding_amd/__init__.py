@@ -1599,15 +1599,16 @@ def embedding_gradient(tokens, dy, rows: int, dtype=None, out=None, accumulate: 
     ``tokens`` (int32 or int64, any shape) has the output gradient ``dy``
     [*tokens.shape, cols] or [number of tokens, cols] (BF16, F16 or float32), as
     a new tensor of ``dtype`` (dy's by default), or written into ``out``, or with
-    ``accumulate`` added to it.  Tokens equal to ``padding_idx``, and tokens
-    outside the table, add nothing.  Deterministic."""
+    ``accumulate`` added to it.  dy's rows are contiguous; those that no one stride
+    reaches (``dy[:, 1:]`` of several sequences) are copied first.  Tokens equal to
+    ``padding_idx``, and tokens outside the table, add nothing.  Deterministic."""
     import torch
 
-    device = dy.device
+    device, used = dy.device, [tokens, dy]
     if dy.dim() != 2:
-        if dy.dim() < 2 or tuple(dy.shape[:-1]) != tuple(tokens.shape):
+        if dy.dim() < 1 or dy.shape[:-1] != tokens.shape:
             raise ValueError("dy must be [number of tokens, cols]")
-        dy = dy.view(tokens.numel(), dy.size(-1))
+        dy = _flat(dy, tokens.numel(), "dy", device, stream)
     g = df11_embedding_grad(dy_stride=_rows_apart(dy, "dy", device), rows=rows, n=tokens.numel(),
                             padding=-1 if padding_idx is None else padding_idx, cols=dy.size(1),
                             dy_type=_type(dy.dtype), token_bits=_token_bits(tokens, device),
@@ -1622,8 +1623,7 @@ def embedding_gradient(tokens, dy, rows: int, dtype=None, out=None, accumulate: 
         raise ValueError("accumulate adds to out")
     guard, st = _on(device, stream)
     with guard:
-        given, tokens = tokens, tokens.contiguous()
-        made = out is None
+        tokens, made = tokens.contiguous(), out is None
         if made:
             out, g.dw_stride = torch.empty(rows, g.cols, dtype=dtype or dy.dtype, device=device), g.cols
         g.dw_type = _type(out.dtype)
@@ -1635,7 +1635,7 @@ def embedding_gradient(tokens, dy, rows: int, dtype=None, out=None, accumulate: 
     if not made:
         torch._C._increment_version([out])
     if stream is not None:
-        _lend(device, stream, [given, dy, out])
+        _lend(device, stream, used + [out])
     return out
 
 

@@ -8,7 +8,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 import entropy_decoding_amd as ed  # noqa: E402
-from test_gpu_vocab_loss import F32, inputs, say  # noqa: E402
+from test_gpu_vocab_loss import F32, inputs, randn, say  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -39,3 +39,22 @@ def test_loss_of_a_batch_without_its_last_tokens(side):
     torch.cuda.synchronize()
     assert losses.shape == (8, 64) and torch.equal(losses.view(-1), want) and torch.equal(lse.view(-1), want_lse)
     assert torch.equal(dx, want_dx) and torch.equal(dw, want_dw)
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_table_gradient_of_a_cut_batch(side):
+    """The same bits as of the rows laid out one behind the other, and of one token's
+    gradient, whose lookup gives a single row."""
+    say(f"[gpu] table gradient of a cut batch, on a stream of its own: {side}")
+    table, tokens = randn(300, 136, seed=1), torch.randint(0, 300, (8, 65), device="cuda")
+    emb, dy, stream = ed.Embedding(table, scale=1.5), randn(8, 65, 136, seed=2), torch.cuda.Stream() if side else None
+    want = emb.gradient(tokens[:, 1:].reshape(-1), dy[:, 1:].reshape(-1, 136))
+    one = emb.gradient(tokens[2, 3].view(1), dy[2, 3].view(1, 136))
+    if side:
+        stream.wait_stream(torch.cuda.current_stream())
+    got = emb.gradient(tokens[:, 1:], dy[:, 1:], stream=stream)
+    got_one = emb.gradient(tokens[2, 3], dy[2, 3], stream=stream)
+    del tokens, dy
+    torch.full((8, 65, 136), 9.0, device="cuda"), torch.full((8, 65), 9, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(got_one, one) and one.any()

@@ -67,3 +67,35 @@ def test_hidden_states_that_are_refused(gpu, seen):  # noqa: F811
         with pytest.raises(ValueError):
             head.gradient(bad, tokens, torch.zeros(3, 4))
     assert not seen
+
+
+@pytest.mark.parametrize("stream", [None, 7])
+def test_table_gradient_of_a_cut_batch(gpu, monkeypatch, stream):  # noqa: F811
+    """The output's gradient of several sequences, each without its first; of one
+    token that is a number of no dimension."""
+    got = []
+
+    def call(g, *_):
+        got.append((gpu.inside, rows_at(g.dy, g.dy_stride, g.n, g.cols, torch.float32)))
+        return ed.DF11_OK
+
+    monkeypatch.setattr(gpu.lib, "df11_embedding_gradient", call, raising=False)
+    dy, tokens = torch.randn(3, 5, 24), torch.zeros(3, 5, dtype=torch.int64)
+    emb = ed.Embedding(torch.zeros(9, 24))
+    for part, at in ((dy[:, 1:], tokens[:, 1:]), (dy.transpose(0, 1)[1:], tokens.t()[1:]), (dy[2, 3], tokens[2, 3]),
+                     (dy[:, 1:, 3:11], tokens[:, 1:])):
+        cols = part.size(-1)
+        want = part.reshape(-1, cols)
+        for f in (lambda: ed.embedding_gradient(at, part, 9, stream=stream),
+                  lambda: emb.gradient(at, part, stream=stream)):
+            got.clear()
+            gpu.lent.clear()
+            assert f().shape == (9, cols)
+            assert len(got) == 1 and got[0][0] == (stream or gpu.current) and torch.equal(got[0][1], want)
+            assert ((part.data_ptr(), 7) in gpu.lent) == (stream == 7)
+    got.clear()
+    for bad, at in ((dy.transpose(1, 2), torch.zeros(3, 24, dtype=torch.int64)), (dy[:, :, ::2], tokens),
+                    (dy[:2], tokens), (dy[0, 0], tokens[0]), (dy[0, 0, 0], tokens[0, 0])):
+        with pytest.raises(ValueError):
+            ed.embedding_gradient(at, bad, 9)
+    assert not got
