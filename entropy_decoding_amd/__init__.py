@@ -14,6 +14,7 @@ importing this module without it raises ImportError.  There is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -1639,6 +1640,25 @@ def embedding_gradient(tokens, dy, rows: int, dtype=None, out=None, accumulate: 
     return out
 
 
+@functools.cache
+def _undifferentiable():
+    """f(why, outputs, *leaves): the outputs as of a function of the leaves whose
+    derivative is the error ``why``."""
+    import torch
+
+    class Undifferentiable(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, why, outputs, *_):
+            ctx.why = why
+            return tuple(outputs)
+
+        @staticmethod
+        def backward(ctx, *_):
+            raise RuntimeError(ctx.why)
+
+    return Undifferentiable.apply
+
+
 class VocabLoss(_Lender):
     """Softmax cross entropy of hidden states under an output head, without keeping
     the logits (df11_vocab_loss), and its gradients (df11_vocab_loss_gradient).
@@ -1738,7 +1758,8 @@ class VocabLoss(_Lender):
         of ``ignore_index`` has loss 0, another one outside the vocabulary NaN.
         ``status``: for a compressed head, as in df11_decompress_tensor.  The call
         records no graph: hidden states that require a gradient are refused (detach
-        them; ``gradient`` makes it)."""
+        them; ``gradient`` makes it), and under pieces that require one the outputs
+        refuse to be differentiated (outside torch.no_grad())."""
         import torch
 
         if x.requires_grad and torch.is_grad_enabled():
@@ -1761,6 +1782,9 @@ class VocabLoss(_Lender):
                 _check("df11_vocab_loss", LIB.df11_vocab_loss(p, *given_to))
         if stream is not None or st not in self._lent:
             self._used(stream, st, used + [losses, lse] + ([] if status is None else [status]))
+        if self.pieces is not None and torch.is_grad_enabled() and any(w.requires_grad for w in self.pieces):
+            return _undifferentiable()("a loss records no gradient for its head: `gradient` makes it; detach the "
+                                       "losses, or call under torch.no_grad()", [losses, lse], *self.pieces)
         return losses, lse
 
     def _used(self, stream, st, tensors):

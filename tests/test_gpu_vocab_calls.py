@@ -58,3 +58,19 @@ def test_table_gradient_of_a_cut_batch(side):
     torch.full((8, 65, 136), 9.0, device="cuda"), torch.full((8, 65), 9, device="cuda")
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(got_one, one) and one.any()
+
+
+def test_losses_under_a_head_that_requires_a_gradient():
+    """The same bits; differentiated, also beside what has a gradient, they are an error."""
+    say("[gpu] head that requires a gradient")
+    x, w, targets = inputs(40, 300, 72, 5)
+    want, want_lse = ed.VocabLoss([w])(x, targets)
+    param, other = torch.nn.Parameter(w), torch.ones(1, device="cuda").requires_grad_()
+    head = ed.VocabLoss([param])
+    losses, lse = head(x, targets)
+    assert torch.equal(losses, want) and torch.equal(lse, want_lse)
+    with pytest.raises(RuntimeError, match="records no gradient for its head"):
+        (losses.sum() + other.sum()).backward()
+    dx, (dw,) = head.gradient(x, targets, lse, losses=losses)
+    want_dx, (want_dw,) = ed.VocabLoss([w]).gradient(x, targets, want_lse, losses=want)
+    assert torch.equal(dx, want_dx) and torch.equal(dw, want_dw)

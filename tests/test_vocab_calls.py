@@ -99,3 +99,21 @@ def test_table_gradient_of_a_cut_batch(gpu, monkeypatch, stream):  # noqa: F811
         with pytest.raises(ValueError):
             ed.embedding_gradient(at, bad, 9)
     assert not got
+
+
+def test_losses_under_a_head_that_requires_a_gradient_are_not_differentiated(gpu):  # noqa: F811
+    """The call records no graph.  A loss summed with what has one must not leave the
+    head without its gradient in silence."""
+    pieces = [torch.zeros(6, 16, dtype=BF16), torch.nn.Parameter(torch.zeros(3, 16, dtype=BF16))]
+    x, targets, other = torch.zeros(5, 16, dtype=BF16), torch.zeros(5, dtype=torch.int64), torch.ones(1).requires_grad_()
+    head = ed.VocabLoss(pieces)
+    losses, lse = head(x, targets)
+    for out in (losses, lse):
+        with pytest.raises(RuntimeError, match="gradient"):
+            (out.sum() + other.sum()).backward()
+    assert pieces[1].grad is None
+    head.gradient(x, targets, lse, losses=losses)
+    with torch.no_grad():
+        assert not any(t.requires_grad for t in head(x, targets))
+    pieces[1].requires_grad_(False)
+    assert not any(t.requires_grad for t in head(x, targets))
