@@ -798,16 +798,17 @@ __global__ __launch_bounds__(256) void spread(TokenArgs a) {
 
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
-// The tiles, how many workgroups a compute unit holds, and the microseconds of a
-// stage with the chip full of them and with one of them alone, fitted to the
-// logits of 16 to 8192 tokens x 128256 rows x 4096 columns and of 1001 x 32003 x
-// 1000.
+// The tiles, their threads, how many workgroups a compute unit holds, and the
+// microseconds of a stage with the chip full of them and with one of them alone,
+// fitted to the logits of 16 to 8192 tokens x 128256 rows x 4096 columns and of
+// 1001 x 32003 x 1000.
 struct Tile {
-    uint32_t t, r, held;
+    uint32_t t, r, threads, held;
     float full, alone;
 };
-constexpr Tile kTiles[] = {{32, 64, 2, 0.30f, 0.20f},   {64, 64, 2, 0.42f, 0.23f},  {64, 128, 2, 0.73f, 0.35f},
-                           {128, 128, 1, 0.57f, 0.42f}, {256, 128, 1, 0.95f, 0.8f}, {256, 256, 1, 1.49f, 1.3f}};
+constexpr Tile kTiles[] = {{32, 64, 128, 2, 0.30f, 0.20f},   {64, 64, 256, 2, 0.42f, 0.23f},
+                           {64, 128, 256, 2, 0.73f, 0.35f},  {128, 128, 512, 1, 0.57f, 0.42f},
+                           {256, 128, 512, 1, 0.95f, 0.8f},  {256, 256, 512, 1, 1.49f, 1.3f}};
 constexpr int kTileKinds = sizeof(kTiles) / sizeof(kTiles[0]);
 constexpr uint32_t kUnits = 256;  // compute units
 
@@ -865,15 +866,15 @@ int run_tiles(int tile, const TileArgs &a, uint64_t t_most, hipStream_t st) {
     const uint64_t all = tiles_of(kTiles[tile], t_most, a.r_size) * a.splits;
     if (!all) return DF11_OK;
     const uint64_t groups = up(all, 8);
-    if (groups >> 22) return DF11_E_INVALID;  // a grid holds less than 2^32 threads
-    const dim3 grid = dim3(uint32_t(groups));
+    if (groups * kTiles[tile].threads >> 32) return DF11_E_INVALID;  // a grid holds less than 2^32 threads
+    const dim3 grid(static_cast<uint32_t>(groups)), block(kTiles[tile].threads);
     switch (tile) {
-    case 0: return status(launch(tiles<Y, S, KIND, 32, 64, 1, 2, 6>, grid, dim3(128), 0, st, a));
-    case 1: return status(launch(tiles<Y, S, KIND, 64, 64, 2, 2, 4>, grid, dim3(256), 0, st, a));
-    case 2: return status(launch(tiles<Y, S, KIND, 64, 128, 1, 4, 3>, grid, dim3(256), 0, st, a));
-    case 3: return status(launch(tiles<Y, S, KIND, 128, 128, 4, 2, 4>, grid, dim3(512), 0, st, a));
-    case 4: return status(launch(tiles<Y, S, KIND, 256, 128, 4, 2, 3>, grid, dim3(512), 0, st, a));
-    default: return status(launch(tiles<Y, S, KIND, 256, 256, 2, 4, 2>, grid, dim3(512), 0, st, a));
+    case 0: return status(launch(tiles<Y, S, KIND, 32, 64, 1, 2, 6>, grid, block, 0, st, a));
+    case 1: return status(launch(tiles<Y, S, KIND, 64, 64, 2, 2, 4>, grid, block, 0, st, a));
+    case 2: return status(launch(tiles<Y, S, KIND, 64, 128, 1, 4, 3>, grid, block, 0, st, a));
+    case 3: return status(launch(tiles<Y, S, KIND, 128, 128, 4, 2, 4>, grid, block, 0, st, a));
+    case 4: return status(launch(tiles<Y, S, KIND, 256, 128, 4, 2, 3>, grid, block, 0, st, a));
+    default: return status(launch(tiles<Y, S, KIND, 256, 256, 2, 4, 2>, grid, block, 0, st, a));
     }
 }
 

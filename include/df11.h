@@ -891,7 +891,9 @@ typedef struct df11_vocab_sizes {
  * df11_vocab_loss_scratch_bytes(sizes) bytes, not shared by calls that may
  * overlap; no initialisation needed.  Asynchronous.  Outputs
  * must not overlap anything.  Errors: DF11_E_INVALID (null or misaligned
- * pointers, sizes, strides, a piece outside the head, the scratch), DF11_E_HIP.
+ * pointers, sizes, strides, a piece outside the head, the scratch, 2^23 tiles of
+ * 256 tokens x 256 rows and more: 2^20 tokens take a piece of less than 2^19 rows),
+ * DF11_E_HIP.
  */
 uint64_t df11_vocab_loss_scratch_bytes(const df11_vocab_sizes *z);
 int df11_vocab_loss(const df11_vocab_piece *p, float *losses, float *lse,
@@ -938,7 +940,8 @@ typedef struct df11_vocab_grad {
  * same in all calls of a gradient.  scratch as above, of
  * df11_vocab_loss_gradient_scratch_bytes(sizes) bytes.  dx and dw need their element's
  * alignment only, and must not overlap anything.  Deterministic.  Asynchronous.
- * Errors as df11_vocab_loss's.
+ * Errors as df11_vocab_loss's, and DF11_E_INVALID for 2^26 parts of 512 columns of x
+ * and more, and for 2^23 tiles of 256 x 256 elements of dw and more.
  */
 uint64_t df11_vocab_loss_gradient_scratch_bytes(const df11_vocab_sizes *z);
 int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g,

@@ -8,7 +8,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 import entropy_decoding_amd as ed  # noqa: E402
-from test_gpu_vocab_loss import F32, inputs, randn, say  # noqa: E402
+from test_gpu_vocab_loss import F32, Exact, check, inputs, randn, say  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -74,3 +74,17 @@ def test_losses_under_a_head_that_requires_a_gradient():
     dx, (dw,) = head.gradient(x, targets, lse, losses=losses)
     want_dx, (want_dw,) = ed.VocabLoss([w]).gradient(x, targets, want_lse, losses=want)
     assert torch.equal(dx, want_dx) and torch.equal(dw, want_dw)
+
+
+def test_loss_of_many_tokens_under_many_rows():
+    """2^22 tiles of 512 threads: half of what a grid holds.  Every block of the same
+    1024 tokens has their bits."""
+    say("[gpu] loss of 2^20 tokens under 262147 rows")
+    x, w, targets = inputs(1024, 262_147, 8, 3)
+    head, e = ed.VocabLoss([w]), Exact(x, w, targets)
+    losses, lse = head(x, targets)
+    check(lse, e.lse, e.off_lse, "lse")
+    check(losses, e.loss, e.off_loss, "loss")
+    del e
+    many, many_lse = head(x.repeat(1024, 1), targets.repeat(1024))
+    assert (many.view(1024, 1024) == losses).all() and (many_lse.view(1024, 1024) == lse).all()

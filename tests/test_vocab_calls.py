@@ -117,3 +117,13 @@ def test_losses_under_a_head_that_requires_a_gradient_are_not_differentiated(gpu
         assert not any(t.requires_grad for t in head(x, targets))
     pieces[1].requires_grad_(False)
     assert not any(t.requires_grad for t in head(x, targets))
+
+
+def test_a_piece_of_more_tiles_than_a_grid_holds_is_refused():
+    """2^12 x 2^11 tiles of 256 tokens x 256 rows, of 512 threads each: 2^32 threads (the
+    pointers are made up)."""
+    z = ed.df11_vocab_sizes(1 << 20, 8, 1 << 19, 0, 0)
+    nbytes = ed.LIB.df11_vocab_loss_scratch_bytes(z)
+    p = ed.df11_vocab_piece(x=4096, targets=8192, w=16384, x_stride=8, w_stride=8, ignored=-100, n=z.n, cols=8,
+                            vocab=z.rows, first=0, rows=z.rows, target_bits=64, begin=1, end=1)
+    assert ed.LIB.df11_vocab_loss(p, 32768, 65536, z, 1 << 20, nbytes, None) == ed.DF11_E_INVALID
