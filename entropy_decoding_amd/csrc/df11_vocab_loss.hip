@@ -45,6 +45,24 @@ enum Kind { STATS, GRAD, DX, DW, DW_PAST };  // DW_PAST: DW stored past the cach
 constexpr uint32_t kDepth = 64;  // of a stage: columns (or rows) that are summed over
 constexpr uint32_t kNever = 0x7FFFFF00u;  // an offset behind every buffer: the load gives zeros
 
+// The tiles, their threads, how many workgroups a compute unit holds, and the
+// microseconds of a stage with the chip full of them and with one of them alone,
+// fitted to the logits of 16 to 8192 tokens x 128256 rows x 4096 columns and of
+// 1001 x 32003 x 1000.
+struct Tile {
+    uint32_t t, r, threads, held;
+    float full, alone;
+};
+constexpr Tile kTiles[] = {{32, 64, 128, 2, 0.30f, 0.20f},   {64, 64, 256, 2, 0.42f, 0.23f},
+                           {64, 128, 256, 2, 0.73f, 0.35f},  {128, 128, 512, 1, 0.57f, 0.42f},
+                           {256, 128, 512, 1, 0.95f, 0.8f},  {256, 256, 512, 1, 1.49f, 1.3f}};
+
+constexpr uint32_t held(int t, int r) {
+    for (const Tile &tile : kTiles)
+        if (int(tile.t) == t && int(tile.r) == r) return tile.held;
+    return 0;
+}
+
 // A product y[t][r] = sum over k of a[t][k] b[r][k].  The operands of DX and
 // DW that hold k as rows are read transposed: b of DX (w), a and b of DW (g, x).
 struct TileArgs {
@@ -211,6 +229,8 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
     __shared__ __align__(16) char x3[NB > 3 ? kA : 16], w3[NB > 3 ? kB : 16];
     __shared__ __align__(16) char x4[NB > 4 ? kA : 16], w4[NB > 4 ? kB : 16];
     __shared__ __align__(16) char x5[NB > 4 ? kA : 16], w5[NB > 4 ? kB : 16];
+    static_assert(held(BT, BR) && held(BT, BR) * (NB * (kA + kB) + BT * 16 + 128) <= 160 * 1024,
+                  "a compute unit's LDS holds the workgroups that the tile's times are for");
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = uniform(threadIdx.x >> 6);
     // tokens that there are, where only the device knows
@@ -456,13 +476,15 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
         // that a t's leave in whole cache lines.
         constexpr int kRows = std::min<int>(128 / sizeof(S), 16 * FR), kParts = kRows / 16;
         constexpr uint32_t kBytes = kRows * sizeof(S), kPitch = kBytes + 16;  // t's in different banks
+        // A wave's 32 t in stages' buffers, which are free now: memory of their own
+        // would leave a compute unit room for one workgroup of the small tiles, not two
+        // (gradient of 16 tokens, 128256 x 4096: dx 296 us, 279 in the buffers)
         constexpr uint32_t kX = kA / (32 * kPitch), kW = kB / (32 * kPitch);
         static_assert(FR % kParts == 0, "whole rows of results");
-        constexpr bool kOwn = kWaves > int(2 * kX + kW);  // small buffers: memory of its own
-        __shared__ __align__(16) char results[kOwn ? kWaves * 32 * kPitch : 16];
-        char *out = kOwn ? results + wave * (32 * kPitch)
-                         : (wave < kX ? x0 : wave < 2 * kX ? x1 : w0) +
-                               (wave < 2 * kX ? wave % std::max(kX, 1u) : wave - 2 * kX) * (32 * kPitch);
+        static_assert(kWaves <= 2 * kX + 2 * kW, "room for the waves' results");
+        const uint32_t of_w = wave - 2 * kX;
+        char *out = wave < 2 * kX ? (wave < kX ? x0 : x1) + wave % std::max(kX, 1u) * (32 * kPitch)
+                                  : (of_w < kW ? w0 : w1) + of_w % std::max(kW, 1u) * (32 * kPitch);
         constexpr uint32_t kEach = 16 / sizeof(S);
         typedef S S4 __attribute__((ext_vector_type(4)));
         typedef S SE __attribute__((ext_vector_type(kEach)));
@@ -798,17 +820,6 @@ __global__ __launch_bounds__(256) void spread(TokenArgs a) {
 
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
-// The tiles, their threads, how many workgroups a compute unit holds, and the
-// microseconds of a stage with the chip full of them and with one of them alone,
-// fitted to the logits of 16 to 8192 tokens x 128256 rows x 4096 columns and of
-// 1001 x 32003 x 1000.
-struct Tile {
-    uint32_t t, r, threads, held;
-    float full, alone;
-};
-constexpr Tile kTiles[] = {{32, 64, 128, 2, 0.30f, 0.20f},   {64, 64, 256, 2, 0.42f, 0.23f},
-                           {64, 128, 256, 2, 0.73f, 0.35f},  {128, 128, 512, 1, 0.57f, 0.42f},
-                           {256, 128, 512, 1, 0.95f, 0.8f},  {256, 256, 512, 1, 1.49f, 1.3f}};
 constexpr int kTileKinds = sizeof(kTiles) / sizeof(kTiles[0]);
 constexpr uint32_t kUnits = 256;  // compute units
 
