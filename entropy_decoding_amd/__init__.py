@@ -1536,6 +1536,11 @@ def _token_bits(tokens, device) -> int:
     return bits
 
 
+def _check_padding(padding_idx, rows):
+    if padding_idx is not None and not 0 <= padding_idx < rows:
+        raise ValueError("padding_idx must be a row of the table")
+
+
 _TOKEN_BITS = {}  # by torch's types, filled when first seen
 
 
@@ -1546,6 +1551,7 @@ class Embedding(_Lender):
 
     def __init__(self, table, scale: float = 1.0, padding_idx: int | None = None):
         stride = _rows_apart(table, "the table")
+        _check_padding(padding_idx, table.size(0))
         self.table, self.scale, self.padding_idx = table, float(scale), padding_idx
         self.device, self._memory, self._lent = table.device, [table.detach()], set()
         self._a = df11_embedding_lookup(table=table.data_ptr(), table_stride=stride, rows=table.size(0),
@@ -1610,14 +1616,13 @@ def embedding_gradient(tokens, dy, rows: int, dtype=None, out=None, accumulate: 
         if dy.dim() < 1 or dy.shape[:-1] != tokens.shape:
             raise ValueError("dy must be [number of tokens, cols]")
         dy = _flat(dy, tokens.numel(), "dy", device, stream)
+    _check_padding(padding_idx, rows)
     g = df11_embedding_grad(dy_stride=_rows_apart(dy, "dy", device), rows=rows, n=tokens.numel(),
                             padding=-1 if padding_idx is None else padding_idx, cols=dy.size(1),
                             dy_type=_type(dy.dtype), token_bits=_token_bits(tokens, device),
                             accumulate=bool(accumulate), scale=scale)
     if dy.size(0) != g.n or rows < 0:
         raise ValueError("dy must be [number of tokens, cols]")
-    if padding_idx is not None and not 0 <= padding_idx < rows:
-        raise ValueError("padding_idx must be a row of the table")
     if out is not None:
         g.dw_stride = _output(out, "out", (rows, g.cols), dtype, device)
     elif accumulate:

@@ -127,3 +127,11 @@ def test_a_piece_of_more_tiles_than_a_grid_holds_is_refused():
     p = ed.df11_vocab_piece(x=4096, targets=8192, w=16384, x_stride=8, w_stride=8, ignored=-100, n=z.n, cols=8,
                             vocab=z.rows, first=0, rows=z.rows, target_bits=64, begin=1, end=1)
     assert ed.LIB.df11_vocab_loss(p, 32768, 65536, z, 1 << 20, nbytes, None) == ed.DF11_E_INVALID
+
+
+def test_padding_outside_the_table_is_refused_at_once(gpu):  # noqa: F811
+    table = torch.zeros(9, 16)
+    for bad in (-1, 9, 1 << 70):
+        with pytest.raises(ValueError, match="padding_idx"):
+            ed.Embedding(table, padding_idx=bad)
+    assert ed.Embedding(table, padding_idx=8).padding_idx == 8
