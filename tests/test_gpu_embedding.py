@@ -332,3 +332,26 @@ def test_named_stream():
         torch.cuda.synchronize()
         assert torch.equal(y, emb.table[kept])
         check_gradient(dw, kept, want, 500)
+
+
+@pytest.mark.parametrize("kind,n", [(F32, 33_000), (BF16, 66_000), (F16, 66_001)])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_gradient_added_from_much_that_is_read_once(kind, n, out):
+    """2^27 bytes of dy and more pass the caches: runs of one token and runs over many
+    chunks, added into rows that lie apart."""
+    rows, cols = 4001, 1033
+    say(f"[gpu] gradient added from {n} x {cols} of {kind}, to {out}")
+    assert n * cols * (4 if kind == F32 else 2) >= 1 << 27
+    tokens, dy = some_tokens(n, rows, 3), randn(n, cols, seed=4).to(kind)
+    tokens[: n // 8], tokens[5::1000] = 17, rows + 3
+    before = randn(rows, cols, seed=5).to(out)
+    room = torch.full((rows, cols + 6), 7.0, dtype=out, device="cuda")
+    dw = room[:, 3:cols + 3]
+    dw.copy_(before)
+    ed.embedding_gradient(tokens, dy, rows, out=dw, accumulate=True, scale=0.5, padding_idx=9)
+    kept = (tokens < rows) & (tokens != 9)
+    count = torch.bincount(tokens[kept], minlength=rows)
+    assert count.max() > n // 8 - 100 and (count == 1).any() and (count == 0).any()
+    assert torch.equal(dw[count == 0], before[count == 0])
+    check_gradient(dw, tokens, dy, rows, 0.5, 9, before)
+    assert (room[:, :3] == 7).all() and (room[:, cols + 3:] == 7).all()

@@ -149,8 +149,8 @@ def check_all(n, rows, cols, seed=0, kind=torch.int64, dx=BF16, dw=BF16, add=Fal
     return head, x, targets, losses, lse, got_dx, got_dw
 
 
-# every tile of the logits (up to 32, up to 64, up to 128 tokens, small and
-# large results) and of both gradients, whole and ragged
+# small and large results, whole and ragged (test_gpu_vocab_tiles.py has every form
+# of the tiles)
 SIZES = [(1, 1, 8), (1, 2, 64), (1, 999, 256), (3, 17, 72), (16, 4000, 128), (31, 65, 8), (32, 64, 64),
          (33, 63, 136), (64, 700, 200), (65, 129, 64), (77, 1003, 1000), (128, 256, 256), (129, 255, 264),
          (300, 2000, 520), (257, 70_001, 40), (700, 24_500, 72), (40, 4300, 4104), (2100, 130, 8200)]

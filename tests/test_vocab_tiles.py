@@ -2,6 +2,8 @@
 many workgroups fit a compute unit as their choice counts on, and no register
 goes to memory."""
 
+import math
+import random
 import re
 import struct
 import subprocess
@@ -9,6 +11,8 @@ import subprocess
 import pytest
 
 import entropy_decoding_amd as ed
+import vocab_shapes
+import vocab_tiles
 
 READELF = "/opt/rocm/llvm/bin/llvm-readelf"
 # (t, r): threads, workgroups of a compute unit
@@ -50,3 +54,36 @@ def test_workgroups_of_a_compute_unit(tmp_path):
         assert int(v["vgpr_spill_count"]) == int(v["sgpr_spill_count"]) == 0, (kind, shape)
         assert int(v["private_segment_fixed_size"]) == 0, (kind, shape)
     assert seen == {(k, s) for k in KINDS for s in TILES}
+
+
+def test_the_choice_of_tiles_is_the_librarys():
+    """As far as the scratch tells it: a tile's rows, g's chunk and dx's parts."""
+    rng = random.Random(1)
+
+    def log(lo, hi):
+        return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+    assert [tuple(map(int, t[:4])) for t in vocab_tiles.TILES] == [(*s, *v) for s, v in TILES.items()]
+    for _ in range(4000):
+        n, rows, cols = log(1, 1 << 20), log(1, 1 << 24), 8 * log(1, 1 << 17)
+        z = ed.df11_vocab_sizes(n, cols, rows, rng.randint(0, 1), rng.randint(0, 1))
+        assert ed.LIB.df11_vocab_loss_scratch_bytes(z) == vocab_tiles.loss_bytes(n, rows, cols)
+        assert (ed.LIB.df11_vocab_loss_gradient_scratch_bytes(z) ==
+                vocab_tiles.gradient_bytes(n, rows, cols, z.dx, z.two_terms))
+
+
+def test_the_gpu_tests_reach_every_form():
+    """All tiles of all products, and each of the logits at 16 stages and more.  Not among
+    them: dw past the caches in tiles that only shapes of more than 2^28 elements
+    of g or w take."""
+    products = ["logits", "g", "dx", "dx in parts", *(f"dw {t}{a}" for t in ("bfloat16", "float32")
+                                                      for a in ("", " added"))]
+    want = {(p, k) for p in products for k in range(6)}
+    want |= {("dw bfloat16 past", k) for k in (3, 4, 5)} | {("dw float32 added past", k) for k in (3, 4, 5)}
+    want |= {("dw float32 past", k) for k in (1, 2, 4, 5)}
+    seen, deep = set(), set()
+    for n, rows, cols, dx, dw, add in vocab_shapes.SHAPES + vocab_shapes.PAST:
+        found = vocab_tiles.forms(n, rows, cols, dw, add)
+        seen |= found
+        deep |= {k for p, k in found if p == "logits" and cols >= 1000}
+    assert not want - seen and deep == set(range(6))
