@@ -1749,8 +1749,13 @@ class VocabLoss(_Lender):
         stride = _rows_apart(x, "hidden states", self.device)
         if x.shape != (targets.numel(), self.cols):
             raise ValueError("hidden states must be [number of targets, cols]")
+        at = x.data_ptr()
+        if at % 16 or stride % 8 or not self.cols <= stride <= DF11_VOCAB_MAX_STRIDE:
+            with _on(self.device, stream)[0]:
+                x = x.clone(memory_format=torch.contiguous_format)
+            at, stride = x.data_ptr(), self.cols
         p = df11_vocab_piece.from_buffer_copy(self._p)
-        p.x, p.x_stride, p.n, p.ignored = x.data_ptr(), stride, x.size(0), ignore_index
+        p.x, p.x_stride, p.n, p.ignored = at, stride, x.size(0), ignore_index
         p.target_bits = _token_bits(targets, self.device)
         return x, p
 
@@ -1758,8 +1763,9 @@ class VocabLoss(_Lender):
         """(losses, lse), float32 like ``targets`` (int32 or int64): the cross entropy
         of each token, and the logarithm of its sum of exponentials.  ``x``: BF16
         hidden states [*targets.shape, cols] or [number of targets, cols], contiguous
-        rows; those of a batch that no one stride reaches (``x[:, :-1]`` of several
-        sequences) are copied first.  A target
+        rows; those that no one stride reaches (``x[:, :-1]`` of several sequences), or
+        that lie otherwise than df11_vocab_loss takes them (``x[:, -1]`` of long ones),
+        are copied first.  A target
         of ``ignore_index`` has loss 0, another one outside the vocabulary NaN.
         ``status``: for a compressed head, as in df11_decompress_tensor.  The call
         records no graph: hidden states that require a gradient are refused (detach

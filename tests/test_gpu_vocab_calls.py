@@ -88,3 +88,24 @@ def test_loss_of_many_tokens_under_many_rows():
     del e
     many, many_lse = head(x.repeat(1024, 1), targets.repeat(1024))
     assert (many.view(1024, 1024) == losses).all() and (many_lse.view(1024, 1024) == lse).all()
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_loss_of_rows_that_the_library_does_not_reach(side):
+    """The last token of each of several long sequences, rows that begin at any
+    element, one row for all targets: the same bits as of rows one behind the other."""
+    say(f"[gpu] loss of rows far apart or misaligned, on a stream of its own: {side}")
+    long, w, _ = inputs(3 * 20_000, 300, 136, 2)
+    targets, stream = torch.tensor([5, -100, 299], device="cuda"), torch.cuda.Stream() if side else None
+    head = ed.VocabLoss([w])
+    for x in (long.view(3, 20_000, 136)[:, -1], randn(3, 200, seed=1).to(long.dtype)[:, 3:139],
+              randn(3, 139, seed=2).to(long.dtype)[:, :136], long[7:8].expand(3, 136)):
+        want, want_lse = head(x.contiguous(), targets)
+        want_dx, (want_dw,) = head.gradient(x.contiguous(), targets, want_lse)
+        if side:
+            stream.wait_stream(torch.cuda.current_stream())
+        losses, lse = head(x, targets, stream=stream)
+        dx, (dw,) = head.gradient(x, targets, lse, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(losses, want) and torch.equal(lse, want_lse)
+        assert torch.equal(dx, want_dx) and torch.equal(dw, want_dw) and dw.any()

@@ -57,6 +57,30 @@ def test_loss_of_a_batch_without_its_last_tokens(gpu, seen, stream):  # noqa: F8
         assert ((part.data_ptr(), 7) in gpu.lent) == (stream == 7)
 
 
+@pytest.mark.parametrize("stream", [None, 7])
+def test_loss_of_rows_that_the_library_does_not_reach(gpu, seen, stream):  # noqa: F811
+    """The last token of each of several long sequences (rows further apart than
+    DF11_VOCAB_MAX_STRIDE); rows that begin at any element, or any number of them apart."""
+    head, targets = ed.VocabLoss([torch.zeros(6, 16, dtype=BF16)]), torch.zeros(2, dtype=torch.int64)
+    long = torch.randn(2, (1 << 17) + 1, 16).to(BF16)
+    odd = torch.randn(2, 27).to(BF16)
+    for x in (long[:, -1], odd[:, 8:24], torch.randn(2, 32).to(BF16)[:, 3:19], torch.randn(1, 16).to(BF16).expand(2, 16)):
+        seen.clear()
+        gpu.lent.clear()
+        _, lse = head(x, targets, stream=stream)
+        head.gradient(x, targets, lse, stream=stream)
+        assert len(seen) == 2 and all(s[1] == (stream or gpu.current) and torch.equal(s[2], x) for s in seen)
+        assert ((x.data_ptr(), 7) in gpu.lent) == (stream == 7)
+    assert all(p % 16 == 0 and s % 8 == 0 and s <= ed.DF11_VOCAB_MAX_STRIDE for p, s in given(head, long[:, -1], odd[:, 8:24]))
+
+
+def given(head, *xs):
+    """Where the rows lie that are passed on, and how far apart."""
+    for x in xs:
+        _, p = head._piece(x, torch.zeros(len(x), dtype=torch.int64), -100, None)
+        yield p.x, p.x_stride
+
+
 def test_hidden_states_that_are_refused(gpu, seen):  # noqa: F811
     head, tokens = ed.VocabLoss([torch.zeros(6, 16, dtype=BF16)]), torch.zeros(3, 4, dtype=torch.int64)
     x = torch.zeros(3, 16, 4, dtype=BF16)
