@@ -1108,8 +1108,14 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
             a.y_stride = g->dw_stride, a.add = g->accumulate;
             const int tile = tile_for(here, p->cols, uint64_t(p->n) * dw_terms);
             // a gradient that the caches do not hold passes them by, which leaves x and g
-            // there (512 tokens, 128256 x 4096: 580 us, 629 through them)
-            const bool past = uint64_t(p->rows) * p->cols * type_bytes(g->dw_type) >= 1ull << 27;
+            // there (512 tokens, 128256 x 4096: 580 us, 629 through them); float32 only
+            // where its rows lie on half lines, as a store's 128 bytes otherwise end in two
+            // parts of lines that the caches have to bring together (whole gradient of 64
+            // tokens, 56639 rows, dw alone: 4352 columns 302 us past them, 390 through
+            // them; 4368 columns 362 and 414; 4360 columns 647 and 447.  In BF16: 512
+            // tokens, 128256 x 4104, 1158 and 1226)
+            const bool whole = g->dw_type == DF11_TYPE_BF16 || (aligned(g->dw, 64) && g->dw_stride % 16 == 0);
+            const bool past = whole && uint64_t(p->rows) * p->cols * type_bytes(g->dw_type) >= 1ull << 27;
             if (g->dw_type == DF11_TYPE_F32) {
                 a.y = static_cast<float *>(g->dw) + c * g->dw_stride;
                 rc = past ? run_tiles<float, float, DW_PAST>(tile, a, here, st)

@@ -84,6 +84,6 @@ def test_the_gpu_tests_reach_every_form():
     seen, deep = set(), set()
     for n, rows, cols, dx, dw, add in vocab_shapes.SHAPES + vocab_shapes.PAST:
         found = vocab_tiles.forms(n, rows, cols, dw, add)
-        seen |= found
+        seen |= found | vocab_tiles.forms(n, rows, cols, dw, add, on_half_lines=True)
         deep |= {k for p, k in found if p == "logits" and cols >= 1000}
     assert not want - seen and deep == set(range(6))

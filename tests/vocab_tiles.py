@@ -54,13 +54,14 @@ def dx_split(n, cols, rows):
     return best
 
 
-def forms(n, rows, cols, dw="bfloat16", add=False):
-    """The (product, tile) of a loss with gradients, a head in one piece.  The products
+def forms(n, rows, cols, dw="bfloat16", add=False, on_half_lines=False):
+    """The (product, tile) of a loss with gradients, a head in one piece; whether dw's
+    rows lie on half lines.  The products
     of dw are told apart by type, by whether they are added, and stored past the caches;
     those of dx by whether they are in parts."""
     found = {("logits", tile_for(n, rows, cols))}
     chunk, size = chunk_rows(n, rows), 4 if dw == "float32" else 2
-    past = rows * cols * size >= PAST and not (add and size == 2)
+    past = rows * cols * size >= PAST and (not add if size == 2 else on_half_lines)
     name = f"dw {dw}{' added' if add else ''}{' past' if past else ''}"
     for c in range(0, rows, chunk):
         here = min(chunk, rows - c)
