@@ -276,13 +276,16 @@ __device__ __forceinline__ void clear_rows(const GradArgs &a, uint32_t wave, uin
 // chunk's first (the run began before) or second slot.  Without ADD further
 // workgroups clear the rows without a token meanwhile.  Bound by HBM.
 //
-// BIG: what would fill the caches passes them by.  With ADD that is dy (32768
-// tokens of 8192 columns, added to float32: 285 -> 262 us for the three launches),
-// otherwise dw, which leaves dy there (8192 tokens, 128256 x 4096 in BF16: 241 ->
-// 212 us; with dy read past the caches as well 240), if of 2 bytes an element: a
-// lane stores 8 float32 in two halves, which the caches have to bring together (the
-// same in float32: 448 us, past the caches 1000); cleared rows are stored otherwise
-// (402 us).
+// BIG: what would fill the caches passes them by.  With ADD that is a dy which the
+// last cache cannot hold (32768 tokens, added to 128256 rows of float32, the same each
+// time, so that dw may stay there: 8192 columns 273 -> 256 us for the three launches,
+// 4096 columns 194 -> 172; other inputs each time: 268 and 197 either way).  One that
+// it holds is read there if it was made before (66000 tokens, 4001 x 1024: 157 us, past
+// the caches 201).  Without ADD it is dw, which leaves dy there (8192 tokens, 128256 x
+// 4096 in BF16: 241 -> 212 us; with dy read past the caches as well 240), if of 2 bytes
+// an element: a lane stores 8 float32 in two halves, which the caches have to bring
+// together (the same in float32: 448 us, past the caches 1000); cleared rows are stored
+// otherwise (402 us).
 template <class X, class Y, bool ADD, bool BIG>
 __global__ __launch_bounds__(256) void sum_runs(GradArgs a) {
     constexpr bool PAST = BIG && !ADD && sizeof(Y) == 2, ONCE = BIG && ADD;
@@ -612,9 +615,9 @@ int df11_embedding_gradient(const df11_embedding_grad *g, void *scratch, uint64_
     a.summing = uint32_t(summing);
     const dim3 sorting((a.rows + a.run - 1) / a.run), both(uint32_t(summing + clearing));
     const size_t lds = (kSortWaves + 1) * a.run * 4;
-    // half of the last cache
-    const bool big = (g->accumulate ? uint64_t(a.n) * a.cols * type_bytes(g->dy_type)
-                                    : uint64_t(a.rows) * a.cols * type_bytes(g->dw_type)) >= 1ull << 27;
+    // dy of the last cache's size, or dw of half of it
+    const bool big = g->accumulate ? uint64_t(a.n) * a.cols * type_bytes(g->dy_type) >= 1ull << 28
+                                   : uint64_t(a.rows) * a.cols * type_bytes(g->dw_type) >= 1ull << 27;
     int rc = status(g->token_bits == 64 ? launch(sort_tokens<int64_t>, sorting, dim3(64 * kSortWaves), lds, st, a)
                                         : launch(sort_tokens<int32_t>, sorting, dim3(64 * kSortWaves), lds, st, a));
     if (rc != DF11_OK) return rc;
