@@ -29,8 +29,6 @@ struct LookupArgs {
     float scale;
 };
 
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
-
 // The token's row of the table, or 2^32 - 1 where it has none.
 template <class I>
 __device__ __forceinline__ uint32_t row_of(I token, uint32_t rows) {
@@ -443,7 +441,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void sum_few(GradArgs a) {
     for (uint32_t u = 0; u < kFewEach; u++)
         match(row[u], row[u] != 0xFFFFFFFFu, [&](uint32_t r0, uint64_t same, uint32_t first) {
             const uint32_t at = place[r0];
-            if (row[u] == r0) list[at + __popcll(same & ((1ull << lane) - 1))] = uint16_t(wave * a.span + 64 * u + lane);
+            if (row[u] == r0)
+                list[at + __popcll(same & ((1ull << lane) - 1))] = uint16_t(wave * a.span + 64 * u + lane);
             if (lane == first) place[r0] = at + __popcll(same);
         });
     __syncthreads();

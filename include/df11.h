@@ -805,9 +805,9 @@ int df11_embedding(const df11_embedding_lookup *e, df11_hip_stream st);
  * output head shares the table's memory).  Sums are float32, of a row's tokens
  * in the order of their positions, or of up to 8 or chunks of 32 to 128 of them
  * and then of those sums in order (as n, rows and cols have it, and the tokens'
- * places among the sorted); scaled, added and rounded once to dw_type.  No atomics on floats: the same inputs give the same bits.  Rows
- * without a token are set to zeros; with accumulate they are neither read nor
- * written.  Tokens equal to padding (-1: none) and tokens outside
+ * places among the sorted); scaled, added and rounded once to dw_type.  No atomics
+ * on floats: the same inputs give the same bits.  Rows without a token are set to
+ * zeros; with accumulate they are neither read nor written.  Tokens equal to padding (-1: none) and tokens outside
  * 0 .. rows - 1 add nothing.  Alignment and strides as df11_embedding's; dw
  * must not overlap anything; dy's rows may be one and the same (stride 0).
  * scratch: device, 128-byte aligned, at least
@@ -909,13 +909,15 @@ int df11_vocab_loss(const df11_vocab_piece *p, float *losses, float *lse,
  * them, a (exp(-loss) - 1) + c exp(-loss), which keeps its digits where the target
  * is nearly certain; the difference of logit and lse has those that lse holds.
  * g is rounded to BF16 for gradients in BF16; for those in float32, and for up to
- * 64 tokens, it is held as two BF16 terms (16 bits and more), which doubles their
- * products.  Sums are float32, rounded once.  Ignored tokens have
+ * 64 tokens in one call, it is held as two BF16 terms (16 bits and more), which
+ * doubles their products: a token's gradients depend, within that rounding, on how
+ * many tokens the call has.  Sums are float32, rounded once.  Ignored tokens have
  * no gradient at all: their dx is zero, and nothing of their x (which may be
  * NaN) enters dw.  A target outside the head makes its token's dx and all of dw
  * NaN.  Pieces as above: begin, then dw of each piece is written by its own
  * call, dx by the one with end.  g exists for up to 2^29 elements at a time (n times
- * the rows of a piece, or of equal parts of it; at least 256 rows).  2 launches for
+ * the rows of a piece, or of equal parts of it; at least 256 rows) in the scratch: 2
+ * bytes each, or 4 in two terms.  2 launches for
  * begin (1 for up to 1024 tokens), 1 for end, and 3 for every such part.
  */
 typedef struct df11_vocab_grad {
