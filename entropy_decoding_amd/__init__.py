@@ -1809,8 +1809,8 @@ class VocabLoss(_Lender):
                  needs_dx: bool = True, needs_dw: bool = True, losses=None, status=None, stream=None):
         """(dx, dws) of a call with these arguments that returned ``lse``: the hidden
         states' gradient [n, cols] and a list of the pieces' gradients, BF16 or
-        float32 (``dx_dtype``, ``dw_dtype``: BF16 by default; float32 doubles that
-        product's work), as new tensors or written into ``dx`` and ``dws``, with
+        float32 (``dx_dtype``, ``dw_dtype``: BF16 by default; float32 takes up to three
+        times that product's work), as new tensors or written into ``dx`` and ``dws``, with
         ``accumulate`` added to dws.  ``loss_grad``: the gradient that the losses
         have, a number or a float32 device tensor of one or of n elements;
         ``lse_grad``: that of lse, such a tensor or None.  ``losses``: the call's; with

@@ -72,10 +72,10 @@ struct TileArgs {
     uint64_t a_stride, b_stride;
     const uint32_t *count;  // where not null, the number of tokens (t, or k of DW)
     uint32_t t_size, r_size, k_size;
-    // g in one or two terms: the second lies `a_half` elements behind the first, and
-    // the stages go over k once for each
-    uint32_t halves;
-    uint64_t a_half;
+    // g in one to three terms, each `a_term` elements behind the one before; the stages
+    // go over k once for each
+    uint32_t terms;
+    uint64_t a_term;
     uint32_t splits, split_stages;  // of k
     // STATS and GRAD
     const void *targets;
@@ -88,7 +88,7 @@ struct TileArgs {
     uint32_t exact_target;
     const uint32_t *target_of;
     __bf16 *g;
-    uint64_t g_stride, g_half;
+    uint64_t g_stride, g_term;
     uint32_t r_padded;  // g is zero up to there
     // DX and DW
     void *y;
@@ -274,30 +274,32 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
     // Logits: stage 0 is the last 8 .. 64 columns, stage s > 0 starts at column
     // 64 (s - 1).  The others' stages go over whole groups of 64 (loads give zeros
     // behind the end of k), a split's own, each once for every term of g, so that
-    // the other operand comes from the cache the second time (16 tokens, 128256 x
+    // the other operand comes from the cache after the first (16 tokens, 128256 x
     // 4096, two terms: 1029 us where the second term followed the first, 911 so).
     const uint32_t whole = (k_size + kDepth - 1) / kDepth;
     const uint32_t s_first = kLogits ? 0 : min(whole, split * a.split_stages);
     const uint32_t s_here = kLogits ? whole : min(whole - s_first, a.split_stages);
-    const uint32_t two = kLogits ? 0 : a.halves - 1;
-    const uint32_t stages = s_here << two;
+    const uint32_t stages = kLogits ? s_here : s_here * a.terms;
+    // where the next stage to be loaded lies, of those of DX and DW, and the term of g
+    uint32_t next_k = s_first * kDepth, next_term = 0;
+    const uint32_t end_k = next_k + s_here * kDepth;
     const auto load_a = [&](char *lds, uint32_t s, int from, int to) {
         if constexpr (kLogits) {
             xa.load(lds, (s - 1) * kDepth, 0, s < stages, wave, lane, from, to);
         } else {
-            const uint32_t k0 = (s_first + (s >> two)) * kDepth;
-            const uint64_t behind = s & two ? a.a_half : 0;
-            if constexpr (KIND == DX) xa.load(lds, k0, behind, s < stages, wave, lane, from, to);
-            else xa.load(lds, k0, s < stages ? k_size : 0, behind, wave, from, to);
+            const uint64_t behind = next_term * a.a_term;
+            if constexpr (KIND == DX) xa.load(lds, next_k, behind, next_k < end_k, wave, lane, from, to);
+            else xa.load(lds, next_k, next_k < end_k ? k_size : 0, behind, wave, from, to);
         }
     };
     const auto load_b = [&](char *lds, uint32_t s, int from, int to) {
-        if constexpr (kLogits) {
-            wb.load(lds, (s - 1) * kDepth, 0, s < stages, wave, lane, from, to);
-        } else {
-            const uint32_t k0 = (s_first + (s >> two)) * kDepth;
-            wb.load(lds, k0, s < stages ? k_size : 0, 0, wave, from, to);
-        }
+        if constexpr (kLogits) wb.load(lds, (s - 1) * kDepth, 0, s < stages, wave, lane, from, to);
+        else wb.load(lds, next_k, next_k < end_k ? k_size : 0, 0, wave, from, to);
+    };
+    const auto load_both = [&](char *xs, char *ws, uint32_t s) {
+        load_b(ws, s, 0, B::kLoads);
+        load_a(xs, s, 0, A::kLoads);
+        if (!kLogits && ++next_term == a.terms) next_term = 0, next_k += kDepth;
     };
 
     // A step of 32 of k multiplies one set of operands while the next set
@@ -342,8 +344,7 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
             products(even, f);
         }
         arrived();
-        load_b(ws, s + NB, 0, WL);
-        load_a(xs, s + NB, 0, XL);
+        load_both(xs, ws, s + NB);
 #pragma unroll
         for (int f = 0; f < kF; f++) {
             read(even, xn, wn, 0, f);
@@ -376,13 +377,11 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
             xa.template load<true>(x0, tail, 0, true, wave, lane, 0, XL, k_size - tail);
             wb.template load<true>(w0, tail, 0, true, wave, lane, 0, WL, k_size - tail);
         } else {
-            load_a(x0, 0, 0, XL);
-            load_b(w0, 0, 0, WL);
+            load_both(x0, w0, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
         const auto begin = [&](char *xs, char *ws, uint32_t s) {
-            load_a(xs, s, 0, XL);
-            load_b(ws, s, 0, WL);
+            load_both(xs, ws, s);
             __builtin_amdgcn_sched_barrier(0);
         };
         begin(x1, w1, 1);
@@ -574,8 +573,8 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
 #pragma unroll
             for (int h0 = 0; h0 < FR; h0 += kParts) {
                 if constexpr (KIND == GRAD) {
-                    // The part of g, rounded to BF16, which the matrix cores multiply; the
-                    // second term is what that leaves.  One term's error is about that of
+                    // The part of g, rounded to BF16, which the matrix cores multiply; a
+                    // further term is what those before it leave.  One term's error is about that of
                     // the gradient's own rounding to BF16 (drawn shapes, of the norm: dx
                     // 0.00166 -> 0.0023 in the median, 0.0036 at most); the second costs
                     // its products again
@@ -606,7 +605,7 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
                         }
                     }
                 }
-                for (uint32_t term = 0; term < (KIND == GRAD ? a.halves : 1); term++) {
+                for (uint32_t term = 0; term < (KIND == GRAD ? a.terms : 1); term++) {
 #pragma unroll
                     for (int h = h0; h < h0 + kParts; h++) {
 #pragma unroll
@@ -628,9 +627,9 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
                         store_added(f, h0, old);
                         old = next;
                     } else {
-                        y += term ? a.g_half : 0;
+                        y += term * a.g_term;
                         store(f, h0);
-                        y -= term ? a.g_half : 0;
+                        y -= term * a.g_term;
                     }
                 }
             }
@@ -938,9 +937,9 @@ struct LossScratch {
     }
 };
 
-// g of so many rows at a time: up to 2^29 elements of it (1 GiB, or 2 in two terms;
-// where the whole of it is less, it takes as much as logits in as many bytes would), in
-// chunks of about the same size.  Every chunk but the first reads and writes dx's sums again: in chunks
+// g of so many rows at a time: up to 2^29 elements of it (1 GiB, 2 or 3 in two or
+// three terms; where the whole of it is less, it takes what logits in as many bytes
+// would), in chunks of about the same size.  Every chunk but the first reads and writes dx's sums again: in chunks
 // of 2^27 elements 8192 tokens x 128256 x 4096 took 25.32 ms, of 2^29 25.03.
 uint64_t chunk_rows(uint64_t n, uint64_t rows) {
     const uint64_t most = std::max<uint64_t>((1ull << 29) / std::max<uint64_t>(n, 1) / 256 * 256, 256);
@@ -953,6 +952,12 @@ uint64_t chunk_rows(uint64_t n, uint64_t rows) {
 // one term 835; 64 tokens 918 and 848; 128 tokens 1134 and 921), and a sum of few
 // products shows a rounding of one of them where they cancel.
 constexpr uint32_t kTwoTermTokens = 64;
+
+// Gradients in float32 have it in three, which hold what float32 does: 2e-7 of dw's norm
+// and 3e-7 of dx's in the median of drawn shapes, where two terms, 17 bits, left 1.6e-6
+// and 2.2e-6 and products in float32 leave 2e-7 and 5e-7.  The third costs its products
+// (1001 tokens, 32003 x 1000, dx and dw in float32: 358 -> 472 us).
+uint32_t terms_for(uint64_t n, bool f32) { return f32 ? 3 : n <= kTwoTermTokens ? 2 : 1; }
 
 struct GradScratch {
     uint32_t *count, *order, *place, *target_of;
@@ -973,7 +978,7 @@ struct GradScratch {
         chunk = chunk_rows(n, z.rows);
         dx = dx_split(n, z.cols, chunk);
         sums = s.take<float>(z.dx ? dx.parts * n * z.cols : 0);
-        g = s.take<__bf16>(n * chunk * (z.two_terms || n <= kTwoTermTokens ? 2 : 1));
+        g = s.take<__bf16>(n * chunk * terms_for(n, z.two_terms));
         bytes = s.at;
     }
 };
@@ -990,7 +995,7 @@ bool other_sizes(const df11_vocab_piece *p, const df11_vocab_sizes *z) {
 
 TileArgs tile_args() {
     TileArgs a{};
-    a.halves = a.splits = 1;
+    a.terms = a.splits = 1;
     a.split_stages = 0xFFFFFFFFu;
     return a;
 }
@@ -1041,9 +1046,8 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
         g->dw_type > DF11_TYPE_BF16 || g->accumulate > 1)
         return DF11_E_INVALID;
     const bool has_dx = sizes->dx, has_dw = g->dw;
-    const bool few = p->n <= kTwoTermTokens;
-    const uint32_t dx_terms = few || g->dx_type == DF11_TYPE_F32 ? 2 : 1;
-    const uint32_t dw_terms = few || g->dw_type == DF11_TYPE_F32 ? 2 : 1;
+    const uint32_t dx_terms = terms_for(p->n, g->dx_type == DF11_TYPE_F32);
+    const uint32_t dw_terms = terms_for(p->n, g->dw_type == DF11_TYPE_F32);
     const uint32_t terms = std::max(has_dx ? dx_terms : 1, has_dw ? dw_terms : 1);
     if (!sizes->two_terms &&
         ((has_dx && g->dx_type == DF11_TYPE_F32) || (has_dw && g->dw_type == DF11_TYPE_F32)))
@@ -1097,13 +1101,13 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
         a.count = s.count;
         a.r_size = here, a.k_size = p->cols, a.first = uint32_t(p->first + c);
         a.lse = s.lse_of, a.factor = s.factor, a.target_of = s.target_of;
-        a.g = s.g, a.g_stride = g_stride, a.g_half = p->n * g_stride, a.r_padded = uint32_t(g_stride);
-        a.halves = terms, a.exact_target = g->losses != nullptr;
+        a.g = s.g, a.g_stride = g_stride, a.g_term = p->n * g_stride, a.r_padded = uint32_t(g_stride);
+        a.terms = terms, a.exact_target = g->losses != nullptr;
         rc = run_tiles<__bf16, __bf16, GRAD>(tile_for(p->n, here, p->cols), a, p->n, st);
         if (rc != DF11_OK) return rc;
         if (has_dx && p->n) {
             a = tile_args();
-            a.a = s.g, a.a_stride = g_stride, a.a_half = p->n * g_stride, a.halves = dx_terms;
+            a.a = s.g, a.a_stride = g_stride, a.a_term = p->n * g_stride, a.terms = dx_terms;
             a.b = w, a.b_stride = p->w_stride;
             a.count = s.count;
             a.r_size = p->cols, a.k_size = here;
@@ -1116,7 +1120,7 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
         }
         if (has_dw && here) {
             a = tile_args();
-            a.a = s.g, a.a_stride = g_stride, a.a_half = p->n * g_stride, a.halves = dw_terms;
+            a.a = s.g, a.a_stride = g_stride, a.a_term = p->n * g_stride, a.terms = dw_terms;
             a.b = s.x, a.b_stride = s.x_stride;
             a.count = s.count;
             a.t_size = here, a.r_size = p->cols;

@@ -882,7 +882,7 @@ typedef struct df11_vocab_sizes {
     uint32_t n, cols;
     uint32_t rows;           /* of the largest piece */
     uint32_t dx;             /* 1: the gradient of x is asked for */
-    uint32_t two_terms;      /* 1: a gradient in float32 is */
+    uint32_t two_terms;      /* 1: one in float32 is (g then has three) */
 } df11_vocab_sizes;
 
 /*
@@ -908,17 +908,17 @@ int df11_vocab_loss(const df11_vocab_piece *p, float *losses, float *lse,
  * The logits are computed again.  With the losses, g at the target is formed from
  * them, a (exp(-loss) - 1) + c exp(-loss), which keeps its digits where the target
  * is nearly certain; the difference of logit and lse has those that lse holds.
- * g is rounded to BF16 for gradients in BF16; for those in float32, and for up to
- * 64 tokens in one call, it is held as two BF16 terms (16 bits and more), which
- * doubles their products: a token's gradients depend, within that rounding, on how
- * many tokens the call has.  Sums are float32, rounded once.  Ignored tokens have
- * no gradient at all: their dx is zero, and nothing of their x (which may be
- * NaN) enters dw.  A target outside the head makes its token's dx and all of dw
- * NaN.  Pieces as above: begin, then dw of each piece is written by its own
+ * g is rounded to BF16 for gradients in BF16, and for up to 64 tokens in one call held
+ * as two BF16 terms (16 bits and more), which doubles the products: a token's
+ * gradients depend, within that rounding, on how many tokens the call has.  For
+ * gradients in float32 it is three terms (24 bits).  Sums are float32, rounded once.
+ * Ignored tokens have no gradient at all: their dx is zero, and nothing of their x
+ * (which may be NaN) enters dw.  A target outside the head makes its token's dx and
+ * all of dw NaN.  Pieces as above: begin, then dw of each piece is written by its own
  * call, dx by the one with end.  g exists for up to 2^29 elements at a time (n times
- * the rows of a piece, or of equal parts of it; at least 256 rows) in the scratch: 2
- * bytes each, or 4 in two terms.  2 launches for
- * begin (1 for up to 1024 tokens), 1 for end, and 3 for every such part.
+ * the rows of a piece, or of equal parts of it; at least 256 rows) in the scratch, 2
+ * bytes a term.  2 launches for begin (1 for up to 1024 tokens), 1 for end, and 3 for
+ * every such part.
  */
 typedef struct df11_vocab_grad {
     const float *lse;        /* n, from df11_vocab_loss */

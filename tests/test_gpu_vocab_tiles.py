@@ -145,3 +145,35 @@ def check_bits(n, rows, cols, dx, dw, add, left, right):
         assert torch.equal(out_w[r:r + step], of_x.to(dw)), f"dw of rows from {r} on"
     assert 0 < most < 2 ** 24
     assert torch.equal(out_x, want.to(dx)), "dx"
+
+
+@pytest.mark.parametrize("n,rows,cols", [(5, 300, 72), (64, 3000, 136), (65, 129, 264), (300, 2000, 520),
+                                         (700, 24_500, 72), (1001, 5001, 1000)])
+@pytest.mark.parametrize("dx,dw", [(F32, F32), (F32, BF16), (BF16, F32)])
+def test_float32_gradients_hold_what_float32_does(n, rows, cols, dx, dw):
+    """As above, g of 1 + 2^-9 + 2^-20, which BF16 holds in three terms, with so few
+    entries in x and w that sums are below 16, so that float32 holds them too."""
+    say(f"[gpu] gradients of {n} tokens, {rows} x {cols}, {dx}, {dw}, of 21 bits")
+    group, off = whole(0, 7, n, seed=1), whole(0, 1, rows, 8, seed=2)
+
+    def few(count, seed):
+        keep = torch.rand(count, cols, generator=gen(seed), device="cuda") < 3 / count
+        return (whole(-1, 1, count, cols, seed=seed + 1) * keep).to(BF16)
+
+    x, w = few(n, 3), few(rows, 5)
+    x[:, 9::2], w[:, 8::2] = 0, 0
+    x[:, :8] = torch.nn.functional.one_hot(group.long(), 8)
+    w[:, :8] = -256.0 * off
+    targets = some_targets(n, rows, cols)
+    a = 1 + 2.0 ** -9 + 2.0 ** -20
+    got_dx, (got_dw,) = ed.VocabLoss([w]).gradient(x, targets, torch.zeros(n, device="cuda"), a, dx_dtype=dx,
+                                                  dw_dtype=dw)
+    here = torch.arange(rows, device="cuda")
+    g = a * (off[:, group.long()].t() == 0) - a * (targets[:, None] == here).double()
+    g[targets == -100] = 0
+    # the 8 columns that say which logits are 0 have long sums
+    x64, w64 = x[:, 8:].double(), w[:, 8:].double()
+    assert max((g.abs() @ w64.abs()).max(), (g.t().abs() @ x64.abs()).max()) < 16
+    for got, want, kind in ((got_dx, g @ w64, dx), (got_dw, g.t() @ x64, dw)):
+        if kind == F32:
+            assert want.any() and torch.equal(got[:, 8:], want.float())

@@ -18,6 +18,10 @@ TILES = [tuple(float(v.strip().rstrip("f")) for v in t.split(",")) for t in re.f
 DEPTH, UNITS, TWO_TERM_TOKENS, PAST = 64, 256, 64, 1 << 27
 
 
+def terms_for(n, float32):
+    return 3 if float32 else 2 if n <= TWO_TERM_TOKENS else 1
+
+
 def up(n, to):
     return -(-n // to) * to
 
@@ -66,7 +70,7 @@ def forms(n, rows, cols, dw="bfloat16", add=False, on_half_lines=False):
     for c in range(0, rows, chunk):
         here = min(chunk, rows - c)
         found.add(("g", tile_for(n, here, cols)))
-        found.add((name, tile_for(here, cols, n * (2 if n <= TWO_TERM_TOKENS or size == 4 else 1))))
+        found.add((name, tile_for(here, cols, n * terms_for(n, size == 4))))
     tile, parts = dx_split(n, cols, chunk)
     return found | {("dx in parts" if parts > 1 else "dx", tile)}
 
@@ -81,4 +85,4 @@ def gradient_bytes(n, rows, cols, dx, two_terms):
     parts = dx_split(n, cols, chunk)[1]
     total = 256 + 3 * up(4 * n, 256) + up(4 * n, 256) + up(8 * n, 256) + up(2 * n * up(cols, 64), 256)
     total += up(4 * parts * n * cols, 256) if dx else 0
-    return total + up(2 * n * chunk * (2 if two_terms or n <= TWO_TERM_TOKENS else 1), 256)
+    return total + up(2 * n * chunk * terms_for(n, two_terms), 256)
