@@ -2,9 +2,9 @@
 // the logits, and its gradients.
 //
 //   l[t][v] = x[t] . w[v]      lse[t] = log(sum_v exp l[t][v])      loss[t] = lse[t] - l[t][target t]
-//   g[t][v] = p_t exp(l[t][v] - lse[t]) - q_t [v = target t]        dx = g w        dw = g^T x
+//   g[t][v] = p_t exp(l[t][v] - lse[t]) - q_t [v = target t]        dx = s g w        dw = s g^T x
 //
-// where p_t and q_t come from the gradients of loss and lse.  All four products
+// where p_t and q_t come from the gradients of loss and lse, divided by s, their digits.  All four products
 // (the logits twice) run on one kernel of tiles on the matrix cores, with the
 // logits' two uses in its epilogues: a tile of logits leaves its rows' largest
 // value and sum of exponentials, or its part of g.  g exists in BF16 for a
@@ -91,6 +91,7 @@ struct TileArgs {
     uint64_t g_stride, g_term;
     uint32_t r_padded;  // g is zero up to there
     // DX and DW
+    const float *scale;   // of DW
     void *y;
     uint64_t y_stride, y_split;
     uint32_t add;
@@ -566,6 +567,7 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
             });
         };
         const bool add = KIND != GRAD && a.add;
+        const float scale = kDw ? *a.scale : 1.0f;
         Old old{};
         if (add) old = fetch(0, 0);
 #pragma unroll
@@ -574,10 +576,10 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
             for (int h0 = 0; h0 < FR; h0 += kParts) {
                 if constexpr (KIND == GRAD) {
                     // The part of g, rounded to BF16, which the matrix cores multiply; a
-                    // further term is what those before it leave.  One term's error is about that of
-                    // the gradient's own rounding to BF16 (drawn shapes, of the norm: dx
-                    // 0.00166 -> 0.0023 in the median, 0.0036 at most); the second costs
-                    // its products again
+                    // further term is what those before it leave.  One term's error is
+                    // below that of the gradient's own rounding to BF16 (drawn shapes, of
+                    // the norm: dx 0.00166 -> 0.0020 in the median, 0.0023 at most); a
+                    // second costs its products again
 #pragma unroll
                     for (int g = 0; g < 2; g++) {
                         const float4 of = tokens[wt + 32 * f + 16 * g + i];
@@ -613,7 +615,7 @@ __global__ __launch_bounds__(64 * WT * WR) void tiles(TileArgs a) {
                             S4 v;
 #pragma unroll
                             for (int e = 0; e < 4; e++) {
-                                v[e] = S(acc[2 * f + g][h][e]);
+                                v[e] = S(kDw ? acc[2 * f + g][h][e] * scale : acc[2 * f + g][h][e]);
                                 if constexpr (KIND == GRAD) acc[2 * f + g][h][e] -= float(v[e]);
                             }
                             *reinterpret_cast<S4 *>(out + (16 * g + i) * kPitch +
@@ -655,7 +657,7 @@ struct TokenArgs {
     uint32_t loss_grad_step, lse_grad_step;
     float loss_grad_all;
     uint32_t *count, *order, *place, *target_of;
-    float *lse_of;
+    float *scale, *lse_of;
     float2 *factor;
     const __bf16 *x;
     uint64_t x_stride, to_stride;
@@ -723,11 +725,27 @@ __global__ __launch_bounds__(1024) void loss_join(TokenArgs a) {
     a.losses[t] = target == a.ignored ? 0.0f : loss;
 }
 
+// The gradient of token t's loss.
+__device__ __forceinline__ float loss_grad_of(const TokenArgs &a, uint32_t t) {
+    return a.loss_grad ? a.loss_grad[t * uint64_t(a.loss_grad_step)] : a.loss_grad_all;
+}
+
+// What g is divided by, and dx and dw are multiplied with: 1 to 2, the digits of the
+// first counted token's gradient, usually those of all.  The target's entry of a token
+// that is not known is then next to a power of two, which BF16 holds, where one of
+// 1 / 120 loses 1 in 290, in every token alike and so in dx and dw (drawn shapes, error
+// of the norm in BF16: dx 0.0023 in the median and 0.0036 at most, 0.0020 and 0.0023 so;
+// dw 0.0021 and 0.0034, 0.0019 and 0.0022 so).
+__device__ __forceinline__ float digits(float x) {
+    const uint32_t bits = __float_as_uint(x), power = bits >> 23 & 0xFFu;
+    return power == 0 || power == 0xFF ? 1.0f : __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u);
+}
+
 // What a token's part of g needs, at its place among those that have a gradient.
-__device__ __forceinline__ void put_token(const TokenArgs &a, uint32_t t, uint32_t at, int64_t target) {
+__device__ __forceinline__ void put_token(const TokenArgs &a, uint32_t t, uint32_t at, int64_t target, float scale) {
     const bool inside = target >= 0 && target < a.vocab;
-    const float of_loss = a.loss_grad ? a.loss_grad[t * uint64_t(a.loss_grad_step)] : a.loss_grad_all;
-    const float of_lse = a.lse_grad ? a.lse_grad[t * uint64_t(a.lse_grad_step)] : 0.0f;
+    const float of_loss = loss_grad_of(a, t) / scale;
+    const float of_lse = a.lse_grad ? a.lse_grad[t * uint64_t(a.lse_grad_step)] / scale : 0.0f;
     const float nan = __builtin_nanf("");
     // at the target p (l - lse) - q = of_loss (exp(-loss) - 1) + of_lse exp(-loss)
     float q = of_loss;
@@ -740,27 +758,30 @@ __device__ __forceinline__ void put_token(const TokenArgs &a, uint32_t t, uint32
 
 // The tokens that have a gradient, in order.
 __global__ __launch_bounds__(1024) void pick(TokenArgs a) {
-    __shared__ uint32_t sums[16];
+    __shared__ uint32_t sums[16], firsts[16];
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     uint32_t before = 0;
+    float scale = 1.0f;
     for (uint32_t t0 = 0; t0 < a.n; t0 += 1024) {
         const uint32_t t = t0 + threadIdx.x;
         const int64_t target = t < a.n ? target_at(a, t) : a.ignored;
         const bool on = t < a.n && target != a.ignored;
         const uint64_t mask = __ballot(on);
-        if (lane == 0) sums[wave] = __popcll(mask);
+        if (lane == 0) sums[wave] = __popcll(mask), firsts[wave] = mask ? t + __builtin_ctzll(mask) : 0;
         __syncthreads();
-        uint32_t at = before + __popcll(mask & ((1ull << lane) - 1)), total = 0;
+        uint32_t at = before + __popcll(mask & ((1ull << lane) - 1)), total = 0, first = 0;
         for (uint32_t w = 0; w < 16; w++) {
             if (w < wave) at += sums[w];
+            if (total == 0) first = firsts[w];
             total += sums[w];
         }
+        if (before == 0 && total) scale = digits(loss_grad_of(a, first));
         before += total;
         __syncthreads();
         if (t < a.n) a.place[t] = on ? at : 0xFFFFFFFFu;
-        if (on) put_token(a, t, at, target);
+        if (on) put_token(a, t, at, target, scale);
     }
-    if (threadIdx.x == 0) *a.count = before;
+    if (threadIdx.x == 0) *a.count = before, *a.scale = scale;
 }
 
 // Their hidden states, one behind the other: a wave for each 512 columns.
@@ -784,21 +805,25 @@ __global__ __launch_bounds__(256) void pick_and_gather(TokenArgs a) {
     const int64_t target = target_at(a, t);
     bf16x8 x;
     if (c < a.cols) x = *reinterpret_cast<const bf16x8 *>(a.x + t * a.x_stride + c);
-    uint32_t at = 0;
+    uint32_t at = 0, first = t;
     for (uint32_t i0 = 0; i0 < t; i0 += 4 * 64) {
         int64_t other[4];
 #pragma unroll
         for (uint32_t u = 0; u < 4; u++) other[u] = target_at(a, min(i0 + 64 * u + lane, t));
 #pragma unroll
-        for (uint32_t u = 0; u < 4; u++)
-            at += __popcll(__ballot(i0 + 64 * u + lane < t && other[u] != a.ignored));
+        for (uint32_t u = 0; u < 4; u++) {
+            const uint64_t mask = __ballot(i0 + 64 * u + lane < t && other[u] != a.ignored);
+            if (at == 0 && mask) first = i0 + 64 * u + __builtin_ctzll(mask);
+            at += __popcll(mask);
+        }
     }
     const bool on = target != a.ignored;
     if (on && c < a.cols) *reinterpret_cast<bf16x8 *>(a.to + at * a.to_stride + c) = x;
     if (wave % parts || lane) return;
     a.place[t] = on ? at : 0xFFFFFFFFu;
-    if (on) put_token(a, t, at, target);
-    if (t == a.n - 1) *a.count = at + on;
+    const float scale = at + on ? digits(loss_grad_of(a, first)) : 1.0f;
+    if (on) put_token(a, t, at, target, scale);
+    if (t == a.n - 1) *a.count = at + on, *a.scale = scale;
 }
 
 // dx of every token: the splits' sums in order, zeros for those without a gradient.
@@ -823,7 +848,7 @@ __global__ __launch_bounds__(256) void spread(TokenArgs a) {
                 if (k + u < a.splits) sum += v[u];
         }
     }
-    store_group<Y>(static_cast<Y *>(a.dx) + t * a.dx_stride, c, a.cols, sum);
+    store_group<Y>(static_cast<Y *>(a.dx) + t * a.dx_stride, c, a.cols, sum * *a.scale);
 }
 
 // ---------------------------------------------------------------- host
@@ -962,7 +987,7 @@ uint32_t terms_for(uint64_t n, bool f32) { return f32 ? 3 : n <= kTwoTermTokens 
 struct GradScratch {
     uint32_t *count, *order, *place, *target_of;
     Split dx;
-    float *lse_of, *sums;
+    float *scale, *lse_of, *sums;
     float2 *factor;
     __bf16 *x, *g;
     uint64_t x_stride, chunk, bytes;
@@ -970,6 +995,7 @@ struct GradScratch {
         Scratch s{static_cast<char *>(p)};
         const uint64_t n = z.n;
         count = s.take<uint32_t>(1);
+        scale = s.take<float>(1);
         order = s.take<uint32_t>(n), place = s.take<uint32_t>(n), target_of = s.take<uint32_t>(n);
         lse_of = s.take<float>(n);
         factor = s.take<float2>(n);
@@ -1079,7 +1105,7 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
     t.loss_grad = g->loss_grad, t.lse_grad = g->lse_grad, t.loss_grad_all = g->loss_grad_all;
     t.loss_grad_step = g->loss_grads > 1, t.lse_grad_step = g->lse_grads > 1;
     t.count = s.count, t.order = s.order, t.place = s.place, t.target_of = s.target_of;
-    t.lse_of = s.lse_of, t.factor = s.factor;
+    t.scale = s.scale, t.lse_of = s.lse_of, t.factor = s.factor;
     t.x = static_cast<const __bf16 *>(p->x), t.x_stride = p->x_stride;
     t.to = s.x, t.to_stride = s.x_stride, t.cols = p->cols;
     int rc = DF11_OK;
@@ -1122,7 +1148,7 @@ int df11_vocab_loss_gradient(const df11_vocab_piece *p, const df11_vocab_grad *g
             a = tile_args();
             a.a = s.g, a.a_stride = g_stride, a.a_term = p->n * g_stride, a.terms = dw_terms;
             a.b = s.x, a.b_stride = s.x_stride;
-            a.count = s.count;
+            a.count = s.count, a.scale = s.scale;
             a.t_size = here, a.r_size = p->cols;
             a.y_stride = g->dw_stride, a.add = g->accumulate;
             const int tile = tile_for(here, p->cols, uint64_t(p->n) * dw_terms);

@@ -911,7 +911,9 @@ int df11_vocab_loss(const df11_vocab_piece *p, float *losses, float *lse,
  * g is rounded to BF16 for gradients in BF16, and for up to 64 tokens in one call held
  * as two BF16 terms (16 bits and more), which doubles the products: a token's
  * gradients depend, within that rounding, on how many tokens the call has.  For
- * gradients in float32 it is three terms (24 bits).  Sums are float32, rounded once.
+ * gradients in float32 it is three terms (24 bits).  The digits of the first counted
+ * token's a, a number of 1 to 2 and usually the same in all of them, are divided out of
+ * g before, and multiplied with the sums.  Sums are float32, rounded once to the type.
  * Ignored tokens have no gradient at all: their dx is zero, and nothing of their x
  * (which may be NaN) enters dw.  A target outside the head makes its token's dx and
  * all of dw NaN.  Pieces as above: begin, then dw of each piece is written by its own

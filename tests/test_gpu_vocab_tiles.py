@@ -115,6 +115,7 @@ def check_bits(n, rows, cols, dx, dw, add, left, right):
     targets = some_targets(n, rows, cols)
     fine = 2.0 ** -8 if rows < 60_000 else 0.0
     a = whole(1, 2, n, seed=5) * whole(0, 1, n, seed=6).mul(2).sub(1) * (1 + fine)
+    a[(targets != -100).nonzero()[0]] = 1  # the digits of the first are taken out of g
     c = whole(0, 1, n, seed=8) * (1 + fine)
     before = whole(-100, 100, rows, cols, seed=9).to(dw) if add else None
     room_x, out_x = held(n, cols, dx, 3, 10)
@@ -165,11 +166,12 @@ def test_float32_gradients_hold_what_float32_does(n, rows, cols, dx, dw):
     x[:, :8] = torch.nn.functional.one_hot(group.long(), 8)
     w[:, :8] = -256.0 * off
     targets = some_targets(n, rows, cols)
-    a = 1 + 2.0 ** -9 + 2.0 ** -20
+    a = torch.full((n,), 1 + 2.0 ** -9 + 2.0 ** -20, device="cuda")
+    a[(targets != -100).nonzero()[0]] = 1
     got_dx, (got_dw,) = ed.VocabLoss([w]).gradient(x, targets, torch.zeros(n, device="cuda"), a, dx_dtype=dx,
                                                   dw_dtype=dw)
     here = torch.arange(rows, device="cuda")
-    g = a * (off[:, group.long()].t() == 0) - a * (targets[:, None] == here).double()
+    g = a.double()[:, None] * ((off[:, group.long()].t() == 0).double() - (targets[:, None] == here).double())
     g[targets == -100] = 0
     # the 8 columns that say which logits are 0 have long sums
     x64, w64 = x[:, 8:].double(), w[:, 8:].double()
@@ -177,3 +179,31 @@ def test_float32_gradients_hold_what_float32_does(n, rows, cols, dx, dw):
     for got, want, kind in ((got_dx, g @ w64, dx), (got_dw, g.t() @ x64, dw)):
         if kind == F32:
             assert want.any() and torch.equal(got[:, 8:], want.float())
+
+
+@pytest.mark.parametrize("n,rows,cols", [(20, 300, 72), (120, 3000, 136), (1500, 2000, 520)])
+@pytest.mark.parametrize("kind", [F32, BF16])
+@pytest.mark.parametrize("given", ["number", "one", "each", "each but ignored"])
+def test_one_gradient_of_all_losses_costs_no_digits(n, rows, cols, kind, given):
+    """1 / 120, which BF16 holds to 1 in 290 only: g is whole but for it, and the
+    gradients are those of whole numbers times it, rounded once more."""
+    say(f"[gpu] gradients of {n} tokens, {rows} x {cols}, {kind}, of one 120th: {given}")
+    group, off = whole(0, 7, n, seed=1), whole(0, 1, rows, 8, seed=2)
+    x, w = whole(-2, 2, n, cols, seed=3).to(BF16), whole(-1, 1, rows, cols, seed=4).to(BF16)
+    x[:, 9::2], w[:, 8::2] = 0, 0
+    x[:, :8] = torch.nn.functional.one_hot(group.long(), 8)
+    w[:, :8] = -256.0 * off
+    targets = some_targets(n, rows, cols)
+    targets[0], targets[1] = -100, 3
+    a = torch.full((n,), 1 / 120, device="cuda")
+    if given == "each but ignored":
+        a[targets == -100] = float("nan")
+    a = {"number": 1 / 120, "one": a[:1]}.get(given, a)
+    dx, (dw,) = ed.VocabLoss([w]).gradient(x, targets, torch.zeros(n, device="cuda"), a, dx_dtype=kind, dw_dtype=kind)
+    g = (off[:, group.long()].t() == 0).double()
+    g -= (targets[:, None] == torch.arange(rows, device="cuda")).double()
+    g[targets == -100] = 0
+    one = torch.tensor(1 / 120, dtype=F32, device="cuda")
+    for got, whole_ones in ((dx, g @ w.double()), (dw, g.t() @ x.double())):
+        assert whole_ones.any() and whole_ones.abs().max() < 2 ** 24
+        assert torch.equal(got, (whole_ones.float() * one).to(kind))

@@ -83,6 +83,6 @@ def loss_bytes(n, rows, cols):
 def gradient_bytes(n, rows, cols, dx, two_terms):
     chunk = chunk_rows(n, rows)
     parts = dx_split(n, cols, chunk)[1]
-    total = 256 + 3 * up(4 * n, 256) + up(4 * n, 256) + up(8 * n, 256) + up(2 * n * up(cols, 64), 256)
+    total = 512 + 3 * up(4 * n, 256) + up(4 * n, 256) + up(8 * n, 256) + up(2 * n * up(cols, 64), 256)
     total += up(4 * parts * n * cols, 256) if dx else 0
     return total + up(2 * n * chunk * terms_for(n, two_terms), 256)
