@@ -4,11 +4,11 @@
 //   l[t][v] = x[t] . w[v]      lse[t] = log(sum_v exp l[t][v])      loss[t] = lse[t] - l[t][target t]
 //   g[t][v] = p_t exp(l[t][v] - lse[t]) - q_t [v = target t]        dx = s g w        dw = s g^T x
 //
-// where p_t and q_t come from the gradients of loss and lse, divided by s, their digits.  All four products
-// (the logits twice) run on one kernel of tiles on the matrix cores, with the
-// logits' two uses in its epilogues: a tile of logits leaves its rows' largest
-// value and sum of exponentials, or its part of g.  g exists in BF16 for a
-// piece of the vocabulary at a time.
+// where p_t and q_t come from the gradients of loss and lse, divided by s, their
+// digits.  All four products (the logits twice) run on one kernel of tiles on the
+// matrix cores, with the logits' two uses in its epilogues: a tile of logits leaves its
+// rows' largest value and sum of exponentials, or its part of g.  g exists in BF16 for
+// a piece of the vocabulary at a time.
 //
 //   stats tiles     logits of a tile; the target's, and the others' largest value and sum
 //   loss_join       joins tiles and pieces: lse and loss
@@ -16,8 +16,8 @@
 //                   tokens in one launch)
 //   grad tiles      logits again; g
 //   dx tiles        g w, added up over pieces in float32
-//   dw tiles        g^T x
-//   spread          dx of all tokens
+//   dw tiles        s g^T x
+//   spread          dx of all tokens, times s
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -834,6 +834,7 @@ __global__ __launch_bounds__(256) void spread(TokenArgs a) {
     const uint32_t t = wave / parts, c = wave % parts * 512 + lane * 8;
     if (t >= a.n || c >= a.cols) return;
     const uint32_t at = a.place[t];
+    const float scale = *a.scale;
     f32x8 sum = 0.0f;
     if (at != 0xFFFFFFFFu) {
         const float *from = a.sums + at * uint64_t(a.cols) + c;
@@ -842,13 +843,13 @@ __global__ __launch_bounds__(256) void spread(TokenArgs a) {
             f32x8 v[kLoads];
 #pragma unroll
             for (uint32_t u = 0; u < kLoads; u++)
-                v[u] = *reinterpret_cast<const f32x8 *>(from + min(k + u, a.splits - 1) * a.sums_split);
+                if (k + u < a.splits) v[u] = *reinterpret_cast<const f32x8 *>(from + (k + u) * a.sums_split);
 #pragma unroll
             for (uint32_t u = 0; u < kLoads; u++)
                 if (k + u < a.splits) sum += v[u];
         }
     }
-    store_group<Y>(static_cast<Y *>(a.dx) + t * a.dx_stride, c, a.cols, sum * *a.scale);
+    store_group<Y>(static_cast<Y *>(a.dx) + t * a.dx_stride, c, a.cols, sum * scale);
 }
 
 // ---------------------------------------------------------------- host
