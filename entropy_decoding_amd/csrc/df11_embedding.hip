@@ -115,8 +115,8 @@ constexpr uint32_t kSortWaves = 16;
 // keeps those of its rows.  The first reading counts them by wave and row, and
 // all tokens of earlier rows, which says where its rows begin; the second puts
 // each at its place.  A wave reads `span` consecutive tokens, in order, so
-// places within a row ascend with the position.  12 us for 8192 and 36 us for 32768
-// tokens of 128256 rows.
+// places within a row ascend with the position.  12 us for 8192 and 31 to 36 us
+// for 32768 tokens of 128256 rows.
 template <class I>
 __global__ __launch_bounds__(64 * kSortWaves) void sort_tokens(GradArgs a) {
     extern __shared__ uint32_t shared[];
