@@ -1647,9 +1647,12 @@ def embedding_gradient(tokens, dy, rows: int, dtype=None, out=None, accumulate: 
 
 @functools.cache
 def _undifferentiable():
-    """f(why, outputs, *leaves): the outputs as of a function of the leaves whose
-    derivative is the error ``why``."""
+    """f(why, outputs): the outputs as of a function whose derivative is the error
+    ``why``.  It is one of a leaf of its own: outputs that hold the nodes of a program's
+    leaves must not live while a backward pass of those is captured."""
     import torch
+
+    leaf = torch.zeros((), requires_grad=True)
 
     class Undifferentiable(torch.autograd.Function):
         @staticmethod
@@ -1661,7 +1664,7 @@ def _undifferentiable():
         def backward(ctx, *_):
             raise RuntimeError(ctx.why)
 
-    return Undifferentiable.apply
+    return lambda why, outputs: Undifferentiable.apply(why, outputs, leaf)
 
 
 class VocabLoss(_Lender):
@@ -1795,7 +1798,7 @@ class VocabLoss(_Lender):
             self._used(stream, st, used + [losses, lse] + ([] if status is None else [status]))
         if self.pieces is not None and torch.is_grad_enabled() and any(w.requires_grad for w in self.pieces):
             return _undifferentiable()("a loss records no gradient for its head: `gradient` makes it; detach the "
-                                       "losses, or call under torch.no_grad()", [losses, lse], *self.pieces)
+                                       "losses, or call under torch.no_grad()", [losses, lse])
         return losses, lse
 
     def _used(self, stream, st, tensors):

@@ -136,6 +136,12 @@ def test_losses_under_a_head_that_requires_a_gradient_are_not_differentiated(gpu
         with pytest.raises(RuntimeError, match="gradient"):
             (out.sum() + other.sum()).backward()
     assert pieces[1].grad is None
+    reached, todo = set(), [losses.grad_fn, lse.grad_fn]
+    while todo:  # the outputs do not hold the node of the head's own leaf
+        node = todo.pop()
+        reached.add(getattr(node, "variable", None))
+        todo += [f for f, _ in node.next_functions if f is not None]
+    assert pieces[1] not in reached
     head.gradient(x, targets, lse, losses=losses)
     with torch.no_grad():
         assert not any(t.requires_grad for t in head(x, targets))
